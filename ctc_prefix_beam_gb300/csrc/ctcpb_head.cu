@@ -1,0 +1,1301 @@
+// The label head's products: log-probabilities log_softmax(x w^T + b) for the
+// decoder, and softmax cross entropy over the same product with its gradients
+// (ctcpb_log_probs, ctcpb_cross_entropy, ctcpb_cross_entropy_backward).
+//
+// All three rest on one matrix kernel, k_gemm, with an epilogue for each use:
+//
+//   z = x w^T + b                        [rows, V], never stored as such
+//   kStats    per row and column tile (max z, sum exp(z - max)), z[target]
+//   kLogp     z - lse, float32           the decoder's log_prob
+//   kDlogits  d = (exp(z - lse) - [c = target]) r   16 bits, a piece of V
+//   kProduct  dx += d w  and  dw = d^T x
+//
+// The matrix kernel is persistent, one block (or pair of blocks) per SM: one
+// thread feeds 128-byte swizzled operand tiles by tiled bulk copies, one
+// issues tcgen05 matrix instructions into tensor memory, eight warps run the
+// epilogue of the previous tile meanwhile (two accumulators).
+#include <mutex>
+
+#include "ctcpb_head.cuh"
+
+namespace ctcpb {
+namespace {
+
+enum Mode { kStats = 0, kLogp = 1, kDlogits = 2, kProduct = 3 };
+
+constexpr int kThreads = 384;      // 4 control warps, 8 epilogue warps
+constexpr int kEpiWarps = 8;
+constexpr int kMaxStages = 8;
+constexpr int kTileBytes = 196608;  // operand stages
+constexpr int kStageBuf = 4096;     // per epilogue warp: 32 rows of 128 bytes
+constexpr int kSmem = kTileBytes + kEpiWarps * (kStageBuf + 64 * 4) + 256;
+constexpr u32 kTmemCols = 512;
+
+struct GemmArgs {
+  const int* rows_dev;  // number of rows, on the device (null: `rows`)
+  int rows;             // ... or its bound
+  int M, N, K;          // output rows and columns, depth; the row count replaces M (K in d^T x)
+  int bn;               // columns of a tile
+  int stages;
+  int group;            // row tiles that share a sweep over the columns
+  int split;            // share the last, partial wave of tiles along K
+  int col0;             // first vocabulary entry of the piece
+  // logits
+  const void* bias;
+  int bias_type;
+  const int* tgt;
+  const float* lse;
+  const float* rs;      // per-row factor of d
+  float* zt;
+  float2* part;
+  long long part_ld;
+  float* dbp;           // column sums of d per 32 rows [4 * row tiles][ldo]
+  // output
+  void* out;
+  long long ldo;
+  int vec;              // rows of `out` start on 16-byte boundaries
+  const float* scale;
+  const int* rowmap;
+  float* slots;         // partial tiles of the split wave
+  float* acc;           // running sum over the pieces (null: one piece)
+  int first, last;      // of the pieces
+  u32* status;
+  int reset_status;
+};
+
+// ---------------------------------------------------------------- tiles and their split
+
+// A worker (block or pair) takes whole tiles in waves; the last wave, if it
+// would leave workers idle, is cut along K into equal shares instead.  A share
+// is at most one tile's depth, so it touches at most two tiles; its sums go to
+// slots 2w, 2w+1, and k_join adds a tile's shares in order.
+struct Seg {
+  int m, n, tile, k0, k1, slot;  // slot -1: the whole depth
+};
+struct Sched {
+  int mt, nt, ks, group, tiles, dp, rem, nw, w, G, t, first;
+  int u, u1;
+  __device__ int share(int i) const { return (int)((long long)rem * ks * i / nw); }
+  __device__ void init(const GemmArgs& a, int cg, int worker, int workers) {
+    const int rows = a.rows_dev ? *a.rows_dev : a.rows;
+    const bool rows_k = a.M > 0;  // M given: the rows are the depth
+    const int M = rows_k ? a.M : rows, K = rows_k ? rows : a.K;
+    mt = (M + 128 * cg - 1) / (128 * cg);
+    if (mt < 1) mt = 1;
+    nt = (a.N + a.bn - 1) / a.bn;
+    ks = (K + 63) / 64;
+    if (ks < 1) ks = 1;
+    group = a.group < mt ? a.group : mt;
+    tiles = mt * nt;
+    G = workers;
+    w = worker;
+    dp = tiles;
+    rem = 0;
+    nw = 1;
+    if (a.split && ks >= 8) {
+      rem = tiles % G;
+      if (5 * rem > 4 * G) rem = 0;  // a nearly full wave: joining would cost more than it gives
+      dp = tiles - rem;
+      nw = rem * ks / 4;  // at least 4 slices of K a share
+      if (nw > G) nw = G;
+      if (nw < rem) nw = rem;
+      if (nw < 1) nw = 1;
+    }
+    t = w;
+    u = w < nw ? share(w) : 0;
+    u1 = w < nw ? share(w + 1) : 0;
+    first = ks > 0 ? u / ks : 0;
+  }
+  __device__ void place(int tile, Seg& s) const {
+    const int per = group * nt, g = tile / per, in = tile - g * per;
+    const int gs = mt - g * group < group ? mt - g * group : group;
+    s.tile = tile;
+    s.n = in / gs;
+    s.m = g * group + in - s.n * gs;
+  }
+  __device__ bool next(Seg& s) {
+    if (t < dp) {
+      place(t, s);
+      s.k0 = 0;
+      s.k1 = ks;
+      s.slot = -1;
+      t += G;
+      return true;
+    }
+    if (u < u1) {
+      const int r = u / ks;
+      place(dp + r, s);
+      s.k0 = u - r * ks;
+      s.k1 = s.k0 + (u1 - u) < ks ? s.k0 + (u1 - u) : ks;
+      s.slot = (s.k0 == 0 && s.k1 == ks) ? -1 : 2 * w + (r - first);
+      u += s.k1 - s.k0;
+      return true;
+    }
+    return false;
+  }
+};
+
+// ---------------------------------------------------------------- writing rows through shared memory
+//
+// A thread holds 32 columns of its own row.  The warp puts them into a 4 KB
+// buffer of 32 rows x 128 bytes, its 16-byte chunks permuted by row & 7 so
+// that neither side has bank conflicts, and then writes whole row pieces.
+
+__device__ __forceinline__ u32 stage_at(int row, int chunk) { return (u32)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
+
+__device__ __forceinline__ void stage_f32(char* buf, int lane, const float (&v)[32]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<float4*>(buf + stage_at(lane, c)) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+template <class T>
+__device__ __forceinline__ void stage_16(char* buf, int lane, const float (&v)[32], int half) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint4 p;
+    p.x = Elem<T>::pack(v[8 * c], v[8 * c + 1]);
+    p.y = Elem<T>::pack(v[8 * c + 2], v[8 * c + 3]);
+    p.z = Elem<T>::pack(v[8 * c + 4], v[8 * c + 5]);
+    p.w = Elem<T>::pack(v[8 * c + 6], v[8 * c + 7]);
+    *reinterpret_cast<uint4*>(buf + stage_at(lane, 4 * half + c)) = p;
+  }
+}
+// Write the buffer's rows (E: float for 32 columns, 16-bit for 64) to columns
+// [c0, cols) of output rows; orow is this lane's output row, -1 for none.
+template <class E>
+__device__ __forceinline__ void flush_rows(const char* buf, int lane, E* out, long long ldo, long long orow, int c0,
+                                           int cols, bool vec) {
+  constexpr int per = 16 / (int)sizeof(E);  // elements of a chunk
+  __syncwarp();
+  if (vec) {
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+      const int row = it * 4 + (lane >> 3), c = lane & 7;
+      const long long r = __shfl_sync(0xffffffffu, orow, row);
+      const uint4 p = *reinterpret_cast<const uint4*>(buf + stage_at(row, c));
+      const int col = c0 + c * per;
+      if (r >= 0 && col < cols) {
+        E* o = out + r * ldo + col;
+        if (col + per <= cols) {
+          *reinterpret_cast<uint4*>(o) = p;
+        } else {
+          const E* e = reinterpret_cast<const E*>(&p);
+#pragma unroll
+          for (int i = 0; i < per; ++i)
+            if (col + i < cols) o[i] = e[i];
+        }
+      }
+    }
+  } else {
+    for (int row = 0; row < 32; ++row) {
+      const long long r = __shfl_sync(0xffffffffu, orow, row);
+      if (r < 0) continue;
+#pragma unroll
+      for (int c = lane; c < 8 * per; c += 32) {
+        const E e = *reinterpret_cast<const E*>(buf + stage_at(row, c / per) + (c % per) * (int)sizeof(E));
+        if (c0 + c < cols) out[r * ldo + c0 + c] = e;
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// Sum of column l over the warp's rows, in lane l: at each halving a lane
+// hands over the half of the columns that its partner keeps (31 exchanges).
+__device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int i = 0; i < s; ++i) {
+      const float give = up ? v[i] : v[i + s], keep = up ? v[i + s] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, s);
+    }
+  }
+  return v[0];
+}
+
+// ---------------------------------------------------------------- the matrix kernel
+
+template <int MODE, class T, bool AMN, bool BMN, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const GemmArgs a) {
+  extern __shared__ __align__(1024) char smem[];
+  char* const ctl = smem + kTileBytes + kEpiWarps * (kStageBuf + 64 * 4);
+  const u32 s_tiles = saddr(smem);
+  const u32 s_full = saddr(ctl), s_empty = s_full + 8 * kMaxStages, s_tfull = s_empty + 8 * kMaxStages,
+            s_tempty = s_tfull + 16, s_tptr = s_tempty + 16;
+  volatile u32* const tmem_ptr = reinterpret_cast<volatile u32*>(ctl + 16 * kMaxStages + 32);
+  volatile u32* const dead = tmem_ptr + 1;
+
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const u32 rank = CG == 2 ? cluster_rank() : 0;
+  const int worker = (int)blockIdx.x / CG, workers = (int)gridDim.x / CG;
+  const int bnb = a.bn / CG;                              // columns of B this block loads
+  const u32 stage_bytes = 16384u + (u32)bnb * 128u;
+
+  if (threadIdx.x == 0) {
+    tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_b);
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init_n(s_full + 8 * i, 1);
+      mbar_init_n(s_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init_n(s_tfull + 8 * i, 1);
+      mbar_init_n(s_tempty + 8 * i, kEpiWarps * CG);
+    }
+    *dead = 0;
+    mbar_init_fence();
+    fence_proxy_async();
+    if (a.reset_status && blockIdx.x == 0) *a.status = 0;
+  }
+  if (warp == 2) tmem_alloc<CG>(s_tptr, kTmemCols);
+  tc_fence_before();
+  if (CG == 2)
+    cluster_sync();
+  else
+    __syncthreads();
+  tc_fence_after();
+  const u32 tmem = *tmem_ptr;
+
+  // bounded wait; false once any wait of the block has given up
+  auto wait = [&](u32 bar, u32 parity) -> bool {
+    if (*dead) return false;
+    for (long long i = 0; i < kWaitSpins; ++i)
+      if (mbar_test_cluster(bar, parity)) return true;
+    *dead = 1;
+    return false;
+  };
+
+  Sched sc;
+  sc.init(a, CG, worker, workers);
+  Seg sg;
+  bool ok = true;
+
+  if (warp == 0) {
+    if (lane == 0) {  // ---- operand tiles
+      int st = 0;
+      u32 ph = 1;
+      const u32 full0 = CG == 2 ? cluster_addr(s_full, 0) : s_full;
+      while (ok && sc.next(sg)) {
+        const int m0 = (sg.m * CG + (int)rank) * 128, n0 = sg.n * a.bn + (int)rank * bnb;
+        for (int k = sg.k0; k < sg.k1; ++k) {
+          if (!(ok = wait(s_empty + 8 * st, ph))) break;
+          const u32 at = s_tiles + (u32)st * stage_bytes, bt = at + 16384u, bar = full0 + 8 * st;
+          if (rank == 0) mbar_expect(s_full + 8 * st, stage_bytes * CG);
+          if constexpr (!AMN) {
+            tma_load<CG>(at, &map_a, k * 64, m0, bar);
+          } else {
+            tma_load<CG>(at, &map_a, m0, k * 64, bar);
+            tma_load<CG>(at + 8192u, &map_a, m0 + 64, k * 64, bar);
+          }
+          if constexpr (!BMN) {
+            tma_load<CG>(bt, &map_b, k * 64, a.col0 + n0, bar);
+          } else {
+            for (int j = 0; j < bnb; j += 64) tma_load<CG>(bt + (u32)j * 128u, &map_b, n0 + j, a.col0 + k * 64, bar);
+          }
+          if (++st == a.stages) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {  // ---- matrix instructions
+      int st = 0, as = 0;
+      u32 ph = 0, aph = 1;
+      const u32 idesc = mma_idesc(Elem<T>::kFormat, AMN, BMN, 128 * CG, a.bn);
+      constexpr u64 kStepA = AMN ? 2048 >> 4 : 32 >> 4, kStepB = BMN ? 2048 >> 4 : 32 >> 4;
+      while (ok && sc.next(sg)) {
+        if (!(ok = wait(s_tempty + 8 * as, aph))) break;
+        tc_fence_after();
+        const u32 d = tmem + 256u * as;
+        for (int k = sg.k0; k < sg.k1; ++k) {
+          if (!(ok = wait(s_full + 8 * st, ph))) break;
+          tc_fence_after();
+          const u32 at = s_tiles + (u32)st * stage_bytes;
+          const u64 da = smem_desc(at, AMN ? 8192 : 16), db = smem_desc(at + 16384u, BMN ? 8192 : 16);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma_f16<CG>(d, da + i * kStepA, db + i * kStepB, idesc, k > sg.k0 || i > 0);
+          mma_commit<CG>(s_empty + 8 * st);
+          if (++st == a.stages) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit<CG>(s_tfull + 8 * as);
+        if (++as == 2) {
+          as = 0;
+          aph ^= 1;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {  // ---- epilogue
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    char* const buf = smem + kTileBytes + (warp - 4) * kStageBuf;
+    float* const bias_s = reinterpret_cast<float*>(smem + kTileBytes + kEpiWarps * kStageBuf) + (warp - 4) * 64;
+    const u32 tempty0 = CG == 2 ? cluster_addr(s_tempty, 0) : s_tempty;
+    const int rows = a.rows_dev ? *a.rows_dev : a.rows;
+    const int mrows = a.M > 0 ? a.M : rows;
+    int as = 0;
+    u32 aph = 0;
+    while (ok && sc.next(sg)) {
+      const int mtile = sg.m * CG + (int)rank;
+      const int row = mtile * 128 + q * 32 + lane, n0 = sg.n * a.bn;
+      float bm = -INFINITY, bs = 0.f;  // running max and sum of the row
+      float lse = 0.f, rs = 0.f;
+      int tgt = -1;
+      long long orow = row < mrows ? row : -1;
+      float bq[4];  // the biases of this warp's columns, two per unit of 64
+      if constexpr (MODE != kProduct) {
+        // a column past the vocabulary gets -inf, so that its exponential is 0
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int col = n0 + half * 64 + (i >> 1) * 128 + (i & 1) * 32 + lane;
+          bq[i] = col < a.N ? (a.bias ? load_elem(a.bias, a.bias_type, (long long)a.col0 + col) : 0.f) : -INFINITY;
+        }
+        if (row < mrows) {
+          if (a.tgt) tgt = a.tgt[row] - a.col0 - n0;
+          if (MODE != kStats) lse = a.lse[row];
+          if (MODE == kDlogits) rs = a.rs[row];
+        }
+      } else if (a.rowmap && orow >= 0) {
+        orow = a.rowmap[row];
+      }
+      if (!(ok = __all_sync(0xffffffffu, wait(s_tfull + 8 * as, aph)))) break;
+      tc_fence_after();
+      const u32 d = tmem + 256u * as + ((u32)(q * 32) << 16);
+      for (int u = half * 64; u < a.bn && n0 + u < (MODE == kDlogits ? (int)a.ldo : a.N); u += 128) {
+        if constexpr (MODE != kProduct) {
+          __syncwarp();
+          bias_s[lane] = u < 128 ? bq[0] : bq[2];
+          bias_s[lane + 32] = u < 128 ? bq[1] : bq[3];
+          __syncwarp();
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int c0 = u + 32 * j;
+          if (c0 < a.bn) {
+            float v[32];
+            tmem_load32(v, d + c0);
+            if constexpr (MODE != kProduct) {
+              const float4* b4 = reinterpret_cast<const float4*>(bias_s + 32 * j);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 b = b4[i];
+                v[4 * i] += b.x;
+                v[4 * i + 1] += b.y;
+                v[4 * i + 2] += b.z;
+                v[4 * i + 3] += b.w;
+              }
+            }
+            if constexpr (MODE == kStats) {
+              float mx = v[0];
+#pragma unroll
+              for (int i = 1; i < 32; ++i) mx = fmaxf(mx, v[i]);
+              const float mn = fmaxf(bm, mx), mm = mn == -INFINITY ? 0.f : mn;
+              float s0 = bs * ex2((bm - mm) * kLog2e), s1 = 0.f, s2 = 0.f, s3 = 0.f;
+              const int tr = tgt - c0;
+              if (__any_sync(0xffffffffu, (u32)tr < 32u)) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (tr == i) a.zt[row] = v[i];
+              }
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                s0 += ex2((v[i] - mm) * kLog2e);
+                s1 += ex2((v[i + 1] - mm) * kLog2e);
+                s2 += ex2((v[i + 2] - mm) * kLog2e);
+                s3 += ex2((v[i + 3] - mm) * kLog2e);
+              }
+              bm = mn;
+              bs = (s0 + s1) + (s2 + s3);
+            } else if constexpr (MODE == kLogp) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] -= lse;
+              stage_f32(buf, lane, v);
+              flush_rows<float>(buf, lane, (float*)a.out, a.ldo, orow, n0 + c0, a.N, a.vec);
+            } else if constexpr (MODE == kDlogits) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = ex2((v[i] - lse) * kLog2e);
+              const int tr = tgt - c0;
+              if (__any_sync(0xffffffffu, (u32)tr < 32u)) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] -= tr == i ? 1.f : 0.f;
+              }
+              // rows past the last one are exact zeros (their z may hold anything)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = row < mrows ? v[i] * rs : 0.f;
+              stage_16<T>(buf, lane, v, j);
+              if (a.dbp) {
+                const float cs = column_sums(v, lane);
+                if (n0 + c0 + lane < a.ldo) a.dbp[((long long)mtile * 4 + q) * a.ldo + n0 + c0 + lane] = cs;
+              }
+            } else {
+              if (sg.slot >= 0) {  // a share of the depth: to its slot, a column's rows side by side
+                float* o = a.slots + ((long long)sg.slot * CG + rank) * 128 * a.bn + (long long)c0 * 128 + q * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i * 128] = v[i];
+              } else {
+                if (a.acc) {
+                  float* o = a.acc + ((long long)sg.tile * CG + rank) * 128 * a.bn + (long long)c0 * 128 + q * 32 + lane;
+                  if (!a.first) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] += o[i * 128];
+                  }
+                  if (!a.last) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i * 128] = v[i];
+                  }
+                }
+                if (a.last) {
+                  const float f = *a.scale;
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) v[i] *= f;
+                  stage_16<T>(buf, lane, v, j);
+                }
+              }
+            }
+          } else if constexpr (MODE == kDlogits) {  // a tile of 32 columns: zeros fill the unit
+            float v[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+            stage_16<T>(buf, lane, v, j);
+          }
+        }
+        if constexpr (MODE == kDlogits)
+          flush_rows<T>(buf, lane, (T*)a.out, a.ldo, (long long)row, n0 + u, (int)a.ldo, true);
+        if constexpr (MODE == kProduct) {
+          if (sg.slot < 0 && a.last) flush_rows<T>(buf, lane, (T*)a.out, a.ldo, orow, n0 + u, a.N, a.vec);
+        }
+      }
+      if constexpr (MODE == kStats)
+        if (row < mrows) a.part[((long long)sg.n * 2 + half) * a.part_ld + row] = make_float2(bm, bs);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * as);
+      if (++as == 2) {
+        as = 0;
+        aph ^= 1;
+      }
+    }
+  }
+  __syncthreads();
+  if (*dead) {
+    // a wait gave up: let the copies and matrix instructions in flight land
+    // before the memory goes to another block
+    for (int i = 0; i < 2000; ++i) __nanosleep(1000);
+    if (threadIdx.x == 0) atomicOr(a.status, CTCPB_DEV_TIMEOUT);
+  }
+  tc_fence_before();
+  if (CG == 2)
+    cluster_sync();
+  else
+    __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc<CG>(tmem, kTmemCols);
+}
+
+// The shares of every tile of the split wave, added in the order of K, and the
+// tile's output written: a warp per 32 rows and 64 columns.
+template <class T, int CG>
+__global__ void __launch_bounds__(256) k_join(const GemmArgs a, int workers) {
+  __shared__ __align__(16) char smem[8 * kStageBuf];
+  Sched sc;
+  sc.init(a, CG, 0, workers);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.x;
+  const int units = CG * 4 * ((a.bn + 63) / 64);
+  const int unit = blockIdx.y * 8 + warp;
+  if (r >= sc.rem || unit >= units) return;
+  const int lo = r * sc.ks, hi = lo + sc.ks;
+  int w = (int)((long long)lo * sc.nw / ((long long)sc.rem * sc.ks));
+  while (w > 0 && sc.share(w) > lo) --w;
+  while (sc.share(w + 1) <= lo) ++w;
+  if (sc.share(w) <= lo && sc.share(w + 1) >= hi) return;  // one share: written by the matrix kernel
+  Seg sg;
+  sc.place(sc.dp + r, sg);
+  const int q = unit & 3, rank = (unit >> 2) % CG, u = (unit >> 2) / CG * 64;
+  const int n0 = sg.n * a.bn;
+  if (n0 + u >= a.N) return;
+  const int rows = a.rows_dev ? *a.rows_dev : a.rows;
+  const int mrows = a.M > 0 ? a.M : rows;
+  const int row = (sg.m * CG + rank) * 128 + q * 32 + lane;
+  long long orow = row < mrows ? (a.rowmap ? a.rowmap[row] : row) : -1;
+  char* const buf = smem + warp * kStageBuf;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int c0 = u + 32 * j;
+    if (c0 < a.bn) {
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = 0.f;
+      for (int x = w; x < sc.nw && sc.share(x) < hi; ++x) {
+        const int slot = 2 * x + (r - sc.share(x) / sc.ks);
+        const float* o = a.slots + ((long long)slot * CG + rank) * 128 * a.bn + (long long)c0 * 128 + q * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += o[i * 128];
+      }
+      if (a.acc) {
+        float* o = a.acc + ((long long)sg.tile * CG + rank) * 128 * a.bn + (long long)c0 * 128 + q * 32 + lane;
+        if (!a.first) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] += o[i * 128];
+        }
+        if (!a.last) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i * 128] = v[i];
+        }
+      }
+      if (a.last) {
+        const float f = *a.scale;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= f;
+        stage_16<T>(buf, lane, v, j);
+      }
+    }
+  }
+  if (a.last) flush_rows<T>(buf, lane, (T*)a.out, a.ldo, orow, n0 + u, a.N, a.vec);
+}
+
+// ---------------------------------------------------------------- rows
+
+// Rows of 16-bit elements to rows of ldo elements, zero from H on.
+__global__ void __launch_bounds__(256) k_copy_rows(const u16* __restrict__ in, long long ldi, u16* __restrict__ out,
+                                                   int ldo, long long n, int H) {
+  const int lane = threadIdx.x & 31;
+  for (long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); r < n; r += (long long)gridDim.x * 8)
+    for (int c = lane; c < ldo; c += 32) out[r * ldo + c] = c < H ? in[r * ldi + c] : (u16)0;
+}
+
+struct RowArgs {
+  const int* targets;
+  int N, V, H, ignore;
+  const u16* x;
+  long long ldx;
+  int vec;             // x's rows are whole 16-byte pieces on 16-byte boundaries
+  u16* xg;
+  int ldg;
+  int* rowmap;
+  int* tgt;
+  int* nv;             // out: number of rows kept
+  u32* status;
+  u32* ticket;
+  // forward
+  float* loss;         // per-row losses (reduction none) or null
+  float* lse;
+  // backward
+  int type, reduction;
+  const float* grad;
+  const float* lse_in;
+  float* lse_c;
+  float* rs;
+  float* scale;
+  u16* dx;
+  long long lddx;
+};
+
+constexpr int kRowBlock = 128;  // rows of a block of k_rows
+
+__device__ __forceinline__ int block_sum(int v, int* red) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  int s = 0;
+  for (int i = 0; i < (int)blockDim.x / 32; ++i) s += red[i];
+  __syncthreads();
+  return s;
+}
+
+// Keep the rows that have a target, in order, side by side: an ignored row
+// costs no product, and whatever it holds (padding may be NaN) never meets a
+// sum.  Each block counts the kept rows before its own by reading the targets,
+// so one launch does it.  The rows up to the next multiple of 256 are zeros.
+__global__ void __launch_bounds__(256) k_rows(const RowArgs a) {
+  __shared__ int red[8];
+  __shared__ float fred[8];
+  __shared__ int src[kRowBlock];
+  const int base = blockIdx.x * kRowBlock, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool last = blockIdx.x == gridDim.x - 1;
+  int before = 0, bad = 0;
+  for (int i = threadIdx.x; i < base; i += 256) {
+    const int t = a.targets[i];
+    const bool in = t >= 0 && t < a.V && t != a.ignore;
+    before += in;
+    bad |= !in && t != a.ignore;
+  }
+  before = block_sum(before, red);
+  // this block's rows
+  int t = a.ignore;
+  bool in = false;
+  const int row = base + (int)threadIdx.x;
+  if (threadIdx.x < kRowBlock && row < a.N) {
+    t = a.targets[row];
+    in = t >= 0 && t < a.V && t != a.ignore;
+    bad |= !in && t != a.ignore;
+  }
+  const u32 m = __ballot_sync(0xffffffffu, in);
+  if (lane == 0) red[warp] = __popc(m);
+  __syncthreads();
+  int off = 0, kept = 0;
+  for (int i = 0; i < kRowBlock / 32; ++i) {
+    if (i < warp) off += red[i];
+    kept += red[i];
+  }
+  const int mine = off + __popc(m & ((1u << lane) - 1));
+  // the largest |grad| (float16 only): d is scaled by it to stay in range
+  float gmax = 1.f;
+  if (a.grad && a.reduction == CTCPB_REDUCE_NONE && a.type == CTCPB_F16) {
+    float g = 0.f;
+    for (int i = threadIdx.x; i < a.N; i += 256) g = fmaxf(g, fabsf(a.grad[i]));
+    for (int s = 16; s > 0; s >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, s));
+    if (lane == 0) fred[warp] = g;
+    __syncthreads();
+    for (int i = 0; i < 8; ++i) g = fmaxf(g, fred[i]);
+    gmax = g > 0.f ? g : 1.f;
+  }
+  const float up = a.type == CTCPB_F16 ? 32768.f : 1.f;  // float16: |d| <= 1 is stored as |d| 2^15
+  if (in) {
+    const int to = before + mine;
+    src[mine] = row;
+    a.rowmap[to] = row;
+    a.tgt[to] = t;
+    if (a.grad) {
+      a.lse_c[to] = a.lse_in[row];
+      a.rs[to] = a.reduction == CTCPB_REDUCE_NONE ? a.grad[row] / gmax * up : up;
+    }
+  } else if (threadIdx.x < kRowBlock && row < a.N) {
+    if (a.loss) a.loss[row] = 0.f;
+    if (a.lse) a.lse[row] = 0.f;
+  }
+  __syncthreads();
+  // the kept rows, a warp each
+  for (int i = warp; i < kept; i += 8) {
+    const u16* s = a.x + (long long)src[i] * a.ldx;
+    u16* d = a.xg + (long long)(before + i) * a.ldg;
+    if (a.vec) {
+      for (int c = lane; c < a.H / 8; c += 32) reinterpret_cast<uint4*>(d)[c] = reinterpret_cast<const uint4*>(s)[c];
+    } else {
+      for (int c = lane; c < a.ldg; c += 32) d[c] = c < a.H ? s[c] : (u16)0;
+    }
+  }
+  // ignored rows have no gradient
+  if (a.dx) {
+    for (int i = warp; i < kRowBlock && base + i < a.N; i += 8) {
+      const int tt = a.targets[base + i];
+      if (tt >= 0 && tt < a.V && tt != a.ignore) continue;
+      u16* d = a.dx + (long long)(base + i) * a.lddx;
+      for (int c = lane; c < a.H; c += 32) d[c] = 0;
+    }
+  }
+  if (last) {
+    const int nv = before + kept;
+    const int end = nv > 0 ? (nv + 255) / 256 * 256 : 256;
+    for (long long i = threadIdx.x; i < (long long)(end - nv) * a.ldg; i += 256) a.xg[(long long)nv * a.ldg + i] = 0;
+    bad = block_sum(bad, red);
+    if (threadIdx.x == 0) {
+      *a.nv = nv;
+      *a.status = bad ? CTCPB_DEV_TARGET : 0u;
+      *a.ticket = 0;
+      if (a.grad)
+        *a.scale = (a.reduction == CTCPB_REDUCE_NONE ? gmax : a.grad[0] / (a.reduction == CTCPB_REDUCE_MEAN ? (float)(nv > 0 ? nv : 1) : 1.f)) / up;
+    }
+  }
+}
+
+struct CombineArgs {
+  const int* rows_dev;
+  int rows;
+  const float2* part;
+  long long part_ld;
+  int slots;
+  float* lse;            // [row]
+  const int* rowmap;     // null: the rows themselves, no loss
+  const float* zt;
+  float* loss;
+  int reduction;
+  float* sums;           // per block
+  u32* ticket;
+};
+
+// lse = m + log(sum_j s_j exp(m_j - m)) over a row's tiles, and the losses:
+// a block per 32 rows, 8 slices of the tiles.
+__global__ void __launch_bounds__(256) k_combine(const CombineArgs a) {
+  __shared__ float2 red[8][32];
+  __shared__ bool fin;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = a.rows_dev ? *a.rows_dev : a.rows;
+  const int i = blockIdx.x * 32 + lane;
+  float m = -INFINITY, s = 0.f;
+  if (i < rows) {
+    for (int j = warp; j < a.slots; j += 8) {
+      const float2 p = a.part[(long long)j * a.part_ld + i];
+      const float mn = fmaxf(m, p.x), mm = mn == -INFINITY ? 0.f : mn;
+      s = s * ex2((m - mm) * kLog2e) + p.y * ex2((p.x - mm) * kLog2e);
+      m = mn;
+    }
+  }
+  red[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  float loss = 0.f;
+  if (warp == 0 && i < rows) {
+    for (int w = 1; w < 8; ++w) m = fmaxf(m, red[w][lane].x);
+    const float mm = m == -INFINITY ? 0.f : m;
+    s = 0.f;
+    for (int w = 0; w < 8; ++w) s += red[w][lane].y * ex2((red[w][lane].x - mm) * kLog2e);
+    const float lse = mm + logf(s);
+    const int row = a.rowmap ? a.rowmap[i] : i;
+    a.lse[row] = lse;
+    if (a.rowmap) {
+      loss = lse - a.zt[i];
+      if (a.reduction == CTCPB_REDUCE_NONE) a.loss[row] = loss;
+    }
+  }
+  if (!a.rowmap || a.reduction == CTCPB_REDUCE_NONE) return;
+  // the sum of the losses: each block's in a fixed order, then the blocks' by the last one
+  if (warp == 0) {
+    for (int k = 16; k > 0; k >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, k);
+    if (lane == 0) {
+      a.sums[blockIdx.x] = loss;
+      __threadfence();
+      fin = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!fin) return;
+  __threadfence();
+  __shared__ double dred[256];
+  double d = 0.0;
+  for (int k = threadIdx.x; k < (int)gridDim.x; k += 256) d += (double)((volatile float*)a.sums)[k];
+  dred[threadIdx.x] = d;
+  __syncthreads();
+  for (int k = 128; k > 0; k >>= 1) {
+    if ((int)threadIdx.x < k) dred[threadIdx.x] += dred[threadIdx.x + k];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    *a.loss = (float)(a.reduction == CTCPB_REDUCE_MEAN ? dred[0] / (double)rows : dred[0]);
+    *a.ticket = 0;
+  }
+}
+
+// db of a piece: the column sums of d over the row tiles, in order.
+__global__ void __launch_bounds__(256) k_bias_grad(const float* __restrict__ dbp, long long ld, const int* rows_dev,
+                                                   int per, const float* __restrict__ scale, void* db, int type, int col0,
+                                                   int cols) {
+  __shared__ float red[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  int n = (*rows_dev + 128 * per - 1) / (128 * per);
+  n = (n < 1 ? 1 : n) * 4 * per;
+  float s = 0.f;
+  if (c < cols)
+    for (int j = warp; j < n; j += 8) s += dbp[(long long)j * ld + c];
+  red[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < cols) {
+    for (int w = 1; w < 8; ++w) s += red[w][lane];
+    store_elem(db, type, (long long)col0 + c, s * *scale);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return (EncodeFn)p;
+  }();
+  return fn;
+}
+
+// A [outer, inner] matrix of 16-bit elements, in boxes of 64 x box_outer.
+bool make_map(CUtensorMap* m, int type, const void* base, long long inner, long long outer, long long ld, int box_outer) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_outer}, es[2] = {1, 1};
+  return fn(m, type == CTCPB_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+            const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, class T, bool AMN, bool BMN, int CG>
+cudaError_t launch_gemm_t(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& a, int blocks, cudaStream_t s) {
+  constexpr auto kern = k_gemm<MODE, T, AMN, BMN, CG>;
+  cudaError_t e = smem_optin<kern>(kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = CG;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CG > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, ma, mb, a);
+}
+
+template <int MODE, bool AMN, bool BMN>
+cudaError_t launch_gemm(int type, int cg, const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& a, int blocks,
+                        cudaStream_t s) {
+  if (cg == 2)
+    return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, AMN, BMN, 2>(ma, mb, a, blocks, s)
+                              : launch_gemm_t<MODE, __half, AMN, BMN, 2>(ma, mb, a, blocks, s);
+  return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, AMN, BMN, 1>(ma, mb, a, blocks, s)
+                            : launch_gemm_t<MODE, __half, AMN, BMN, 1>(ma, mb, a, blocks, s);
+}
+
+constexpr int kWorkers = 152;  // SMs; the split wave's slots are sized by it
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return kWorkers;
+  return n < kWorkers ? n : kWorkers;
+}
+
+long long up_to(long long x, long long a) { return (x + a - 1) / a * a; }
+
+// Columns of a tile of the logits: as wide as leaves no SM idle.
+int logits_bn(long long rows, int V) {
+  const long long mt = (rows + 127) / 128;
+  for (int bn = 256; bn > 64; bn >>= 1)
+    if (V > bn / 2 && mt * ((V + bn - 1) / bn) >= kWorkers) return bn;
+  return V > 32 ? 64 : 32;
+}
+int product_bn(int N) { return N > 128 ? 256 : N > 64 ? 128 : 64; }
+int stages_of(int bn, int cg) {
+  const int n = kTileBytes / (16384 + bn / cg * 128);
+  return n < kMaxStages ? n : kMaxStages;
+}
+// Row tiles whose operand rows fit in half of L2 sweep the columns together.
+int group_of(int K, int cg) {
+  const long long g = (48ll << 20) / ((long long)128 * cg * K * 2);
+  return g < 1 ? 1 : g > (1 << 20) ? 1 << 20 : (int)g;
+}
+
+bool rows_aligned(const void* p, long long ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
+
+cudaError_t copy_rows(const void* in, long long ldi, void* out, int ldo, long long n, int H, cudaStream_t s) {
+  const long long b = (n + 7) / 8;
+  k_copy_rows<<<(unsigned)(b < 4864 ? b : 4864), 256, 0, s>>>((const u16*)in, ldi, (u16*)out, ldo, n, H);
+  return cudaGetLastError();
+}
+
+int check_types(int type, int param_type) {
+  if (type != CTCPB_BF16 && type != CTCPB_F16) return CTCPB_EINVAL;
+  if (param_type != type && param_type != CTCPB_F32) return CTCPB_EINVAL;
+  return CTCPB_OK;
+}
+int check_dims(long long N, int V, int H) {
+  if (N < 0 || N > kHeadMaxRows || V < 1 || V > kMaxV || H < 1 || H > kHeadMaxWidth) return CTCPB_EINVAL;
+  return CTCPB_OK;
+}
+int check_ws(const void* p, size_t have, size_t need) {
+  if (!p) return CTCPB_ENULL;
+  if (((uintptr_t)p & 255u) != 0) return CTCPB_EALIGN;
+  if (have < need) return CTCPB_ESIZE;
+  return CTCPB_OK;
+}
+
+#define TRY(x)                                 \
+  do {                                         \
+    if ((x) != cudaSuccess) return CTCPB_ECUDA; \
+  } while (0)
+
+struct Taker {
+  size_t off = sizeof(Header);
+  size_t take(size_t bytes) {
+    const size_t at = align_up(off, 1024);
+    off = at + bytes;
+    return at;
+  }
+};
+
+struct LogpLayout {
+  int bn, nt, Hp;
+  long long Np;
+  size_t o_part, o_lse, o_x, o_w, total;
+};
+LogpLayout logp_layout(long long N, int V, int H) {
+  LogpLayout l{};
+  l.bn = logits_bn(N, V);
+  l.nt = (V + l.bn - 1) / l.bn;
+  l.Hp = (int)up_to(H, 8);
+  l.Np = up_to(N > 0 ? N : 1, 256);
+  Taker t;
+  l.o_part = t.take((size_t)l.nt * 2 * l.Np * 8);
+  l.o_lse = t.take((size_t)l.Np * 4);
+  l.o_x = t.take((size_t)N * l.Hp * 2);  // rows that no tiled copy can read are laid out here
+  l.o_w = t.take((size_t)V * l.Hp * 2);
+  l.total = align_up(t.off, 256);
+  return l;
+}
+
+struct CeLayout {
+  int bn, nt, Hp, pieces, piece, pbn;
+  long long Np;
+  size_t o_ctl, o_map, o_tgt, o_xg, o_w;
+  size_t o_part, o_zt, o_sums;
+  size_t o_lse, o_rs, o_d, o_dbp, o_slots, o_acc, total;
+};
+CeLayout ce_layout(long long N, int V, int H, bool backward) {
+  CeLayout l{};
+  l.Hp = (int)up_to(H, 8);
+  l.Np = up_to(N > 0 ? N : 1, 256);
+  Taker t;
+  l.o_ctl = t.take(256);
+  l.o_map = t.take((size_t)l.Np * 4);
+  l.o_tgt = t.take((size_t)l.Np * 4);
+  l.o_xg = t.take((size_t)l.Np * l.Hp * 2);
+  l.o_w = t.take((size_t)V * l.Hp * 2);
+  l.bn = logits_bn(N, V);
+  if (!backward) {
+    l.nt = (V + l.bn - 1) / l.bn;
+    l.o_part = t.take((size_t)l.nt * 2 * l.Np * 8);
+    l.o_zt = t.take((size_t)l.Np * 4);
+    l.o_sums = t.take((size_t)(l.Np / 32) * 4);
+  } else {
+    // pieces of the vocabulary whose d takes at most 256 MB, of equal width
+    const long long most = (256ll << 20) / (l.Np * 2) / 256 * 256;
+    const long long Vp = up_to(V, 256);
+    l.pieces = (int)((Vp + (most > 256 ? most : 256) - 1) / (most > 256 ? most : 256));
+    l.piece = (int)up_to((V + l.pieces - 1) / l.pieces, 256);
+    if (l.pieces == 1) l.piece = (int)up_to(V, 64);
+    l.pieces = (V + l.piece - 1) / l.piece;
+    l.pbn = product_bn(H);
+    const long long mt = l.Np / 128, nt = (H + l.pbn - 1) / l.pbn;
+    l.o_lse = t.take((size_t)l.Np * 4);
+    l.o_rs = t.take((size_t)l.Np * 4);
+    l.o_d = t.take((size_t)l.Np * l.piece * 2);
+    l.o_dbp = t.take((size_t)mt * 4 * l.piece * 4);
+    l.o_slots = t.take((size_t)2 * kWorkers * 128 * l.pbn * 4);
+    l.o_acc = t.take(l.pieces > 1 ? (size_t)mt * nt * 128 * l.pbn * 4 : 0);
+  }
+  l.total = align_up(t.off, 256);
+  return l;
+}
+
+template <class T, int CG>
+cudaError_t launch_join_t(const GemmArgs& a, long long max_tiles, int workers, cudaStream_t s) {
+  const int units = CG * 4 * ((a.bn + 63) / 64);
+  const long long r = max_tiles < workers - 1 ? max_tiles : workers - 1;
+  if (r < 1) return cudaSuccess;
+  k_join<T, CG><<<dim3((unsigned)r, (units + 7) / 8), 256, 0, s>>>(a, workers);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace ctcpb
+
+using namespace ctcpb;
+
+extern "C" {
+
+int ctcpb_log_probs_workspace_size(int type, int64_t N, int V, int H, size_t* bytes) {
+  int rc = check_types(type, type);
+  if (rc || (rc = check_dims(N, V, H))) return rc;
+  if (!bytes) return CTCPB_ENULL;
+  *bytes = logp_layout(N, V, H).total;
+  return CTCPB_OK;
+}
+
+int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const void* weight, int64_t ldw,
+                    const void* bias, int64_t N, int V, int H, float* out, int64_t ldo, void* ws, size_t ws_bytes,
+                    ctcpb_stream_t stream) {
+  int rc = check_types(type, bias ? bias_type : type);
+  if (rc || (rc = check_dims(N, V, H))) return rc;
+  if (N == 0) return CTCPB_OK;
+  if (ldx < H || ldw < H || ldo < V) return CTCPB_EINVAL;
+  if (!x || !weight || !out) return CTCPB_ENULL;
+  const LogpLayout l = logp_layout(N, V, H);
+  if ((rc = check_ws(ws, ws_bytes, l.total))) return rc;
+  cudaStream_t s = (cudaStream_t)stream;
+  char* b = (char*)ws;
+  if (!rows_aligned(x, ldx)) {
+    TRY(copy_rows(x, ldx, b + l.o_x, l.Hp, N, H, s));
+    x = b + l.o_x;
+    ldx = l.Hp;
+  }
+  if (!rows_aligned(weight, ldw)) {
+    TRY(copy_rows(weight, ldw, b + l.o_w, l.Hp, V, H, s));
+    weight = b + l.o_w;
+    ldw = l.Hp;
+  }
+  const int cg = 1;
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, type, x, H, N, ldx, 128) || !make_map(&mb, type, weight, H, V, ldw, l.bn / cg)) return CTCPB_ECUDA;
+  GemmArgs a{};
+  a.rows = (int)N;
+  a.N = V;
+  a.K = H;
+  a.bn = l.bn;
+  a.stages = stages_of(l.bn, cg);
+  a.group = group_of(H, cg);
+  a.bias = bias;
+  a.bias_type = bias_type;
+  a.part = (float2*)(b + l.o_part);
+  a.part_ld = l.Np;
+  a.lse = (float*)(b + l.o_lse);
+  a.out = out;
+  a.ldo = ldo;
+  a.vec = ((uintptr_t)out & 15) == 0 && ldo % 4 == 0;
+  a.status = &((Header*)ws)->status;
+  a.reset_status = 1;
+  const long long tiles = (N + 127) / 128 * l.nt;
+  const int sms = sm_count(), blocks = (int)(tiles < sms ? tiles : sms);
+  TRY((launch_gemm<kStats, false, false>(type, cg, ma, mb, a, blocks, s)));
+  a.reset_status = 0;
+  CombineArgs c{};
+  c.rows = (int)N;
+  c.part = a.part;
+  c.part_ld = l.Np;
+  c.slots = 2 * l.nt;
+  c.lse = (float*)(b + l.o_lse);
+  k_combine<<<(unsigned)((N + 31) / 32), 256, 0, s>>>(c);
+  TRY(cudaGetLastError());
+  TRY((launch_gemm<kLogp, false, false>(type, cg, ma, mb, a, blocks, s)));
+  return CTCPB_OK;
+}
+
+int ctcpb_cross_entropy_workspace_size(int type, int64_t N, int V, int H, int backward, size_t* bytes) {
+  int rc = check_types(type, type);
+  if (rc || (rc = check_dims(N, V, H))) return rc;
+  if (backward != 0 && backward != 1) return CTCPB_EINVAL;
+  if (!bytes) return CTCPB_ENULL;
+  *bytes = ce_layout(N, V, H, backward != 0).total;
+  return CTCPB_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// The checks and the row kernel that both directions share.
+int ce_rows(int type, const void* x, int64_t ldx, const int32_t* targets, int64_t N, int V, int H, int32_t ignore_index,
+            int reduction, const CeLayout& l, char* b, RowArgs& r, cudaStream_t s) {
+  r.targets = targets;
+  r.N = (int)N;
+  r.V = V;
+  r.H = H;
+  r.ignore = ignore_index;
+  r.x = (const u16*)x;
+  r.ldx = ldx;
+  r.vec = rows_aligned(x, ldx) && H % 8 == 0;
+  r.xg = (u16*)(b + l.o_xg);
+  r.ldg = l.Hp;
+  r.rowmap = (int*)(b + l.o_map);
+  r.tgt = (int*)(b + l.o_tgt);
+  r.nv = (int*)(b + l.o_ctl);
+  r.scale = (float*)(b + l.o_ctl + 4);
+  r.ticket = (u32*)(b + l.o_ctl + 8);
+  r.status = &((Header*)b)->status;
+  r.type = type;
+  r.reduction = reduction;
+  const long long blocks = N > 0 ? (N + kRowBlock - 1) / kRowBlock : 1;
+  k_rows<<<(unsigned)blocks, 256, 0, s>>>(r);
+  TRY(cudaGetLastError());
+  return CTCPB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, const void* weight, int64_t ldw,
+                        const void* bias, const int32_t* targets, int64_t N, int V, int H, int32_t ignore_index,
+                        int reduction, float* loss, float* lse, void* ws, size_t ws_bytes, ctcpb_stream_t stream) {
+  int rc = check_types(type, bias ? bias_type : type);
+  if (rc || (rc = check_dims(N, V, H))) return rc;
+  if (reduction < CTCPB_REDUCE_NONE || reduction > CTCPB_REDUCE_SUM) return CTCPB_EINVAL;
+  if (N == 0 && reduction == CTCPB_REDUCE_NONE) return CTCPB_OK;
+  if (N > 0 && (ldx < H || ldw < H)) return CTCPB_EINVAL;
+  if (!weight || !loss || (N > 0 && (!x || !targets || !lse))) return CTCPB_ENULL;
+  const CeLayout l = ce_layout(N, V, H, false);
+  if ((rc = check_ws(ws, ws_bytes, l.total))) return rc;
+  cudaStream_t s = (cudaStream_t)stream;
+  char* b = (char*)ws;
+  RowArgs r{};
+  if (reduction == CTCPB_REDUCE_NONE) r.loss = loss;
+  r.lse = lse;
+  if ((rc = ce_rows(type, x, ldx, targets, N, V, H, ignore_index, reduction, l, b, r, s))) return rc;
+  if (!rows_aligned(weight, ldw)) {
+    TRY(copy_rows(weight, ldw, b + l.o_w, l.Hp, V, H, s));
+    weight = b + l.o_w;
+    ldw = l.Hp;
+  }
+  const int cg = 1;
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, type, r.xg, l.Hp, l.Np, l.Hp, 128) || !make_map(&mb, type, weight, H, V, ldw, l.bn / cg))
+    return CTCPB_ECUDA;
+  GemmArgs a{};
+  a.rows_dev = r.nv;
+  a.rows = (int)N;
+  a.N = V;
+  a.K = H;
+  a.bn = l.bn;
+  a.stages = stages_of(l.bn, cg);
+  a.group = group_of(H, cg);
+  a.bias = bias;
+  a.bias_type = bias_type;
+  a.tgt = r.tgt;
+  a.zt = (float*)(b + l.o_zt);
+  a.part = (float2*)(b + l.o_part);
+  a.part_ld = l.Np;
+  a.status = r.status;
+  const long long tiles = l.Np / 128 * l.nt;
+  const int sms = sm_count();
+  TRY((launch_gemm<kStats, false, false>(type, cg, ma, mb, a, (int)(tiles < sms ? tiles : sms), s)));
+  CombineArgs c{};
+  c.rows_dev = r.nv;
+  c.part = a.part;
+  c.part_ld = l.Np;
+  c.slots = 2 * l.nt;
+  c.lse = lse;
+  c.rowmap = r.rowmap;
+  c.zt = a.zt;
+  c.loss = loss;
+  c.reduction = reduction;
+  c.sums = (float*)(b + l.o_sums);
+  c.ticket = r.ticket;
+  k_combine<<<(unsigned)(l.Np / 32), 256, 0, s>>>(c);
+  TRY(cudaGetLastError());
+  return CTCPB_OK;
+}
+
+int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, const void* x, int64_t ldx,
+                                 const void* weight, int64_t ldw, const void* bias, const int32_t* targets,
+                                 const float* lse, int64_t N, int V, int H, int32_t ignore_index, int reduction,
+                                 void* dx, int64_t lddx, void* dweight, int64_t lddw, void* dbias, void* ws,
+                                 size_t ws_bytes, ctcpb_stream_t stream) {
+  int rc = check_types(type, bias || dbias ? bias_type : type);
+  if (rc || (rc = check_dims(N, V, H))) return rc;
+  if (reduction < CTCPB_REDUCE_NONE || reduction > CTCPB_REDUCE_SUM) return CTCPB_EINVAL;
+  if (!dx && !dweight && !dbias) return CTCPB_OK;
+  if ((N > 0 && (ldx < H || (dx && lddx < H))) || ldw < H || (dweight && lddw < H)) return CTCPB_EINVAL;
+  if (!weight || (N > 0 && (!x || !targets || !lse || !grad)) || (reduction != CTCPB_REDUCE_NONE && !grad))
+    return CTCPB_ENULL;
+  const CeLayout l = ce_layout(N, V, H, true);
+  if ((rc = check_ws(ws, ws_bytes, l.total))) return rc;
+  cudaStream_t s = (cudaStream_t)stream;
+  char* b = (char*)ws;
+  RowArgs r{};
+  // with no rows and no reduction there is no gradient to read: the scale does not matter, nothing is summed
+  r.grad = grad ? grad : (const float*)(b + l.o_ctl + 16);
+  r.lse_in = lse;
+  r.lse_c = (float*)(b + l.o_lse);
+  r.rs = (float*)(b + l.o_rs);
+  r.dx = (u16*)dx;
+  r.lddx = lddx;
+  if ((rc = ce_rows(type, x, ldx, targets, N, V, H, ignore_index, reduction, l, b, r, s))) return rc;
+  if (!rows_aligned(weight, ldw)) {
+    TRY(copy_rows(weight, ldw, b + l.o_w, l.Hp, V, H, s));
+    weight = b + l.o_w;
+    ldw = l.Hp;
+  }
+  const int cg = 1, sms = sm_count();
+  for (int p = 0; p < l.pieces; ++p) {
+    const int v0 = p * l.piece, cols = V - v0 < l.piece ? V - v0 : l.piece;
+    CUtensorMap ma, mb;
+    // d
+    if (!make_map(&ma, type, r.xg, l.Hp, l.Np, l.Hp, 128) || !make_map(&mb, type, weight, H, V, ldw, l.bn / cg))
+      return CTCPB_ECUDA;
+    GemmArgs a{};
+    a.rows_dev = r.nv;
+    a.rows = (int)N;
+    a.N = cols;
+    a.K = H;
+    a.bn = l.bn;
+    a.stages = stages_of(l.bn, cg);
+    a.group = group_of(H, cg);
+    a.col0 = v0;
+    a.bias = bias;
+    a.bias_type = bias_type;
+    a.tgt = r.tgt;
+    a.lse = r.lse_c;
+    a.rs = r.rs;
+    a.out = b + l.o_d;
+    a.ldo = l.piece;
+    a.dbp = dbias ? (float*)(b + l.o_dbp) : nullptr;
+    a.status = r.status;
+    long long tiles = l.Np / 128 * ((cols + l.bn - 1) / l.bn);
+    TRY((launch_gemm<kDlogits, false, false>(type, cg, ma, mb, a, (int)(tiles < sms ? tiles : sms), s)));
+    if (dbias) {
+      k_bias_grad<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(a.dbp, l.piece, r.nv, cg, r.scale, dbias, bias_type, v0,
+                                                               cols);
+      TRY(cudaGetLastError());
+    }
+    if (dx && N > 0) {  // dx (+)= d w[piece]
+      if (!make_map(&ma, type, b + l.o_d, l.piece, l.Np, l.piece, 128) || !make_map(&mb, type, weight, H, V, ldw, 64))
+        return CTCPB_ECUDA;
+      GemmArgs g{};
+      g.rows_dev = r.nv;
+      g.rows = (int)N;
+      g.N = H;
+      g.K = cols;
+      g.bn = l.pbn;
+      g.stages = stages_of(l.pbn, cg);
+      g.group = group_of(l.piece, cg);
+      g.split = 1;
+      g.col0 = v0;
+      g.out = dx;
+      g.ldo = lddx;
+      g.vec = rows_aligned(dx, lddx);
+      g.scale = r.scale;
+      g.rowmap = r.rowmap;
+      g.slots = (float*)(b + l.o_slots);
+      g.acc = l.pieces > 1 ? (float*)(b + l.o_acc) : nullptr;
+      g.first = p == 0;
+      g.last = p == l.pieces - 1;
+      g.status = r.status;
+      TRY((launch_gemm<kProduct, false, true>(type, cg, ma, mb, g, sms, s)));
+      tiles = l.Np / 128 * ((H + l.pbn - 1) / l.pbn);
+      TRY(type == CTCPB_BF16 ? (launch_join_t<__nv_bfloat16, 1>(g, tiles, sms, s)) : (launch_join_t<__half, 1>(g, tiles, sms, s)));
+    }
+    if (dweight) {  // dw[piece] = d^T x
+      if (!make_map(&ma, type, b + l.o_d, l.piece, l.Np, l.piece, 64) || !make_map(&mb, type, r.xg, l.Hp, l.Np, l.Hp, 64))
+        return CTCPB_ECUDA;
+      GemmArgs g{};
+      g.rows_dev = r.nv;
+      g.rows = (int)N;
+      g.M = cols;
+      g.N = H;
+      g.bn = l.pbn;
+      g.stages = stages_of(l.pbn, cg);
+      g.group = 8;
+      g.split = 1;
+      g.out = (u16*)dweight + (long long)v0 * lddw;
+      g.ldo = lddw;
+      g.vec = rows_aligned(g.out, lddw);
+      g.scale = r.scale;
+      g.slots = (float*)(b + l.o_slots);
+      g.first = g.last = 1;
+      g.status = r.status;
+      TRY((launch_gemm<kProduct, true, true>(type, cg, ma, mb, g, sms, s)));
+      tiles = (long long)((cols + 127) / 128) * ((H + l.pbn - 1) / l.pbn);
+      TRY(type == CTCPB_BF16 ? (launch_join_t<__nv_bfloat16, 1>(g, tiles, sms, s)) : (launch_join_t<__half, 1>(g, tiles, sms, s)));
+    }
+  }
+  return CTCPB_OK;
+}
+
+}  // extern "C"

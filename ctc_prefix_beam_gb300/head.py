@@ -1,0 +1,268 @@
+"""Thin Python binding of the label head (include/ctcpb.h): what produces the
+decoder's ``log_prob`` and what trains it.
+
+    y, mean, rstd = layer_norm(x, weight, bias)
+    log_prob = log_probs(y, w, b)                       # [..., V] float32, for decode_offline / step_chunk
+    loss, lse = cross_entropy(y, w, targets, b)         # the logits are never stored
+    dy, dw, db = cross_entropy_backward(grad, y, w, targets, lse, b)
+    dx, dweight, dbias = layer_norm_backward(dy, x, weight, mean, rstd)
+
+Argument marshalling only, as in ``decoder``: tensors live on one CUDA device,
+the calls run on its current stream and allocate their outputs and workspaces
+from PyTorch unless they are given.  Rows are frames: ``x`` is [..., H].
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import decoder as D
+
+NONE, MEAN, SUM = 0, 1, 2
+DEV_TARGET = 0x20
+_REDUCTIONS = {"none": NONE, "mean": MEAN, "sum": SUM}
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_fns = None
+
+
+def _lib():
+    global _fns
+    if _fns is None:
+        L = D.lib()
+        P, I, I64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
+        SZ, SZP = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+        sig = {
+            "ctcpb_layer_norm": [I, I, P, I64, P, P, F, I64, I, P, I64, P, P, P],
+            "ctcpb_layer_norm_workspace_size": [I64, I, SZP],
+            "ctcpb_layer_norm_backward": [I, I, P, I64, P, I64, P, P, P, I64, I, P, I64, P, P, P, SZ, P],
+            "ctcpb_log_probs_workspace_size": [I, I64, I, I, SZP],
+            "ctcpb_log_probs": [I, I, P, I64, P, I64, P, I64, I, I, P, I64, P, SZ, P],
+            "ctcpb_cross_entropy_workspace_size": [I, I64, I, I, I, SZP],
+            "ctcpb_cross_entropy": [I, I, P, I64, P, I64, P, P, I64, I, I, I, I, P, P, P, SZ, P],
+            "ctcpb_cross_entropy_backward": [I, I, P, P, I64, P, I64, P, P, P, I64, I, I, I, I, P, I64, P, I64, P, P, SZ,
+                                             P],
+        }
+        fns = {}
+        for name, args in sig.items():
+            fn = getattr(L, name)
+            fn.restype, fn.argtypes = I, args
+            fns[name] = fn
+        _fns = fns
+    return _fns
+
+
+def _rows(t: torch.Tensor, what: str, dtype=None):
+    """``t`` [..., H] as rows: (tensor, N, H, row stride).  Leading dimensions
+    that do not lie at one stride are copied together."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() < 1 or t.dtype not in _TYPES:
+        raise ValueError(f"{what} must be a CUDA float32, bfloat16 or float16 tensor [..., H]")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}")
+    if not (t.is_contiguous() or (t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1])):
+        H = t.shape[-1]
+        ld = t.stride(-2) if t.dim() > 1 else H
+        n = 1
+        ok = (H <= 1 or t.stride(-1) == 1) and ld >= H
+        for d in range(t.dim() - 2, -1, -1):
+            ok = ok and (t.shape[d] <= 1 or t.stride(d) == ld * n)
+            n *= t.shape[d]
+        if not ok:
+            t = t.contiguous()
+    H = t.shape[-1]
+    N = t.numel() // H if H else 0
+    ld = t.stride(-2) if t.dim() > 1 and t.shape[-2] > 1 else H
+    if N > 1 and t.dim() > 2 and t.shape[-2] == 1:  # the rows lie along an outer dimension
+        ld = next(t.stride(d) for d in range(t.dim() - 3, -1, -1) if t.shape[d] > 1)
+    return t, N, H, ld
+
+
+def _matrix(w: torch.Tensor, dtype, device, what: str) -> torch.Tensor:
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.dtype != dtype or w.device != device:
+        raise ValueError(f"{what} must be a {dtype} tensor [V, H] on {device}")
+    if w.shape[1] > 1 and w.stride(1) != 1 or w.shape[0] > 1 and w.stride(0) < w.shape[1]:
+        w = w.contiguous()
+    return w
+
+
+def _ld(w: torch.Tensor) -> int:
+    return w.stride(0) if w.shape[0] > 1 else w.shape[1]
+
+
+def _params(dtype, n: int, device, **named):
+    """The parameter vectors (contiguous) and their common type."""
+    kind = None
+    out = []
+    for name, p in named.items():
+        if p is not None:
+            if not isinstance(p, torch.Tensor) or p.device != device or p.shape != (n,) or \
+                    p.dtype not in (dtype, torch.float32) or (kind is not None and p.dtype != kind):
+                raise ValueError(f"{name} must be a {dtype} or float32 tensor [{n}] on {device}, "
+                                 "the parameters of one type")
+            kind = p.dtype
+            p = p.contiguous()
+        out.append(p)
+    return out, kind if kind is not None else dtype
+
+
+def _given(t: torch.Tensor, shape, dtype, device, what: str) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device \
+            or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+    return t
+
+
+def _size(name: str, *args) -> int:
+    n = ctypes.c_size_t()
+    D._check(_lib()[name](*args, ctypes.byref(n)), name[6:])
+    return n.value
+
+
+def _workspace(ws, need: int, device):
+    if ws is None:
+        ws = D._alloc(need, device)
+    return ws, D._check_buf(ws, need, device, "workspace")
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, *,
+               eps: float = 1e-5, outputs=None):
+    """Layer norm over the last dimension.  Returns (y like x, mean, rstd
+    [...] float32); ``outputs``: the three to write."""
+    xr, N, H, ldx = _rows(x, "x")
+    dev, dt = xr.device, xr.dtype
+    (w, b), pt = _params(dt, H, dev, weight=weight, bias=bias)
+    lead = x.shape[:-1]
+    if outputs is None:
+        y = torch.empty(x.shape, dtype=dt, device=dev)
+        mean, rstd = torch.empty((2, *lead), dtype=torch.float32, device=dev).unbind(0)
+    else:
+        y, mean, rstd = outputs
+        _given(y, x.shape, dt, dev, "y")
+        _given(mean, lead, torch.float32, dev, "mean")
+        _given(rstd, lead, torch.float32, dev, "rstd")
+    D._check(D._call(dev, _lib()["ctcpb_layer_norm"], _TYPES[dt], _TYPES[pt], D._ptr(xr), ldx, D._ptr(w), D._ptr(b),
+                     eps, N, H, D._ptr(y), H, D._ptr(mean), D._ptr(rstd), D._stream(dev)), "layer_norm")
+    return y, mean, rstd
+
+
+def layer_norm_workspace_size(N: int, H: int) -> int:
+    return _size("ctcpb_layer_norm_workspace_size", N, H)
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
+                        rstd: torch.Tensor, *, param_dtype=None, workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``layer_norm``: (dx like x, dweight, dbias [H]).  The last
+    two are of ``weight``'s type, or ``param_dtype`` (x's) without a weight."""
+    xr, N, H, ldx = _rows(x, "x")
+    dev, dt = xr.device, xr.dtype
+    dyr, n2, h2, lddy = _rows(dy, "dy", dt)
+    if dy.shape != x.shape or dyr.device != dev:
+        raise ValueError("dy must have x's shape and device")
+    lead = x.shape[:-1]
+    _given(mean, lead, torch.float32, dev, "mean")
+    _given(rstd, lead, torch.float32, dev, "rstd")
+    (w,), pt = _params(dt, H, dev, weight=weight)
+    if weight is None and param_dtype is not None:
+        if param_dtype not in (dt, torch.float32):
+            raise ValueError(f"param_dtype must be {dt} or float32")
+        pt = param_dtype
+    dx = torch.empty(x.shape, dtype=dt, device=dev)
+    dw, db = torch.empty((2, H), dtype=pt, device=dev).unbind(0)
+    ws, nbytes = _workspace(workspace, layer_norm_workspace_size(N, H), dev)
+    D._check(D._call(dev, _lib()["ctcpb_layer_norm_backward"], _TYPES[dt], _TYPES[pt], D._ptr(dyr), lddy, D._ptr(xr),
+                     ldx, D._ptr(w), D._ptr(mean), D._ptr(rstd), N, H, D._ptr(dx), H, D._ptr(dw), D._ptr(db),
+                     D._ptr(ws), nbytes, D._stream(dev)), "layer_norm_backward")
+    return dx, dw, db
+
+
+def _head_args(x, weight, bias):
+    xr, N, H, ldx = _rows(x, "x")
+    dev, dt = xr.device, xr.dtype
+    w = _matrix(weight, dt, dev, "weight")
+    V = w.shape[0]
+    if w.shape[1] != H:
+        raise ValueError(f"weight must be [V, {H}]")
+    (b,), bt = _params(dt, V, dev, bias=bias)
+    return xr, N, H, ldx, dev, dt, w, V, b, bt
+
+
+def log_probs_workspace_size(dtype, N: int, V: int, H: int) -> int:
+    return _size("ctcpb_log_probs_workspace_size", _TYPES[dtype], N, V, H)
+
+
+def log_probs(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+              out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The decoder's input, log_softmax(x weight^T + bias): float32 [..., V].
+    x and weight are bfloat16 or float16.  ``out``: a tensor [..., V] to write,
+    its rows at one stride (the padded rows of a wider tensor, for instance)."""
+    xr, N, H, ldx, dev, dt, w, V, b, bt = _head_args(x, weight, bias)
+    shape = (*x.shape[:-1], V)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=dev)
+    if tuple(out.shape) != shape or out.dtype != torch.float32 or out.device != dev:
+        raise ValueError(f"out must be a float32 tensor {list(shape)} on {dev}")
+    o, _, _, ldo = _rows(out, "out")
+    if o is not out:
+        raise ValueError("out's rows must lie at one stride, their labels contiguous")
+    ws, nbytes = _workspace(workspace, log_probs_workspace_size(dt, N, V, H), dev)
+    D._check(D._call(dev, _lib()["ctcpb_log_probs"], _TYPES[dt], _TYPES[bt], D._ptr(xr), ldx, D._ptr(w), _ld(w),
+                     D._ptr(b), N, V, H, D._ptr(out), ldo, D._ptr(ws), nbytes, D._stream(dev)), "log_probs")
+    return out
+
+
+def cross_entropy_workspace_size(dtype, N: int, V: int, H: int, backward: bool) -> int:
+    return _size("ctcpb_cross_entropy_workspace_size", _TYPES[dtype], N, V, H, int(bool(backward)))
+
+
+def _targets(targets, x, dev):
+    if not isinstance(targets, torch.Tensor) or targets.dtype != torch.int32 or targets.device != dev or \
+            targets.shape != x.shape[:-1]:
+        raise ValueError(f"targets must be an int32 tensor {list(x.shape[:-1])} on {dev}")
+    return targets.contiguous()
+
+
+def _reduction(reduction: str) -> int:
+    if reduction not in _REDUCTIONS:
+        raise ValueError("reduction must be none, mean or sum")
+    return _REDUCTIONS[reduction]
+
+
+def cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+                  ignore_index: int = -1, reduction: str = "mean", workspace: Optional[torch.Tensor] = None):
+    """Softmax cross entropy of the logits x weight^T + bias, which are never
+    stored.  ``targets`` int32 [...]; rows whose target is ``ignore_index`` take
+    no part.  Returns (loss, lse [...]): float32, the loss a scalar or [...]
+    (reduction "none").  ``D.read_status(workspace)`` holds ``DEV_TARGET`` if a
+    target was out of range (such a row is ignored)."""
+    xr, N, H, ldx, dev, dt, w, V, b, bt = _head_args(x, weight, bias)
+    t, red = _targets(targets, x, dev), _reduction(reduction)
+    lead = x.shape[:-1]
+    loss = torch.empty(lead if red == NONE else (), dtype=torch.float32, device=dev)
+    lse = torch.empty(lead, dtype=torch.float32, device=dev)
+    ws, nbytes = _workspace(workspace, cross_entropy_workspace_size(dt, N, V, H, False), dev)
+    D._check(D._call(dev, _lib()["ctcpb_cross_entropy"], _TYPES[dt], _TYPES[bt], D._ptr(xr), ldx, D._ptr(w), _ld(w),
+                     D._ptr(b), D._ptr(t), N, V, H, ignore_index, red, D._ptr(loss), D._ptr(lse), D._ptr(ws), nbytes,
+                     D._stream(dev)), "cross_entropy")
+    return loss, lse
+
+
+def cross_entropy_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                           lse: torch.Tensor, bias: Optional[torch.Tensor] = None, *, ignore_index: int = -1,
+                           reduction: str = "mean", workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``cross_entropy`` for the loss's gradient ``grad`` (float32,
+    a scalar, or [...] for reduction "none"): (dx like x, dweight, dbias; dbias
+    is None without a bias)."""
+    xr, N, H, ldx, dev, dt, w, V, b, bt = _head_args(x, weight, bias)
+    t, red = _targets(targets, x, dev), _reduction(reduction)
+    lead = x.shape[:-1]
+    _given(lse, lead, torch.float32, dev, "lse")
+    _given(grad, lead if red == NONE else (), torch.float32, dev, "grad")
+    dx = torch.empty(x.shape, dtype=dt, device=dev)
+    dw = torch.empty((V, H), dtype=dt, device=dev)
+    db = torch.empty((V,), dtype=bt, device=dev) if bias is not None else None
+    ws, nbytes = _workspace(workspace, cross_entropy_workspace_size(dt, N, V, H, True), dev)
+    D._check(D._call(dev, _lib()["ctcpb_cross_entropy_backward"], _TYPES[dt], _TYPES[bt], D._ptr(grad), D._ptr(xr), ldx,
+                     D._ptr(w), _ld(w), D._ptr(b), D._ptr(t), D._ptr(lse), N, V, H, ignore_index, red, D._ptr(dx), H,
+                     D._ptr(dw), H, D._ptr(db), D._ptr(ws), nbytes, D._stream(dev)), "cross_entropy_backward")
+    return dx, dw, db

@@ -68,6 +68,7 @@ int ctcpb_lse_table(float* out, int n);
 #define CTCPB_DEV_TIMEOUT 0x4u  /* a bounded inter-block wait gave up: results of the call are invalid */
 #define CTCPB_DEV_OVERFLOW 0x8u /* an internal candidate buffer overflowed: results are invalid */
 #define CTCPB_DEV_BOOST 0x10u   /* a label-boost entry was rejected and ignored (see ctcpb_boost) */
+#define CTCPB_DEV_TARGET 0x20u  /* a target outside [0, V) was ignored (ctcpb_cross_entropy) */
 
 /*
  * Decoder configuration (section 11).
@@ -423,6 +424,105 @@ int ctcpb_select_frames(const ctcpb_config* cfg, const float* log_prob, int64_t 
 int ctcpb_topk_prepass(const ctcpb_config* cfg, const float* log_prob, int64_t stride_r, int R, int V,
                        int32_t* ids, float* lps, int32_t* cnt, float* lpb, float* front_lp, int32_t* front_id,
                        ctcpb_stream_t stream);
+
+/* ---- The label head: what produces log_prob and what trains it.
+ *
+ * An acoustic model ends in a layer norm and a linear head; the head's
+ * log-softmax is the decoder's log_prob.  Rows are frames (or tokens): x is
+ * [N, H], row r at x + r * ldx elements, its features contiguous.  The
+ * conventions above hold: device pointers, caller-owned memory, asynchronous
+ * calls, statuses.  Element types: */
+#define CTCPB_F32 0
+#define CTCPB_BF16 1
+#define CTCPB_F16 2
+/* Limits: N <= 2^24 rows, H <= 8192 features, V <= 2^20 labels. */
+
+/*
+ * Layer norm: y = (x - mean) * rstd * weight + bias, with the mean and
+ * rstd = 1 / sqrt(variance + eps) of each row (variance over H, not H - 1).
+ *   type         of x and y: CTCPB_F32, CTCPB_BF16 or CTCPB_F16.
+ *   param_type   of weight and bias: `type` or CTCPB_F32.
+ *   weight, bias [H], each may be NULL (1 and 0).
+ *   mean, rstd   [N] float32, for the backward pass; both NULL: not written.
+ * Sums and statistics are float32; y is rounded once.  N == 0 is a no-op.
+ */
+int ctcpb_layer_norm(int type, int param_type, const void* x, int64_t ldx, const void* weight, const void* bias,
+                     float eps, int64_t N, int H, void* y, int64_t ldy, float* mean, float* rstd,
+                     ctcpb_stream_t stream);
+
+/*
+ * Its backward pass: with xh = (x - mean) * rstd and t = dy * weight,
+ *   dx = rstd * (t - mean_H(t) - xh * mean_H(t * xh)),
+ *   dweight = sum over rows of dy * xh,  dbias = sum over rows of dy.
+ * x, mean, rstd as given to and written by ctcpb_layer_norm.  dx, dweight and
+ * dbias may each be NULL (not computed); with N == 0 the sums are 0.  The row
+ * sums are made in a fixed order, so results are reproducible bit for bit.
+ * The workspace is needed for dweight and dbias.
+ */
+int ctcpb_layer_norm_workspace_size(int64_t N, int H, size_t* bytes);
+int ctcpb_layer_norm_backward(int type, int param_type, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                              const void* weight, const float* mean, const float* rstd, int64_t N, int H, void* dx,
+                              int64_t lddx, void* dweight, void* dbias, void* ws, size_t ws_bytes,
+                              ctcpb_stream_t stream);
+
+/*
+ * The decoder's input: out[r, :] = log_softmax(x[r] weight^T + bias), float32.
+ *   type       of x and weight: CTCPB_BF16 or CTCPB_F16 (products on the
+ *              tensor cores, accumulated in float32).
+ *   weight     [V, H], row stride ldw elements.
+ *   bias       [V] of bias_type (`type` or CTCPB_F32), or NULL.  A bias of
+ *              -inf takes its label out (log-probability -inf); a row whose
+ *              labels are all out is NaN.
+ *   out        row stride ldo (>= V) elements.  Rows that start on 16-byte
+ *              boundaries (ldo % 4 == 0) are written, and decoded, fastest.
+ *   ws         ctcpb_log_probs_workspace_size() bytes.
+ * Any strides >= H and any alignment of the element type are taken; x or
+ * weight whose rows do not start on 16-byte boundaries are laid out again in
+ * the workspace first.  N == 0 is a no-op.
+ */
+int ctcpb_log_probs_workspace_size(int type, int64_t N, int V, int H, size_t* bytes);
+int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const void* weight, int64_t ldw,
+                    const void* bias, int64_t N, int V, int H, float* out, int64_t ldo, void* ws, size_t ws_bytes,
+                    ctcpb_stream_t stream);
+
+/*
+ * Softmax cross entropy of the head's logits z = x weight^T + bias, which are
+ * never stored: loss_r = lse_r - z[r, target_r], lse_r = log sum_c exp z[r, c].
+ *   targets       [N] int32.  A row whose target is ignore_index takes no part:
+ *                 its x is not read into any sum, its loss and lse are 0.  Any
+ *                 other target outside [0, V) is ignored as well and sets
+ *                 CTCPB_DEV_TARGET in the status word.
+ *   reduction     CTCPB_REDUCE_NONE: loss is [N]; _MEAN: one value, the mean over
+ *                 the rows that take part (NaN if none does); _SUM: one value.
+ *   lse           [N] float32, for the backward pass.
+ * Types as in ctcpb_log_probs; the losses are float32.
+ */
+#define CTCPB_REDUCE_NONE 0
+#define CTCPB_REDUCE_MEAN 1
+#define CTCPB_REDUCE_SUM 2
+int ctcpb_cross_entropy_workspace_size(int type, int64_t N, int V, int H, int backward, size_t* bytes);
+int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, const void* weight, int64_t ldw,
+                        const void* bias, const int32_t* targets, int64_t N, int V, int H, int32_t ignore_index,
+                        int reduction, float* loss, float* lse, void* ws, size_t ws_bytes, ctcpb_stream_t stream);
+
+/*
+ * Its gradients: with d[r, c] = (exp(z[r, c] - lse_r) - [c = target_r]) * g_r,
+ *   dx = d weight  [N, H],  dweight = d^T x  [V, H],  dbias = sum_r d[r]  [V],
+ * where g_r is grad[r] (REDUCE_NONE), grad[0] (REDUCE_SUM) or grad[0] over the
+ * number of rows that take part (REDUCE_MEAN); ignored rows get exact zeros.
+ *   grad          device float32: [N] or one value.
+ *   lse           of the forward call, on the same x, weight, bias and targets.
+ *   dx, dweight   of `type`, row strides lddx, lddw;  dbias of bias_type.  Each
+ *                 may be NULL (not computed).
+ * The logits are made again, in pieces of the vocabulary whose d fits in 256 MB
+ * of the workspace.  d is held in `type` (16 bits); every sum is float32 and in
+ * a fixed order, so results are reproducible bit for bit.
+ */
+int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, const void* x, int64_t ldx,
+                                 const void* weight, int64_t ldw, const void* bias, const int32_t* targets,
+                                 const float* lse, int64_t N, int V, int H, int32_t ignore_index, int reduction,
+                                 void* dx, int64_t lddx, void* dweight, int64_t lddw, void* dbias, void* ws,
+                                 size_t ws_bytes, ctcpb_stream_t stream);
 
 #ifdef __cplusplus
 }
