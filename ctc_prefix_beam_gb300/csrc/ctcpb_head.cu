@@ -30,6 +30,7 @@ constexpr int kTileBytes = 196608;  // operand stages
 constexpr int kStageBuf = 4096;     // per epilogue warp: 32 rows of 128 bytes
 constexpr int kSmem = kTileBytes + kEpiWarps * (kStageBuf + 64 * 4) + 256;
 constexpr u32 kTmemCols = 512;
+constexpr int kSplitDepth = 8;     // slices of 64 below which a tile is never split along K
 
 struct GemmArgs {
   const int* rows_dev;  // number of rows, on the device (null: `rows`)
@@ -46,6 +47,8 @@ struct GemmArgs {
   const int* tgt;
   const float* lse;
   const float* rs;      // per-row factor of d
+  int per_row;          // ... which differs from row to row
+  float factor;         // of the accumulator: log2(e) (kLogp: 1), times what truncation lost
   float* zt;
   float2* part;
   long long part_ld;
@@ -92,7 +95,7 @@ struct Sched {
     dp = tiles;
     rem = 0;
     nw = 1;
-    if (a.split && ks >= 8) {
+    if (a.split && ks >= kSplitDepth) {
       rem = tiles % G;
       if (5 * rem > 4 * G) rem = 0;  // a nearly full wave: joining would cost more than it gives
       dp = tiles - rem;
@@ -149,16 +152,14 @@ __device__ __forceinline__ void stage_f32(char* buf, int lane, const float (&v)[
     *reinterpret_cast<float4*>(buf + stage_at(lane, c)) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
 }
 template <class T>
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(Elem<T>::pack(v[0], v[1]), Elem<T>::pack(v[2], v[3]), Elem<T>::pack(v[4], v[5]),
+                    Elem<T>::pack(v[6], v[7]));
+}
+template <class T>
 __device__ __forceinline__ void stage_16(char* buf, int lane, const float (&v)[32], int half) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint4 p;
-    p.x = Elem<T>::pack(v[8 * c], v[8 * c + 1]);
-    p.y = Elem<T>::pack(v[8 * c + 2], v[8 * c + 3]);
-    p.z = Elem<T>::pack(v[8 * c + 4], v[8 * c + 5]);
-    p.w = Elem<T>::pack(v[8 * c + 6], v[8 * c + 7]);
-    *reinterpret_cast<uint4*>(buf + stage_at(lane, 4 * half + c)) = p;
-  }
+  for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(buf + stage_at(lane, 4 * half + c)) = pack8<T>(v + 8 * c);
 }
 // Write the buffer's rows (E: float for 32 columns, 16-bit for 64) to columns
 // [c0, cols) of output rows; orow is this lane's output row, -1 for none.
@@ -248,7 +249,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     *dead = 0;
     mbar_init_fence();
     fence_proxy_async();
-    if (a.reset_status && blockIdx.x == 0) *a.status = 0;
   }
   if (warp == 2) tmem_alloc<CG>(s_tptr, kTmemCols);
   tc_fence_before();
@@ -258,6 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   tc_fence_after();
   const u32 tmem = *tmem_ptr;
+  pdl_wait();
+  pdl_next();
+  if (a.reset_status && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
 
   // bounded wait; false once any wait of the block has given up
   auto wait = [&](u32 bar, u32 parity) -> bool {
@@ -357,12 +360,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int col = n0 + half * 64 + (i >> 1) * 128 + (i & 1) * 32 + lane;
-          bq[i] = col < a.N ? (a.bias ? load_elem(a.bias, a.bias_type, (long long)a.col0 + col) : 0.f) : -INFINITY;
+          bq[i] = col < a.N ? (a.bias ? load_elem(a.bias, a.bias_type, (long long)a.col0 + col) * (MODE == kLogp ? 1.f : kLog2e) : 0.f)
+                            : -INFINITY;
         }
         if (row < mrows) {
           if (a.tgt) tgt = a.tgt[row] - a.col0 - n0;
-          if (MODE != kStats) lse = a.lse[row];
-          if (MODE == kDlogits) rs = a.rs[row];
+          if (MODE == kLogp) lse = a.lse[row];
+          if (MODE == kDlogits) {
+            // d = exp(z - lse) r: a factor r that all rows share is in the exponent
+            rs = a.rs[row];
+            lse = __fmaf_rn(a.lse[row], kLog2e, a.per_row ? 0.f : -log2f(rs));
+          }
         }
       } else if (a.rowmap && orow >= 0) {
         orow = a.rowmap[row];
@@ -370,103 +378,127 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = __all_sync(0xffffffffu, wait(s_tfull + 8 * as, aph)))) break;
       tc_fence_after();
       const u32 d = tmem + 256u * as + ((u32)(q * 32) << 16);
-      for (int u = half * 64; u < a.bn && n0 + u < (MODE == kDlogits ? (int)a.ldo : a.N); u += 128) {
+      // 32 columns of the row, from c0 on (the j-th half of a unit of 64)
+      auto chunk = [&](float(&v)[32], int c0, int j) {
+        if constexpr (MODE != kProduct) {
+          // to base 2 (but for kLogp), so that exp and log cost nothing more: z log2(e) + b log2(e)
+          const float4* b4 = reinterpret_cast<const float4*>(bias_s + 32 * j);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 b = b4[i];
+            fma2(v[4 * i], v[4 * i + 1], a.factor, b.x, b.y);
+            fma2(v[4 * i + 2], v[4 * i + 3], a.factor, b.z, b.w);
+          }
+        }
+        if constexpr (MODE == kStats) {
+          float m4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m4[i] = fmaxf(v[i], v[i + 4]);
+#pragma unroll
+          for (int i = 8; i < 32; i += 8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], fmaxf(v[i + k], v[i + k + 4]));
+          }
+          const float mn = fmaxf(fmaxf(bm, fmaxf(m4[0], m4[1])), fmaxf(m4[2], m4[3]));
+          const float mm = mn == -INFINITY ? 0.f : mn;
+          const int tr = tgt - c0;
+          if (__any_sync(0xffffffffu, (u32)tr < 32u)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (tr == i) a.zt[row] = v[i];
+          }
+          float s[4] = {bs * ex2(bm - mm), 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            add2(v[i], v[i + 1], -mm);
+            add2(v[i + 2], v[i + 3], -mm);
+            add2(s[0], s[1], ex2(v[i]), ex2(v[i + 1]));
+            add2(s[2], s[3], ex2(v[i + 2]), ex2(v[i + 3]));
+          }
+          bm = mn;
+          bs = (s[0] + s[1]) + (s[2] + s[3]);
+        } else if constexpr (MODE == kLogp) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) add2(v[i], v[i + 1], -lse);
+          stage_f32(buf, lane, v);
+          flush_rows<float>(buf, lane, (float*)a.out, a.ldo, orow, n0 + c0, a.N, a.vec);
+        } else if constexpr (MODE == kDlogits) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            add2(v[i], v[i + 1], -lse);
+            v[i] = ex2(v[i]);
+            v[i + 1] = ex2(v[i + 1]);
+          }
+          const int tr = tgt - c0;
+          if (__any_sync(0xffffffffu, (u32)tr < 32u)) {
+            const float one = a.per_row ? 1.f : rs;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] -= tr == i ? one : 0.f;
+          }
+          if (a.per_row) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= rs;
+          }
+          if (__any_sync(0xffffffffu, row >= mrows)) {  // rows past the last one are exact zeros (their z may hold anything)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = row < mrows ? v[i] : 0.f;
+          }
+          stage_16<T>(buf, lane, v, j);
+          if (a.dbp) {
+            const float cs = column_sums(v, lane);
+            if (n0 + c0 + lane < a.ldo) a.dbp[((long long)mtile * 4 + q) * a.ldo + n0 + c0 + lane] = cs;
+          }
+        } else {
+          if (sg.slot >= 0) {  // a share of the depth: to its slot, a column's rows side by side
+            float* o = a.slots + ((long long)sg.slot * CG + rank) * 128 * a.bn + (long long)c0 * 128 + q * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i * 128] = v[i];
+          } else {
+            if (a.acc) {
+              float* o = a.acc + ((long long)sg.tile * CG + rank) * 128 * a.bn + (long long)c0 * 128 + q * 32 + lane;
+              if (!a.first) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] += o[i * 128];
+              }
+              if (!a.last) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i * 128] = v[i];
+              }
+            }
+            if (a.last) {
+              const float f = *a.scale;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] *= f;
+              stage_16<T>(buf, lane, v, j);
+            }
+          }
+        }
+      };
+      // units of 64 columns, every other one to each half of the warps; a
+      // chunk's loads from tensor memory are in flight while the one before
+      // it is worked on
+      const int lim = MODE == kDlogits ? (int)a.ldo - n0 : a.N - n0, end = a.bn < lim ? a.bn : lim;
+      float v0[32], v1[32];
+      if (half * 64 < end) tmem_load32(v0, d + half * 64);
+      for (int u = half * 64; u < end; u += 128) {
         if constexpr (MODE != kProduct) {
           __syncwarp();
           bias_s[lane] = u < 128 ? bq[0] : bq[2];
           bias_s[lane + 32] = u < 128 ? bq[1] : bq[3];
           __syncwarp();
         }
+        const bool two = u + 32 < a.bn;  // a tile of 32 columns has no second half
+        tmem_wait(v0);
+        if (two) tmem_load32(v1, d + u + 32);
+        chunk(v0, u, 0);
+        if (two) {
+          tmem_wait(v1);
+          if (u + 128 < end) tmem_load32(v0, d + u + 128);
+          chunk(v1, u + 32, 1);
+        } else if constexpr (MODE == kDlogits) {  // zeros fill the unit
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int c0 = u + 32 * j;
-          if (c0 < a.bn) {
-            float v[32];
-            tmem_load32(v, d + c0);
-            if constexpr (MODE != kProduct) {
-              const float4* b4 = reinterpret_cast<const float4*>(bias_s + 32 * j);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 b = b4[i];
-                v[4 * i] += b.x;
-                v[4 * i + 1] += b.y;
-                v[4 * i + 2] += b.z;
-                v[4 * i + 3] += b.w;
-              }
-            }
-            if constexpr (MODE == kStats) {
-              float mx = v[0];
-#pragma unroll
-              for (int i = 1; i < 32; ++i) mx = fmaxf(mx, v[i]);
-              const float mn = fmaxf(bm, mx), mm = mn == -INFINITY ? 0.f : mn;
-              float s0 = bs * ex2((bm - mm) * kLog2e), s1 = 0.f, s2 = 0.f, s3 = 0.f;
-              const int tr = tgt - c0;
-              if (__any_sync(0xffffffffu, (u32)tr < 32u)) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (tr == i) a.zt[row] = v[i];
-              }
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                s0 += ex2((v[i] - mm) * kLog2e);
-                s1 += ex2((v[i + 1] - mm) * kLog2e);
-                s2 += ex2((v[i + 2] - mm) * kLog2e);
-                s3 += ex2((v[i + 3] - mm) * kLog2e);
-              }
-              bm = mn;
-              bs = (s0 + s1) + (s2 + s3);
-            } else if constexpr (MODE == kLogp) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] -= lse;
-              stage_f32(buf, lane, v);
-              flush_rows<float>(buf, lane, (float*)a.out, a.ldo, orow, n0 + c0, a.N, a.vec);
-            } else if constexpr (MODE == kDlogits) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = ex2((v[i] - lse) * kLog2e);
-              const int tr = tgt - c0;
-              if (__any_sync(0xffffffffu, (u32)tr < 32u)) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] -= tr == i ? 1.f : 0.f;
-              }
-              // rows past the last one are exact zeros (their z may hold anything)
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = row < mrows ? v[i] * rs : 0.f;
-              stage_16<T>(buf, lane, v, j);
-              if (a.dbp) {
-                const float cs = column_sums(v, lane);
-                if (n0 + c0 + lane < a.ldo) a.dbp[((long long)mtile * 4 + q) * a.ldo + n0 + c0 + lane] = cs;
-              }
-            } else {
-              if (sg.slot >= 0) {  // a share of the depth: to its slot, a column's rows side by side
-                float* o = a.slots + ((long long)sg.slot * CG + rank) * 128 * a.bn + (long long)c0 * 128 + q * 32 + lane;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i * 128] = v[i];
-              } else {
-                if (a.acc) {
-                  float* o = a.acc + ((long long)sg.tile * CG + rank) * 128 * a.bn + (long long)c0 * 128 + q * 32 + lane;
-                  if (!a.first) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += o[i * 128];
-                  }
-                  if (!a.last) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i * 128] = v[i];
-                  }
-                }
-                if (a.last) {
-                  const float f = *a.scale;
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) v[i] *= f;
-                  stage_16<T>(buf, lane, v, j);
-                }
-              }
-            }
-          } else if constexpr (MODE == kDlogits) {  // a tile of 32 columns: zeros fill the unit
-            float v[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-            stage_16<T>(buf, lane, v, j);
-          }
+          for (int i = 0; i < 32; ++i) v1[i] = 0.f;
+          stage_16<T>(buf, lane, v1, 1);
         }
         if constexpr (MODE == kDlogits)
           flush_rows<T>(buf, lane, (T*)a.out, a.ldo, (long long)row, n0 + u, (int)a.ldo, true);
@@ -502,17 +534,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The shares of every tile of the split wave, added in the order of K, and the
-// tile's output written: a warp per 32 rows and 64 columns.
+// tile's output written: a block per 32 rows and 64 columns, 8 columns a warp
+// (16 bytes of each row), two shares' loads in flight.
 template <class T, int CG>
 __global__ void __launch_bounds__(256) k_join(const GemmArgs a, int workers) {
-  __shared__ __align__(16) char smem[8 * kStageBuf];
+  __shared__ __align__(16) char buf[kStageBuf];
+  pdl_wait();
   Sched sc;
   sc.init(a, CG, 0, workers);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.x;
-  const int units = CG * 4 * ((a.bn + 63) / 64);
-  const int unit = blockIdx.y * 8 + warp;
-  if (r >= sc.rem || unit >= units) return;
+  const int r = blockIdx.x, unit = blockIdx.y;
+  if (r >= sc.rem) return;
   const int lo = r * sc.ks, hi = lo + sc.ks;
   int w = (int)((long long)lo * sc.nw / ((long long)sc.rem * sc.ks));
   while (w > 0 && sc.share(w) > lo) --w;
@@ -525,52 +557,104 @@ __global__ void __launch_bounds__(256) k_join(const GemmArgs a, int workers) {
   if (n0 + u >= a.N) return;
   const int rows = a.rows_dev ? *a.rows_dev : a.rows;
   const int mrows = a.M > 0 ? a.M : rows;
-  const int row = (sg.m * CG + rank) * 128 + q * 32 + lane;
-  long long orow = row < mrows ? (a.rowmap ? a.rowmap[row] : row) : -1;
-  char* const buf = smem + warp * kStageBuf;
+  const int c0 = u + 8 * warp;  // bn is a multiple of 64
+  const long long at = (long long)c0 * 128 + q * 32 + lane, tile = 128ll * a.bn;
+  float v[8];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int c0 = u + 32 * j;
-    if (c0 < a.bn) {
-      float v[32];
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  auto slot_of = [&](int x) { return a.slots + ((2ll * x + (r - sc.share(x) / sc.ks)) * CG + rank) * tile + at; };
+  for (int x = w; x < sc.nw && sc.share(x) < hi; x += 2) {
+    const bool two = x + 1 < sc.nw && sc.share(x + 1) < hi;
+    const float *o = slot_of(x), *p = two ? slot_of(x + 1) : o;
+    float e[8], f[8];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0.f;
-      for (int x = w; x < sc.nw && sc.share(x) < hi; ++x) {
-        const int slot = 2 * x + (r - sc.share(x) / sc.ks);
-        const float* o = a.slots + ((long long)slot * CG + rank) * 128 * a.bn + (long long)c0 * 128 + q * 32 + lane;
+    for (int i = 0; i < 8; ++i) e[i] = o[i * 128];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += o[i * 128];
-      }
-      if (a.acc) {
-        float* o = a.acc + ((long long)sg.tile * CG + rank) * 128 * a.bn + (long long)c0 * 128 + q * 32 + lane;
-        if (!a.first) {
+    for (int i = 0; i < 8; ++i) f[i] = two ? p[i * 128] : 0.f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] += o[i * 128];
-        }
-        if (!a.last) {
+    for (int i = 0; i < 8; ++i) v[i] = (v[i] + e[i]) + f[i];
+  }
+  if (a.acc) {
+    float* o = a.acc + ((long long)sg.tile * CG + rank) * tile + at;
+    if (!a.first) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i * 128] = v[i];
-        }
-      }
-      if (a.last) {
-        const float f = *a.scale;
+      for (int i = 0; i < 8; ++i) v[i] += o[i * 128];
+    }
+    if (!a.last) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= f;
-        stage_16<T>(buf, lane, v, j);
-      }
+      for (int i = 0; i < 8; ++i) o[i * 128] = v[i];
     }
   }
-  if (a.last) flush_rows<T>(buf, lane, (T*)a.out, a.ldo, orow, n0 + u, a.N, a.vec);
+  if (!a.last) return;
+  const float f = *a.scale;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= f;
+  *reinterpret_cast<uint4*>(buf + stage_at(lane, warp)) = pack8<T>(v);
+  __syncthreads();
+  // four rows a warp
+  T* const out = (T*)a.out;
+  const int rr = warp * 4 + (lane >> 3);
+  const int mine = (sg.m * CG + rank) * 128 + q * 32 + rr;
+  if (mine >= mrows) return;
+  const long long orow = a.rowmap ? a.rowmap[mine] : mine;
+  if (a.vec) {
+    const int col = n0 + u + (lane & 7) * 8;
+    const uint4 p = *reinterpret_cast<const uint4*>(buf + stage_at(rr, lane & 7));
+    if (col + 8 <= a.N) {
+      *reinterpret_cast<uint4*>(out + orow * a.ldo + col) = p;
+    } else {
+      const T* e = reinterpret_cast<const T*>(&p);
+      for (int i = 0; i < 8; ++i)
+        if (col + i < a.N) out[orow * a.ldo + col + i] = e[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // 8 lanes a row, neighbouring columns
+      const int c = (lane & 7) + 8 * i;
+      const T e = *reinterpret_cast<const T*>(buf + stage_at(rr, c >> 3) + (c & 7) * 2);
+      if (n0 + u + c < a.N) out[orow * a.ldo + n0 + u + c] = e;
+    }
+  }
 }
 
 // ---------------------------------------------------------------- rows
 
+// Copy H 16-bit elements of a row by a warp, zero up to ld; `vec`: both sides
+// on 16-byte boundaries and H a multiple of 8.
+__device__ __forceinline__ void copy_row(const u16* __restrict__ in, u16* __restrict__ out, int H, int ld, bool vec,
+                                         int lane) {
+  if (vec) {
+    const uint4* const i4 = reinterpret_cast<const uint4*>(in);
+    uint4* const o4 = reinterpret_cast<uint4*>(out);
+    const int n = H >> 3;
+    for (int c = lane; c < n; c += 128) {
+      uint4 p[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c + 32 * k < n) p[k] = i4[c + 32 * k];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c + 32 * k < n) o4[c + 32 * k] = p[k];
+    }
+  } else {
+    for (int c = lane; c < ld; c += 256) {
+      u16 p[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) p[k] = c + 32 * k < H ? in[c + 32 * k] : (u16)0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + 32 * k < ld) out[c + 32 * k] = p[k];
+    }
+  }
+}
+
 // Rows of 16-bit elements to rows of ldo elements, zero from H on.
 __global__ void __launch_bounds__(256) k_copy_rows(const u16* __restrict__ in, long long ldi, u16* __restrict__ out,
                                                    int ldo, long long n, int H) {
-  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_next();
   for (long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); r < n; r += (long long)gridDim.x * 8)
-    for (int c = lane; c < ldo; c += 32) out[r * ldo + c] = c < H ? in[r * ldi + c] : (u16)0;
+    copy_row(in + r * ldi, out + r * ldo, H, ldo, false, threadIdx.x & 31);
 }
 
 struct RowArgs {
@@ -598,9 +682,10 @@ struct RowArgs {
   float* scale;
   u16* dx;
   long long lddx;
+  int dx_vec;
 };
 
-constexpr int kRowBlock = 128;  // rows of a block of k_rows
+constexpr int kRowBlocks = 1024;  // blocks of k_rows at most
 
 __device__ __forceinline__ int block_sum(int v, int* red) {
   v = __reduce_add_sync(0xffffffffu, v);
@@ -615,39 +700,32 @@ __device__ __forceinline__ int block_sum(int v, int* red) {
 // Keep the rows that have a target, in order, side by side: an ignored row
 // costs no product, and whatever it holds (padding may be NaN) never meets a
 // sum.  Each block counts the kept rows before its own by reading the targets,
-// so one launch does it.  The rows up to the next multiple of 256 are zeros.
-__global__ void __launch_bounds__(256) k_rows(const RowArgs a) {
+// so one launch does it; `per` rows a block keep the blocks, and so the
+// targets read, in proportion to N.  The rows up to the next multiple of 64,
+// the depth that the last step of d^T x reads, are zeros.
+__global__ void __launch_bounds__(256) k_rows(const RowArgs a, int per) {
   __shared__ int red[8];
   __shared__ float fred[8];
-  __shared__ int src[kRowBlock];
-  const int base = blockIdx.x * kRowBlock, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ int src[256];
+  pdl_wait();
+  pdl_next();
+  const int base = blockIdx.x * per, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int end = base + per < a.N ? base + per : a.N;
   const bool last = blockIdx.x == gridDim.x - 1;
+  auto kept = [&](int t) { return t >= 0 && t < a.V && t != a.ignore; };
   int before = 0, bad = 0;
-  for (int i = threadIdx.x; i < base; i += 256) {
-    const int t = a.targets[i];
-    const bool in = t >= 0 && t < a.V && t != a.ignore;
-    before += in;
-    bad |= !in && t != a.ignore;
+  for (int i = threadIdx.x; i < base; i += 256 * 8) {
+    int t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = i + 256 * k < base ? a.targets[i + 256 * k] : a.ignore;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool in = kept(t[k]);
+      before += in;
+      bad |= !in && t[k] != a.ignore;
+    }
   }
   before = block_sum(before, red);
-  // this block's rows
-  int t = a.ignore;
-  bool in = false;
-  const int row = base + (int)threadIdx.x;
-  if (threadIdx.x < kRowBlock && row < a.N) {
-    t = a.targets[row];
-    in = t >= 0 && t < a.V && t != a.ignore;
-    bad |= !in && t != a.ignore;
-  }
-  const u32 m = __ballot_sync(0xffffffffu, in);
-  if (lane == 0) red[warp] = __popc(m);
-  __syncthreads();
-  int off = 0, kept = 0;
-  for (int i = 0; i < kRowBlock / 32; ++i) {
-    if (i < warp) off += red[i];
-    kept += red[i];
-  }
-  const int mine = off + __popc(m & ((1u << lane) - 1));
   // the largest |grad| (float16 only): d is scaled by it to stay in range
   float gmax = 1.f;
   if (a.grad && a.reduction == CTCPB_REDUCE_NONE && a.type == CTCPB_F16) {
@@ -660,50 +738,66 @@ __global__ void __launch_bounds__(256) k_rows(const RowArgs a) {
     gmax = g > 0.f ? g : 1.f;
   }
   const float up = a.type == CTCPB_F16 ? 32768.f : 1.f;  // float16: |d| <= 1 is stored as |d| 2^15
-  if (in) {
-    const int to = before + mine;
-    src[mine] = row;
-    a.rowmap[to] = row;
-    a.tgt[to] = t;
-    if (a.grad) {
-      a.lse_c[to] = a.lse_in[row];
-      a.rs[to] = a.reduction == CTCPB_REDUCE_NONE ? a.grad[row] / gmax * up : up;
+  for (int r0 = base; r0 < end; r0 += 256) {  // 256 rows at a time
+    const int row = r0 + (int)threadIdx.x;
+    const int t = row < end ? a.targets[row] : a.ignore;
+    const bool in = kept(t);
+    bad |= !in && t != a.ignore;
+    const u32 m = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) red[warp] = __popc(m);
+    __syncthreads();
+    int off = 0, count = 0;
+    for (int i = 0; i < 8; ++i) {
+      if (i < warp) off += red[i];
+      count += red[i];
     }
-  } else if (threadIdx.x < kRowBlock && row < a.N) {
-    if (a.loss) a.loss[row] = 0.f;
-    if (a.lse) a.lse[row] = 0.f;
-  }
-  __syncthreads();
-  // the kept rows, a warp each
-  for (int i = warp; i < kept; i += 8) {
-    const u16* s = a.x + (long long)src[i] * a.ldx;
-    u16* d = a.xg + (long long)(before + i) * a.ldg;
-    if (a.vec) {
-      for (int c = lane; c < a.H / 8; c += 32) reinterpret_cast<uint4*>(d)[c] = reinterpret_cast<const uint4*>(s)[c];
-    } else {
-      for (int c = lane; c < a.ldg; c += 32) d[c] = c < a.H ? s[c] : (u16)0;
+    if (row < end) {
+      // a kept row's place, an ignored row's complement
+      src[threadIdx.x] = in ? before + off + __popc(m & ((1u << lane) - 1)) : -1;
+      if (in) {
+        const int to = src[threadIdx.x];
+        a.rowmap[to] = row;
+        a.tgt[to] = t;
+        if (a.grad) {
+          a.lse_c[to] = a.lse_in[row];
+          a.rs[to] = a.reduction == CTCPB_REDUCE_NONE ? a.grad[row] / gmax * up : up;
+        }
+      } else {
+        if (a.loss) a.loss[row] = 0.f;
+        if (a.lse) a.lse[row] = 0.f;
+      }
     }
-  }
-  // ignored rows have no gradient
-  if (a.dx) {
-    for (int i = warp; i < kRowBlock && base + i < a.N; i += 8) {
-      const int tt = a.targets[base + i];
-      if (tt >= 0 && tt < a.V && tt != a.ignore) continue;
-      u16* d = a.dx + (long long)(base + i) * a.lddx;
-      for (int c = lane; c < a.H; c += 32) d[c] = 0;
+    __syncthreads();
+    const int n = end - r0 < 256 ? end - r0 : 256;
+    for (int i = warp; i < n; i += 8) {
+      const int to = src[i];
+      if (to >= 0) {
+        copy_row(a.x + (long long)(r0 + i) * a.ldx, a.xg + (long long)to * a.ldg, a.H, a.ldg, a.vec, lane);
+      } else if (a.dx) {  // an ignored row has no gradient
+        u16* d = a.dx + (long long)(r0 + i) * a.lddx;
+        if (a.dx_vec)
+          for (int c = lane; c < a.H / 8; c += 32) reinterpret_cast<uint4*>(d)[c] = make_uint4(0, 0, 0, 0);
+        else
+          for (int c = lane; c < a.H; c += 32) d[c] = 0;
+      }
     }
+    before += count;
+    __syncthreads();
   }
   if (last) {
-    const int nv = before + kept;
-    const int end = nv > 0 ? (nv + 255) / 256 * 256 : 256;
-    for (long long i = threadIdx.x; i < (long long)(end - nv) * a.ldg; i += 256) a.xg[(long long)nv * a.ldg + i] = 0;
+    const int nv = before;  // every kept row
+    const long long z0 = (long long)nv * a.ldg / 8, z1 = (long long)(nv > 0 ? (nv + 63) / 64 * 64 : 64) * a.ldg / 8;
+    for (long long i = z0 + threadIdx.x; i < z1; i += 256) reinterpret_cast<uint4*>(a.xg)[i] = make_uint4(0, 0, 0, 0);
     bad = block_sum(bad, red);
     if (threadIdx.x == 0) {
       *a.nv = nv;
       *a.status = bad ? CTCPB_DEV_TARGET : 0u;
       *a.ticket = 0;
       if (a.grad)
-        *a.scale = (a.reduction == CTCPB_REDUCE_NONE ? gmax : a.grad[0] / (a.reduction == CTCPB_REDUCE_MEAN ? (float)(nv > 0 ? nv : 1) : 1.f)) / up;
+        *a.scale = (a.reduction == CTCPB_REDUCE_NONE
+                        ? gmax
+                        : a.grad[0] / (a.reduction == CTCPB_REDUCE_MEAN ? (float)(nv > 0 ? nv : 1) : 1.f)) /
+                   up;
     }
   }
 }
@@ -723,20 +817,30 @@ struct CombineArgs {
   u32* ticket;
 };
 
-// lse = m + log(sum_j s_j exp(m_j - m)) over a row's tiles, and the losses:
-// a block per 32 rows, 8 slices of the tiles.
-__global__ void __launch_bounds__(256) k_combine(const CombineArgs a) {
-  __shared__ float2 red[8][32];
+// lse = m + log(sum_j s_j exp(m_j - m)) over a row's tiles (m, s and z[target]
+// are to base 2, see kStats), and the losses: a block per 32 rows, 16 slices of
+// the tiles, four of a slice's loads in flight.
+constexpr int kSlices = 16;
+__global__ void __launch_bounds__(32 * kSlices) k_combine(const CombineArgs a) {
+  __shared__ float2 red[kSlices][32];
   __shared__ bool fin;
+  pdl_wait();
+  pdl_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = a.rows_dev ? *a.rows_dev : a.rows;
   const int i = blockIdx.x * 32 + lane;
   float m = -INFINITY, s = 0.f;
   if (i < rows) {
-    for (int j = warp; j < a.slots; j += 8) {
-      const float2 p = a.part[(long long)j * a.part_ld + i];
-      const float mn = fmaxf(m, p.x), mm = mn == -INFINITY ? 0.f : mn;
-      s = s * ex2((m - mm) * kLog2e) + p.y * ex2((p.x - mm) * kLog2e);
+    for (int j = warp; j < a.slots; j += 4 * kSlices) {
+      float2 p[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        p[k] = j + k * kSlices < a.slots ? a.part[(long long)(j + k * kSlices) * a.part_ld + i]
+                                         : make_float2(-INFINITY, 0.f);
+      const float mn = fmaxf(fmaxf(m, fmaxf(p[0].x, p[1].x)), fmaxf(p[2].x, p[3].x)), mm = mn == -INFINITY ? 0.f : mn;
+      s *= ex2(m - mm);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s = __fmaf_rn(p[k].y, ex2(p[k].x - mm), s);
       m = mn;
     }
   }
@@ -744,15 +848,15 @@ __global__ void __launch_bounds__(256) k_combine(const CombineArgs a) {
   __syncthreads();
   float loss = 0.f;
   if (warp == 0 && i < rows) {
-    for (int w = 1; w < 8; ++w) m = fmaxf(m, red[w][lane].x);
+    for (int w = 1; w < kSlices; ++w) m = fmaxf(m, red[w][lane].x);
     const float mm = m == -INFINITY ? 0.f : m;
     s = 0.f;
-    for (int w = 0; w < 8; ++w) s += red[w][lane].y * ex2((red[w][lane].x - mm) * kLog2e);
-    const float lse = mm + logf(s);
+    for (int w = 0; w < kSlices; ++w) s = __fmaf_rn(red[w][lane].y, ex2(red[w][lane].x - mm), s);
+    const float lse2 = mm + log2f(s);
     const int row = a.rowmap ? a.rowmap[i] : i;
-    a.lse[row] = lse;
+    a.lse[row] = lse2 * kLn2;
     if (a.rowmap) {
-      loss = lse - a.zt[i];
+      loss = (lse2 - a.zt[i]) * kLn2;
       if (a.reduction == CTCPB_REDUCE_NONE) a.loss[row] = loss;
     }
   }
@@ -769,12 +873,12 @@ __global__ void __launch_bounds__(256) k_combine(const CombineArgs a) {
   __syncthreads();
   if (!fin) return;
   __threadfence();
-  __shared__ double dred[256];
+  __shared__ double dred[32 * kSlices];
   double d = 0.0;
-  for (int k = threadIdx.x; k < (int)gridDim.x; k += 256) d += (double)((volatile float*)a.sums)[k];
+  for (int k = threadIdx.x; k < (int)gridDim.x; k += 32 * kSlices) d += (double)((volatile float*)a.sums)[k];
   dred[threadIdx.x] = d;
   __syncthreads();
-  for (int k = 128; k > 0; k >>= 1) {
+  for (int k = 16 * kSlices; k > 0; k >>= 1) {
     if ((int)threadIdx.x < k) dred[threadIdx.x] += dred[threadIdx.x + k];
     __syncthreads();
   }
@@ -789,13 +893,21 @@ __global__ void __launch_bounds__(256) k_bias_grad(const float* __restrict__ dbp
                                                    int per, const float* __restrict__ scale, void* db, int type, int col0,
                                                    int cols) {
   __shared__ float red[8][32];
+  pdl_wait();
+  pdl_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   int n = (*rows_dev + 128 * per - 1) / (128 * per);
   n = (n < 1 ? 1 : n) * 4 * per;
   float s = 0.f;
   if (c < cols)
-    for (int j = warp; j < n; j += 8) s += dbp[(long long)j * ld + c];
+    for (int j = warp; j < n; j += 64) {
+      float p[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) p[k] = j + 8 * k < n ? dbp[(long long)(j + 8 * k) * ld + c] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += p[k];
+    }
   red[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < cols) {
@@ -834,24 +946,34 @@ bool make_map(CUtensorMap* m, int type, const void* base, long long inner, long 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch that may begin while the one before it on the stream ends: each
+// kernel waits for that (pdl_wait) before it touches memory, so only its set-up
+// overlaps.
+template <class... P, class... A>
+cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 template <int MODE, class T, bool AMN, bool BMN, int CG>
 cudaError_t launch_gemm_t(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& a, int blocks, cudaStream_t s) {
   constexpr auto kern = k_gemm<MODE, T, AMN, BMN, CG>;
   cudaError_t e = smem_optin<kern>(kSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CG;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = CG > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, ma, mb, a);
+  return launch(kern, dim3(blocks), kThreads, kSmem, s, CG, ma, mb, a);
 }
 
 template <int MODE, bool AMN, bool BMN>
@@ -893,12 +1015,20 @@ int group_of(int K, int cg) {
   return g < 1 ? 1 : g > (1 << 20) ? 1 << 20 : (int)g;
 }
 
+// The tensor cores truncate the float32 accumulator at every K = 16 step, so
+// a sum ends short of its value: each step loses half a unit of a partial sum
+// on average, and partial sums are half the final one on average.  Measured
+// for sums of K = 64 to 2048 products the relative loss is 0.26 (K / 16)
+// 2^-24, for logits of either sign and the large ones of targets alike; the
+// factor that scales the accumulator anyway puts it back.
+constexpr double kLog2ed = 1.4426950408889634;
+float factor_of(int K, double f) { return (float)(f * (1.0 + 0.26 * ((K + 15) / 16) * (1.0 / 16777216.0))); }
+
 bool rows_aligned(const void* p, long long ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
 
 cudaError_t copy_rows(const void* in, long long ldi, void* out, int ldo, long long n, int H, cudaStream_t s) {
   const long long b = (n + 7) / 8;
-  k_copy_rows<<<(unsigned)(b < 4864 ? b : 4864), 256, 0, s>>>((const u16*)in, ldi, (u16*)out, ldo, n, H);
-  return cudaGetLastError();
+  return launch(k_copy_rows, (unsigned)(b < 4864 ? b : 4864), 256, 0, s, 1, (const u16*)in, (long long)ldi, (u16*)out, ldo, n, H);
 }
 
 int check_types(int type, int param_type) {
@@ -999,9 +1129,9 @@ template <class T, int CG>
 cudaError_t launch_join_t(const GemmArgs& a, long long max_tiles, int workers, cudaStream_t s) {
   const int units = CG * 4 * ((a.bn + 63) / 64);
   const long long r = max_tiles < workers - 1 ? max_tiles : workers - 1;
-  if (r < 1) return cudaSuccess;
-  k_join<T, CG><<<dim3((unsigned)r, (units + 7) / 8), 256, 0, s>>>(a, workers);
-  return cudaGetLastError();
+  const long long depth = a.M > 0 ? a.rows : a.K;
+  if (r < 1 || depth <= 64 * (kSplitDepth - 1)) return cudaSuccess;  // nothing can be split
+  return launch(k_join<T, CG>, dim3((unsigned)r, units), 256, 0, s, 1, a, workers);
 }
 
 }  // namespace
@@ -1055,6 +1185,7 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   a.bias_type = bias_type;
   a.part = (float2*)(b + l.o_part);
   a.part_ld = l.Np;
+  a.factor = factor_of(H, kLog2ed);
   a.lse = (float*)(b + l.o_lse);
   a.out = out;
   a.ldo = ldo;
@@ -1071,8 +1202,8 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   c.part_ld = l.Np;
   c.slots = 2 * l.nt;
   c.lse = (float*)(b + l.o_lse);
-  k_combine<<<(unsigned)((N + 31) / 32), 256, 0, s>>>(c);
-  TRY(cudaGetLastError());
+  TRY(launch(k_combine, (unsigned)((N + 31) / 32), 32 * kSlices, 0, s, 1, c));
+  a.factor = factor_of(H, 1.0);
   TRY((launch_gemm<kLogp, false, false>(type, cg, ma, mb, a, blocks, s)));
   return CTCPB_OK;
 }
@@ -1111,9 +1242,11 @@ int ce_rows(int type, const void* x, int64_t ldx, const int32_t* targets, int64_
   r.status = &((Header*)b)->status;
   r.type = type;
   r.reduction = reduction;
-  const long long blocks = N > 0 ? (N + kRowBlock - 1) / kRowBlock : 1;
-  k_rows<<<(unsigned)blocks, 256, 0, s>>>(r);
-  TRY(cudaGetLastError());
+  r.dx_vec = r.dx && rows_aligned(r.dx, r.lddx) && H % 8 == 0;
+  long long per = up_to((N + kRowBlocks - 1) / kRowBlocks, 32);
+  if (per < 32) per = 32;
+  const long long blocks = N > 0 ? (N + per - 1) / per : 1;
+  TRY(launch(k_rows, (unsigned)blocks, 256, 0, s, 1, r, (int)per));
   return CTCPB_OK;
 }
 
@@ -1158,6 +1291,7 @@ int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, con
   a.bias = bias;
   a.bias_type = bias_type;
   a.tgt = r.tgt;
+  a.factor = factor_of(H, kLog2ed);
   a.zt = (float*)(b + l.o_zt);
   a.part = (float2*)(b + l.o_part);
   a.part_ld = l.Np;
@@ -1177,8 +1311,7 @@ int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, con
   c.reduction = reduction;
   c.sums = (float*)(b + l.o_sums);
   c.ticket = r.ticket;
-  k_combine<<<(unsigned)(l.Np / 32), 256, 0, s>>>(c);
-  TRY(cudaGetLastError());
+  TRY(launch(k_combine, (unsigned)(l.Np / 32), 32 * kSlices, 0, s, 1, c));
   return CTCPB_OK;
 }
 
@@ -1233,6 +1366,8 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
     a.tgt = r.tgt;
     a.lse = r.lse_c;
     a.rs = r.rs;
+    a.per_row = reduction == CTCPB_REDUCE_NONE;
+    a.factor = factor_of(H, kLog2ed);
     a.out = b + l.o_d;
     a.ldo = l.piece;
     a.dbp = dbias ? (float*)(b + l.o_dbp) : nullptr;
@@ -1240,9 +1375,8 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
     long long tiles = l.Np / 128 * ((cols + l.bn - 1) / l.bn);
     TRY((launch_gemm<kDlogits, false, false>(type, cg, ma, mb, a, (int)(tiles < sms ? tiles : sms), s)));
     if (dbias) {
-      k_bias_grad<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(a.dbp, l.piece, r.nv, cg, r.scale, dbias, bias_type, v0,
-                                                               cols);
-      TRY(cudaGetLastError());
+      TRY(launch(k_bias_grad, (unsigned)((cols + 31) / 32), 256, 0, s, 1, (const float*)a.dbp, (long long)l.piece,
+                 (const int*)r.nv, cg, (const float*)r.scale, dbias, bias_type, v0, cols));
     }
     if (dx && N > 0) {  // dx (+)= d w[piece]
       if (!make_map(&ma, type, b + l.o_d, l.piece, l.Np, l.piece, 128) || !make_map(&mb, type, weight, H, V, ldw, 64))

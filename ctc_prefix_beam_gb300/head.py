@@ -14,6 +14,7 @@ from PyTorch unless they are given.  Rows are frames: ``x`` is [..., H].
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -113,6 +114,7 @@ def _given(t: torch.Tensor, shape, dtype, device, what: str) -> torch.Tensor:
     return t
 
 
+@functools.lru_cache(maxsize=1024)
 def _size(name: str, *args) -> int:
     n = ctypes.c_size_t()
     D._check(_lib()[name](*args, ctypes.byref(n)), name[6:])
@@ -121,8 +123,24 @@ def _size(name: str, *args) -> int:
 
 def _workspace(ws, need: int, device):
     if ws is None:
-        ws = D._alloc(need, device)
+        return D._alloc(need, device), need
     return ws, D._check_buf(ws, need, device, "workspace")
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _run(dev: torch.device, what: str, *args):
+    """Call a library entry point on ``dev``'s current stream, ``dev`` current."""
+    fn = _lib()["ctcpb_" + what]
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if rc != D.OK:
+        raise D.CtcpbError(rc, what)
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, *,
@@ -135,14 +153,15 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     lead = x.shape[:-1]
     if outputs is None:
         y = torch.empty(x.shape, dtype=dt, device=dev)
-        mean, rstd = torch.empty((2, *lead), dtype=torch.float32, device=dev).unbind(0)
+        mean = torch.empty(lead, dtype=torch.float32, device=dev)
+        rstd = torch.empty(lead, dtype=torch.float32, device=dev)
     else:
         y, mean, rstd = outputs
         _given(y, x.shape, dt, dev, "y")
         _given(mean, lead, torch.float32, dev, "mean")
         _given(rstd, lead, torch.float32, dev, "rstd")
-    D._check(D._call(dev, _lib()["ctcpb_layer_norm"], _TYPES[dt], _TYPES[pt], D._ptr(xr), ldx, D._ptr(w), D._ptr(b),
-                     eps, N, H, D._ptr(y), H, D._ptr(mean), D._ptr(rstd), D._stream(dev)), "layer_norm")
+    _run(dev, "layer_norm", _TYPES[dt], _TYPES[pt], _p(xr), ldx, _p(w), _p(b),
+                     eps, N, H, _p(y), H, _p(mean), _p(rstd))
     return y, mean, rstd
 
 
@@ -168,11 +187,12 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
             raise ValueError(f"param_dtype must be {dt} or float32")
         pt = param_dtype
     dx = torch.empty(x.shape, dtype=dt, device=dev)
-    dw, db = torch.empty((2, H), dtype=pt, device=dev).unbind(0)
+    dw = torch.empty((H,), dtype=pt, device=dev)
+    db = torch.empty((H,), dtype=pt, device=dev)
     ws, nbytes = _workspace(workspace, layer_norm_workspace_size(N, H), dev)
-    D._check(D._call(dev, _lib()["ctcpb_layer_norm_backward"], _TYPES[dt], _TYPES[pt], D._ptr(dyr), lddy, D._ptr(xr),
-                     ldx, D._ptr(w), D._ptr(mean), D._ptr(rstd), N, H, D._ptr(dx), H, D._ptr(dw), D._ptr(db),
-                     D._ptr(ws), nbytes, D._stream(dev)), "layer_norm_backward")
+    _run(dev, "layer_norm_backward", _TYPES[dt], _TYPES[pt], _p(dyr), lddy, _p(xr),
+                     ldx, _p(w), _p(mean), _p(rstd), N, H, _p(dx), H, _p(dw), _p(db),
+                     _p(ws), nbytes)
     return dx, dw, db
 
 
@@ -206,8 +226,8 @@ def log_probs(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor
     if o is not out:
         raise ValueError("out's rows must lie at one stride, their labels contiguous")
     ws, nbytes = _workspace(workspace, log_probs_workspace_size(dt, N, V, H), dev)
-    D._check(D._call(dev, _lib()["ctcpb_log_probs"], _TYPES[dt], _TYPES[bt], D._ptr(xr), ldx, D._ptr(w), _ld(w),
-                     D._ptr(b), N, V, H, D._ptr(out), ldo, D._ptr(ws), nbytes, D._stream(dev)), "log_probs")
+    _run(dev, "log_probs", _TYPES[dt], _TYPES[bt], _p(xr), ldx, _p(w), _ld(w),
+                     _p(b), N, V, H, _p(out), ldo, _p(ws), nbytes)
     return out
 
 
@@ -241,9 +261,8 @@ def cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, 
     loss = torch.empty(lead if red == NONE else (), dtype=torch.float32, device=dev)
     lse = torch.empty(lead, dtype=torch.float32, device=dev)
     ws, nbytes = _workspace(workspace, cross_entropy_workspace_size(dt, N, V, H, False), dev)
-    D._check(D._call(dev, _lib()["ctcpb_cross_entropy"], _TYPES[dt], _TYPES[bt], D._ptr(xr), ldx, D._ptr(w), _ld(w),
-                     D._ptr(b), D._ptr(t), N, V, H, ignore_index, red, D._ptr(loss), D._ptr(lse), D._ptr(ws), nbytes,
-                     D._stream(dev)), "cross_entropy")
+    _run(dev, "cross_entropy", _TYPES[dt], _TYPES[bt], _p(xr), ldx, _p(w), _ld(w),
+                     _p(b), _p(t), N, V, H, ignore_index, red, _p(loss), _p(lse), _p(ws), nbytes)
     return loss, lse
 
 
@@ -262,7 +281,7 @@ def cross_entropy_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Te
     dw = torch.empty((V, H), dtype=dt, device=dev)
     db = torch.empty((V,), dtype=bt, device=dev) if bias is not None else None
     ws, nbytes = _workspace(workspace, cross_entropy_workspace_size(dt, N, V, H, True), dev)
-    D._check(D._call(dev, _lib()["ctcpb_cross_entropy_backward"], _TYPES[dt], _TYPES[bt], D._ptr(grad), D._ptr(xr), ldx,
-                     D._ptr(w), _ld(w), D._ptr(b), D._ptr(t), D._ptr(lse), N, V, H, ignore_index, red, D._ptr(dx), H,
-                     D._ptr(dw), H, D._ptr(db), D._ptr(ws), nbytes, D._stream(dev)), "cross_entropy_backward")
+    _run(dev, "cross_entropy_backward", _TYPES[dt], _TYPES[bt], _p(grad), _p(xr), ldx,
+                     _p(w), _ld(w), _p(b), _p(t), _p(lse), N, V, H, ignore_index, red, _p(dx), H,
+                     _p(dw), H, _p(db), _p(ws), nbytes)
     return dx, dw, db
