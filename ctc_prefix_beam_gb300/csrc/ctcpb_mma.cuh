@@ -11,6 +11,44 @@
 
 namespace ctcpb {
 
+// ---------------------------------------------------------------- pairs
+
+// Two float32 operations in one instruction, on a pair of values.
+__device__ __forceinline__ u64 pair(float x, float y) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(float& x, float& y, u64 r) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r)); }
+__device__ __forceinline__ float pair_sum(u64 r) {
+  float x, y;
+  unpair(x, y, r);
+  return x + y;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// (x, y) = (x, y) * f + (bx, by)
+__device__ __forceinline__ void fma2(float& x, float& y, float f, float bx, float by) {
+  unpair(x, y, fma2(pair(x, y), pair(f, f), pair(bx, by)));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float bx, float by) {
+  unpair(x, y, add2(pair(x, y), pair(bx, by)));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float b) { add2(x, y, b, b); }
+
 // ---------------------------------------------------------------- element types
 
 template <class T>
@@ -25,6 +63,9 @@ struct Elem<__nv_bfloat16> {
   static constexpr u32 kFormat = 1;  // operand format code of a 16-bit matrix instruction
   static __device__ __forceinline__ float to(__nv_bfloat16 v) { return __bfloat162float(v); }
   static __device__ __forceinline__ __nv_bfloat16 from(float v) { return __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ u64 unpack(u32 q) {
+    return pair(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u));
+  }
   static __device__ __forceinline__ u32 pack(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const u32*>(&v);
@@ -35,6 +76,10 @@ struct Elem<__half> {
   static constexpr u32 kFormat = 0;
   static __device__ __forceinline__ float to(__half v) { return __half2float(v); }
   static __device__ __forceinline__ __half from(float v) { return __float2half_rn(v); }
+  static __device__ __forceinline__ u64 unpack(u32 q) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&q));
+    return pair(f.x, f.y);
+  }
   static __device__ __forceinline__ u32 pack(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const u32*>(&v);
@@ -65,26 +110,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-// Two float32 operations in one instruction.
-__device__ __forceinline__ u64 pair(float x, float y) {
-  u64 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void unpair(float& x, float& y, u64 r) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r)); }
-// (x, y) = (x, y) * f + (bx, by)
-__device__ __forceinline__ void fma2(float& x, float& y, float f, float bx, float by) {
-  u64 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(x, y)), "l"(pair(f, f)), "l"(pair(bx, by)));
-  unpair(x, y, r);
-}
-__device__ __forceinline__ void add2(float& x, float& y, float bx, float by) {
-  u64 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(x, y)), "l"(pair(bx, by)));
-  unpair(x, y, r);
-}
-__device__ __forceinline__ void add2(float& x, float& y, float b) { add2(x, y, b, b); }
 
 // Programmatic launches: wait for the launch before this one on the stream to
 // be done, its writes visible; let the next one's blocks begin their set-up.

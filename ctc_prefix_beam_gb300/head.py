@@ -61,7 +61,10 @@ def _rows(t: torch.Tensor, what: str, dtype=None):
         raise ValueError(f"{what} must be a CUDA float32, bfloat16 or float16 tensor [..., H]")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}")
-    if not (t.is_contiguous() or (t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1])):
+    if t.is_contiguous():
+        H = t.shape[-1]
+        return t, t.numel() // H if H else 0, H, H
+    if not (t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]):
         H = t.shape[-1]
         ld = t.stride(-2) if t.dim() > 1 else H
         n = 1
@@ -131,16 +134,27 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _raw_stream(dev: torch.device) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# the same without building a Stream object, where this PyTorch has it
+_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw is not None:
+    def _raw_stream(dev: torch.device) -> int:  # noqa: F811
+        return _raw(dev.index)
+
+
 def _run(dev: torch.device, what: str, *args):
     """Call a library entry point on ``dev``'s current stream, ``dev`` current."""
-    fn = _lib()["ctcpb_" + what]
+    fn = _lib()[what]
     if dev.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        rc = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            rc = fn(*args, _raw_stream(dev))
     if rc != D.OK:
-        raise D.CtcpbError(rc, what)
+        raise D.CtcpbError(rc, what[6:])
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, *,
@@ -160,8 +174,8 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         _given(y, x.shape, dt, dev, "y")
         _given(mean, lead, torch.float32, dev, "mean")
         _given(rstd, lead, torch.float32, dev, "rstd")
-    _run(dev, "layer_norm", _TYPES[dt], _TYPES[pt], _p(xr), ldx, _p(w), _p(b),
-                     eps, N, H, _p(y), H, _p(mean), _p(rstd))
+    _run(dev, "ctcpb_layer_norm", _TYPES[dt], _TYPES[pt], _p(xr), ldx, _p(w), _p(b), eps, N, H, _p(y), H, _p(mean),
+         _p(rstd))
     return y, mean, rstd
 
 
@@ -190,9 +204,8 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     dw = torch.empty((H,), dtype=pt, device=dev)
     db = torch.empty((H,), dtype=pt, device=dev)
     ws, nbytes = _workspace(workspace, layer_norm_workspace_size(N, H), dev)
-    _run(dev, "layer_norm_backward", _TYPES[dt], _TYPES[pt], _p(dyr), lddy, _p(xr),
-                     ldx, _p(w), _p(mean), _p(rstd), N, H, _p(dx), H, _p(dw), _p(db),
-                     _p(ws), nbytes)
+    _run(dev, "ctcpb_layer_norm_backward", _TYPES[dt], _TYPES[pt], _p(dyr), lddy, _p(xr), ldx, _p(w), _p(mean),
+         _p(rstd), N, H, _p(dx), H, _p(dw), _p(db), _p(ws), nbytes)
     return dx, dw, db
 
 
@@ -226,8 +239,8 @@ def log_probs(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor
     if o is not out:
         raise ValueError("out's rows must lie at one stride, their labels contiguous")
     ws, nbytes = _workspace(workspace, log_probs_workspace_size(dt, N, V, H), dev)
-    _run(dev, "log_probs", _TYPES[dt], _TYPES[bt], _p(xr), ldx, _p(w), _ld(w),
-                     _p(b), N, V, H, _p(out), ldo, _p(ws), nbytes)
+    _run(dev, "ctcpb_log_probs", _TYPES[dt], _TYPES[bt], _p(xr), ldx, _p(w), _ld(w), _p(b), N, V, H, _p(out), ldo,
+         _p(ws), nbytes)
     return out
 
 
@@ -261,8 +274,8 @@ def cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, 
     loss = torch.empty(lead if red == NONE else (), dtype=torch.float32, device=dev)
     lse = torch.empty(lead, dtype=torch.float32, device=dev)
     ws, nbytes = _workspace(workspace, cross_entropy_workspace_size(dt, N, V, H, False), dev)
-    _run(dev, "cross_entropy", _TYPES[dt], _TYPES[bt], _p(xr), ldx, _p(w), _ld(w),
-                     _p(b), _p(t), N, V, H, ignore_index, red, _p(loss), _p(lse), _p(ws), nbytes)
+    _run(dev, "ctcpb_cross_entropy", _TYPES[dt], _TYPES[bt], _p(xr), ldx, _p(w), _ld(w), _p(b), _p(t), N, V, H,
+         ignore_index, red, _p(loss), _p(lse), _p(ws), nbytes)
     return loss, lse
 
 
@@ -281,7 +294,6 @@ def cross_entropy_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Te
     dw = torch.empty((V, H), dtype=dt, device=dev)
     db = torch.empty((V,), dtype=bt, device=dev) if bias is not None else None
     ws, nbytes = _workspace(workspace, cross_entropy_workspace_size(dt, N, V, H, True), dev)
-    _run(dev, "cross_entropy_backward", _TYPES[dt], _TYPES[bt], _p(grad), _p(xr), ldx,
-                     _p(w), _ld(w), _p(b), _p(t), _p(lse), N, V, H, ignore_index, red, _p(dx), H,
-                     _p(dw), H, _p(db), _p(ws), nbytes)
+    _run(dev, "ctcpb_cross_entropy_backward", _TYPES[dt], _TYPES[bt], _p(grad), _p(xr), ldx, _p(w), _ld(w), _p(b),
+         _p(t), _p(lse), N, V, H, ignore_index, red, _p(dx), H, _p(dw), H, _p(db), _p(ws), nbytes)
     return dx, dw, db
