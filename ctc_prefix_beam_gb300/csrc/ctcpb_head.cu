@@ -23,14 +23,19 @@ namespace {
 
 enum Mode { kStats = 0, kLogp = 1, kDlogits = 2, kProduct = 3 };
 
-constexpr int kThreads = 384;      // 4 control warps, 8 epilogue warps
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;      // 4 for each quarter of a tile's 256 columns
+constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kMaxStages = 8;
-constexpr int kTileBytes = 196608;  // operand stages
-constexpr int kStageBuf = 4096;     // per epilogue warp: 32 rows of 128 bytes
-constexpr int kSmem = kTileBytes + kEpiWarps * (kStageBuf + 64 * 4) + 256;
+constexpr int kTileBytes = 196608;  // operand tiles
+constexpr int kStageBuf = 2048;     // per epilogue warp: 32 rows of 64 bytes
+constexpr int kEpiBytes = kEpiWarps * (kStageBuf + 32 * 4);  // ... and 32 biases
+constexpr int kCtlBytes = 512;      // barriers, the tensor-memory address, the give-up flag
+constexpr int kSmem = kTileBytes + kEpiBytes + kCtlBytes;
 constexpr u32 kTmemCols = 512;
-constexpr int kSplitDepth = 8;     // slices of 64 below which a tile is never split along K
+constexpr int kSplitDepth = 8;      // slices of 64 below which a tile is never split along K
+
+// Partial (max, sum) pairs a row has for each column tile: one for each 64 columns.
+__host__ __device__ constexpr int part_slots(int bn) { return (bn + 63) / 64; }
 
 struct GemmArgs {
   const int* rows_dev;  // number of rows, on the device (null: `rows`)
@@ -71,7 +76,7 @@ struct GemmArgs {
 // A worker (block or pair) takes whole tiles in waves; the last wave, if it
 // would leave workers idle, is cut along K into equal shares instead.  A share
 // is at most one tile's depth, so it touches at most two tiles; its sums go to
-// slots 2w, 2w+1, and k_join adds a tile's shares in order.
+// slots 2w, 2w+1, and k_finish adds a tile's shares in order.
 struct Seg {
   int m, n, tile, k0, k1, slot;  // slot -1: the whole depth
 };
@@ -140,43 +145,33 @@ struct Sched {
 
 // ---------------------------------------------------------------- writing rows through shared memory
 //
-// A thread holds 32 columns of its own row.  The warp puts them into a 4 KB
-// buffer of 32 rows x 128 bytes, its 16-byte chunks permuted by row & 7 so
-// that neither side has bank conflicts, and then writes whole row pieces.
+// A thread holds 32 columns of its own row.  The warp puts 64 bytes of each row
+// into a 2 KB buffer, its 16-byte chunks permuted by (row / 2) & 3 so that
+// neither side has bank conflicts, and then writes whole row pieces.
 
-__device__ __forceinline__ u32 stage_at(int row, int chunk) { return (u32)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
+__device__ __forceinline__ u32 stage_at(int row, int chunk) { return (u32)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4)); }
 
-__device__ __forceinline__ void stage_f32(char* buf, int lane, const float (&v)[32]) {
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<float4*>(buf + stage_at(lane, c)) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-}
 template <class T>
 __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(Elem<T>::pack(v[0], v[1]), Elem<T>::pack(v[2], v[3]), Elem<T>::pack(v[4], v[5]),
                     Elem<T>::pack(v[6], v[7]));
 }
-template <class T>
-__device__ __forceinline__ void stage_16(char* buf, int lane, const float (&v)[32], int half) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(buf + stage_at(lane, 4 * half + c)) = pack8<T>(v + 8 * c);
-}
-// Write the buffer's rows (E: float for 32 columns, 16-bit for 64) to columns
-// [c0, cols) of output rows; orow is this lane's output row, -1 for none.
+// Write the buffer's rows (64 / sizeof(E) columns from c0 on, those below
+// `cols`) to the output; orow is this lane's output row, -1 for none.
 template <class E>
-__device__ __forceinline__ void flush_rows(const char* buf, int lane, E* out, long long ldo, long long orow, int c0,
-                                           int cols, bool vec) {
-  constexpr int per = 16 / (int)sizeof(E);  // elements of a chunk
+__device__ __forceinline__ void flush_rows(const char* buf, int lane, E* out, long long ldo, int orow, int c0, int cols,
+                                           bool vec) {
+  constexpr int per = 16 / (int)sizeof(E), width = 64 / (int)sizeof(E);  // elements of a chunk, of a row piece
   __syncwarp();
   if (vec) {
+    const int c = lane & 3, col = c0 + c * per;
 #pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      const int row = it * 4 + (lane >> 3), c = lane & 7;
-      const long long r = __shfl_sync(0xffffffffu, orow, row);
+    for (int it = 0; it < 4; ++it) {
+      const int row = it * 8 + (lane >> 2);
+      const int r = __shfl_sync(0xffffffffu, orow, row);
       const uint4 p = *reinterpret_cast<const uint4*>(buf + stage_at(row, c));
-      const int col = c0 + c * per;
       if (r >= 0 && col < cols) {
-        E* o = out + r * ldo + col;
+        E* const o = out + (long long)r * ldo + col;
         if (col + per <= cols) {
           *reinterpret_cast<uint4*>(o) = p;
         } else {
@@ -188,17 +183,36 @@ __device__ __forceinline__ void flush_rows(const char* buf, int lane, E* out, lo
       }
     }
   } else {
-    for (int row = 0; row < 32; ++row) {
-      const long long r = __shfl_sync(0xffffffffu, orow, row);
-      if (r < 0) continue;
-#pragma unroll
-      for (int c = lane; c < 8 * per; c += 32) {
-        const E e = *reinterpret_cast<const E*>(buf + stage_at(row, c / per) + (c % per) * (int)sizeof(E));
-        if (c0 + c < cols) out[r * ldo + c0 + c] = e;
-      }
+    constexpr int rows = 32 / width;  // rows a warp writes at once
+    const int c = lane % width;
+#pragma unroll 4
+    for (int it = 0; it < 32; it += rows) {
+      const int row = it + lane / width;
+      const int r = __shfl_sync(0xffffffffu, orow, row);
+      const E e = *reinterpret_cast<const E*>(buf + stage_at(row, c / per) + (c % per) * (int)sizeof(E));
+      if (r >= 0 && c0 + c < cols) out[(long long)r * ldo + c0 + c] = e;
     }
   }
   __syncwarp();
+}
+// 32 columns of a thread's row to the output
+__device__ __forceinline__ void write_f32(char* buf, int lane, const float (&v)[32], float* out, long long ldo, int orow,
+                                          int c0, int cols, bool vec) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<float4*>(buf + stage_at(lane, c)) =
+          make_float4(v[16 * h + 4 * c], v[16 * h + 4 * c + 1], v[16 * h + 4 * c + 2], v[16 * h + 4 * c + 3]);
+    flush_rows<float>(buf, lane, out, ldo, orow, c0 + 16 * h, cols, vec);
+  }
+}
+template <class T>
+__device__ __forceinline__ void write_16(char* buf, int lane, const float (&v)[32], T* out, long long ldo, int orow, int c0,
+                                         int cols, bool vec) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(buf + stage_at(lane, c)) = pack8<T>(v + 8 * c);
+  flush_rows<T>(buf, lane, out, ldo, orow, c0, cols, vec);
 }
 
 // Sum of column l over the warp's rows, in lane l: at each halving a lane
@@ -218,21 +232,23 @@ __device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
 
 // ---------------------------------------------------------------- the matrix kernel
 
+// Shared memory: a ring of operand tiles, the epilogue warps' buffers, the
+// barriers.
 template <int MODE, class T, bool AMN, bool BMN, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const GemmArgs a) {
   extern __shared__ __align__(1024) char smem[];
-  char* const ctl = smem + kTileBytes + kEpiWarps * (kStageBuf + 64 * 4);
+  char* const ctl = smem + kTileBytes + kEpiBytes;
   const u32 s_tiles = saddr(smem);
   const u32 s_full = saddr(ctl), s_empty = s_full + 8 * kMaxStages, s_tfull = s_empty + 8 * kMaxStages,
             s_tempty = s_tfull + 16, s_tptr = s_tempty + 16;
-  volatile u32* const tmem_ptr = reinterpret_cast<volatile u32*>(ctl + 16 * kMaxStages + 32);
+  volatile u32* const tmem_ptr = reinterpret_cast<volatile u32*>(ctl + (s_tptr - s_full));
   volatile u32* const dead = tmem_ptr + 1;
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const u32 rank = CG == 2 ? cluster_rank() : 0;
   const int worker = (int)blockIdx.x / CG, workers = (int)gridDim.x / CG;
-  const int bnb = a.bn / CG;                              // columns of B this block loads
+  const int bnb = a.bn / CG;  // columns of B this block loads
   const u32 stage_bytes = 16384u + (u32)bnb * 128u;
 
   if (threadIdx.x == 0) {
@@ -264,9 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // bounded wait; false once any wait of the block has given up
   auto wait = [&](u32 bar, u32 parity) -> bool {
-    if (*dead) return false;
-    for (long long i = 0; i < kWaitSpins; ++i)
-      if (mbar_test_cluster(bar, parity)) return true;
+    if (mbar_test_at(bar, parity)) return true;
+    for (long long i = 0; i < kWaitSpins && !*dead; ++i)
+      if (mbar_test_at(bar, parity)) return true;
     *dead = 1;
     return false;
   };
@@ -312,22 +328,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       u32 ph = 0, aph = 1;
       const u32 idesc = mma_idesc(Elem<T>::kFormat, AMN, BMN, 128 * CG, a.bn);
       constexpr u64 kStepA = AMN ? 2048 >> 4 : 32 >> 4, kStepB = BMN ? 2048 >> 4 : 32 >> 4;
-      while (ok && sc.next(sg)) {
+      bool more = sc.next(sg);
+      while (more) {
         if (!(ok = wait(s_tempty + 8 * as, aph))) break;
         tc_fence_after();
         const u32 d = tmem + 256u * as;
-        for (int k = sg.k0; k < sg.k1; ++k) {
+        const int k0 = sg.k0, k1 = sg.k1;
+        for (int k = k0; k < k1; ++k) {
           if (!(ok = wait(s_full + 8 * st, ph))) break;
           tc_fence_after();
           const u32 at = s_tiles + (u32)st * stage_bytes;
           const u64 da = smem_desc(at, AMN ? 8192 : 16), db = smem_desc(at + 16384u, BMN ? 8192 : 16);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma_f16<CG>(d, da + i * kStepA, db + i * kStepB, idesc, k > sg.k0 || i > 0);
+          for (int i = 0; i < 4; ++i) mma_f16<CG>(d, da + i * kStepA, db + i * kStepB, idesc, k > k0 || i > 0);
           mma_commit<CG>(s_empty + 8 * st);
           if (++st == a.stages) {
             st = 0;
             ph ^= 1;
           }
+          if (k == k0) more = sc.next(sg);  // found while the tensor cores are busy
         }
         if (!ok) break;
         mma_commit<CG>(s_tfull + 8 * as);
@@ -338,10 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {  // ---- epilogue
-    const int q = warp & 3, half = (warp - 4) >> 2;
+  } else if (warp >= 4) {  // ---- epilogue: a warp's 32 rows and 64 columns of a tile
+    const int q = warp & 3, u = ((warp - 4) >> 2) * 64;
     char* const buf = smem + kTileBytes + (warp - 4) * kStageBuf;
-    float* const bias_s = reinterpret_cast<float*>(smem + kTileBytes + kEpiWarps * kStageBuf) + (warp - 4) * 64;
+    float* const bias_s = reinterpret_cast<float*>(smem + kTileBytes + kEpiWarps * kStageBuf) + (warp - 4) * 32;
     const u32 tempty0 = CG == 2 ? cluster_addr(s_tempty, 0) : s_tempty;
     const int rows = a.rows_dev ? *a.rows_dev : a.rows;
     const int mrows = a.M > 0 ? a.M : rows;
@@ -350,26 +369,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && sc.next(sg)) {
       const int mtile = sg.m * CG + (int)rank;
       const int row = mtile * 128 + q * 32 + lane, n0 = sg.n * a.bn;
+      // the columns that this tile writes end here (kDlogits fills its piece's width)
+      const int lim = MODE == kDlogits ? (int)a.ldo - n0 : a.N - n0;
+      const bool busy = u < a.bn && u < lim;
       float bm = -INFINITY, bs = 0.f;  // running max and sum of the row
-      float lse = 0.f, rs = 0.f;
-      int tgt = -1;
-      long long orow = row < mrows ? row : -1;
-      float bq[4];  // the biases of this warp's columns, two per unit of 64
+      float lse = 0.f, rs = 0.f, bq[2] = {0.f, 0.f};
+      int tgt = -1, orow = row < mrows ? row : -1;
       if constexpr (MODE != kProduct) {
-        // a column past the vocabulary gets -inf, so that its exponential is 0
+        if (busy) {
+          // a column past the vocabulary gets -inf, so that its exponential is 0
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = n0 + half * 64 + (i >> 1) * 128 + (i & 1) * 32 + lane;
-          bq[i] = col < a.N ? (a.bias ? load_elem(a.bias, a.bias_type, (long long)a.col0 + col) * (MODE == kLogp ? 1.f : kLog2e) : 0.f)
-                            : -INFINITY;
-        }
-        if (row < mrows) {
-          if (a.tgt) tgt = a.tgt[row] - a.col0 - n0;
-          if (MODE == kLogp) lse = a.lse[row];
-          if (MODE == kDlogits) {
-            // d = exp(z - lse) r: a factor r that all rows share is in the exponent
-            rs = a.rs[row];
-            lse = __fmaf_rn(a.lse[row], kLog2e, a.per_row ? 0.f : -log2f(rs));
+          for (int i = 0; i < 2; ++i) {
+            const int col = n0 + u + 32 * i + lane;
+            bq[i] = col < a.N ? (a.bias ? load_elem(a.bias, a.bias_type, (long long)a.col0 + col) * (MODE == kLogp ? 1.f : kLog2e)
+                                        : 0.f)
+                              : -INFINITY;
+          }
+          if (row < mrows) {
+            if (a.tgt) tgt = a.tgt[row] - a.col0 - n0;
+            if (MODE == kLogp) lse = a.lse[row];
+            if (MODE == kDlogits) {
+              // d = exp(z - lse) r: a factor r that all rows share is in the exponent
+              rs = a.rs[row];
+              lse = __fmaf_rn(a.lse[row], kLog2e, a.per_row ? 0.f : -log2f(rs));
+            }
           }
         }
       } else if (a.rowmap && orow >= 0) {
@@ -378,16 +401,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = __all_sync(0xffffffffu, wait(s_tfull + 8 * as, aph)))) break;
       tc_fence_after();
       const u32 d = tmem + 256u * as + ((u32)(q * 32) << 16);
-      // 32 columns of the row, from c0 on (the j-th half of a unit of 64)
-      auto chunk = [&](float(&v)[32], int c0, int j) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c0 = u + 32 * j;
+        if (!busy || c0 >= lim) break;
+        float v[32];
+        if (c0 < a.bn) {
+          tmem_load32(v, d + c0);
+          if constexpr (MODE != kProduct) {
+            bias_s[lane] = bq[j];
+            __syncwarp();
+          }
+          tmem_wait(v);
+        } else {  // kDlogits, a tile of 32 columns: zeros fill the piece
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
         if constexpr (MODE != kProduct) {
           // to base 2 (but for kLogp), so that exp and log cost nothing more: z log2(e) + b log2(e)
-          const float4* b4 = reinterpret_cast<const float4*>(bias_s + 32 * j);
+          if (c0 < a.bn) {
+            const float4* b4 = reinterpret_cast<const float4*>(bias_s);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 b = b4[i];
-            fma2(v[4 * i], v[4 * i + 1], a.factor, b.x, b.y);
-            fma2(v[4 * i + 2], v[4 * i + 3], a.factor, b.z, b.w);
+            for (int i = 0; i < 8; ++i) {
+              const float4 b = b4[i];
+              fma2(v[4 * i], v[4 * i + 1], a.factor, b.x, b.y);
+              fma2(v[4 * i + 2], v[4 * i + 3], a.factor, b.z, b.w);
+            }
           }
         }
         if constexpr (MODE == kStats) {
@@ -420,42 +459,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if constexpr (MODE == kLogp) {
 #pragma unroll
           for (int i = 0; i < 32; i += 2) add2(v[i], v[i + 1], -lse);
-          stage_f32(buf, lane, v);
-          flush_rows<float>(buf, lane, (float*)a.out, a.ldo, orow, n0 + c0, a.N, a.vec);
+          write_f32(buf, lane, v, (float*)a.out, a.ldo, orow, n0 + c0, a.N, a.vec);
         } else if constexpr (MODE == kDlogits) {
+          if (c0 < a.bn) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            add2(v[i], v[i + 1], -lse);
-            v[i] = ex2(v[i]);
-            v[i + 1] = ex2(v[i + 1]);
-          }
-          const int tr = tgt - c0;
-          if (__any_sync(0xffffffffu, (u32)tr < 32u)) {
-            const float one = a.per_row ? 1.f : rs;
+            for (int i = 0; i < 32; i += 2) {
+              add2(v[i], v[i + 1], -lse);
+              v[i] = ex2(v[i]);
+              v[i + 1] = ex2(v[i + 1]);
+            }
+            const int tr = tgt - c0;
+            if (__any_sync(0xffffffffu, (u32)tr < 32u)) {
+              const float one = a.per_row ? 1.f : rs;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] -= tr == i ? one : 0.f;
-          }
-          if (a.per_row) {
+              for (int i = 0; i < 32; ++i) v[i] -= tr == i ? one : 0.f;
+            }
+            if (a.per_row) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= rs;
-          }
-          if (__any_sync(0xffffffffu, row >= mrows)) {  // rows past the last one are exact zeros (their z may hold anything)
+              for (int i = 0; i < 32; ++i) v[i] *= rs;
+            }
+            if (__any_sync(0xffffffffu, row >= mrows)) {  // rows past the last one are exact zeros (their z may hold anything)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = row < mrows ? v[i] : 0.f;
+              for (int i = 0; i < 32; ++i) v[i] = row < mrows ? v[i] : 0.f;
+            }
           }
-          stage_16<T>(buf, lane, v, j);
+          write_16<T>(buf, lane, v, (T*)a.out, a.ldo, row, n0 + c0, (int)a.ldo, true);
           if (a.dbp) {
             const float cs = column_sums(v, lane);
-            if (n0 + c0 + lane < a.ldo) a.dbp[((long long)mtile * 4 + q) * a.ldo + n0 + c0 + lane] = cs;
+            if (c0 + lane < lim) a.dbp[((long long)mtile * 4 + q) * a.ldo + n0 + c0 + lane] = cs;
           }
         } else {
+          const long long at = (long long)c0 * 128 + q * 32 + lane, tile = 128ll * a.bn;
           if (sg.slot >= 0) {  // a share of the depth: to its slot, a column's rows side by side
-            float* o = a.slots + ((long long)sg.slot * CG + rank) * 128 * a.bn + (long long)c0 * 128 + q * 32 + lane;
+            float* o = a.slots + ((long long)sg.slot * CG + rank) * tile + at;
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i * 128] = v[i];
           } else {
             if (a.acc) {
-              float* o = a.acc + ((long long)sg.tile * CG + rank) * 128 * a.bn + (long long)c0 * 128 + q * 32 + lane;
+              float* o = a.acc + ((long long)sg.tile * CG + rank) * tile + at;
               if (!a.first) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] += o[i * 128];
@@ -469,45 +510,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float f = *a.scale;
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] *= f;
-              stage_16<T>(buf, lane, v, j);
+              write_16<T>(buf, lane, v, (T*)a.out, a.ldo, orow, n0 + c0, a.N, a.vec);
             }
           }
         }
-      };
-      // units of 64 columns, every other one to each half of the warps; a
-      // chunk's loads from tensor memory are in flight while the one before
-      // it is worked on
-      const int lim = MODE == kDlogits ? (int)a.ldo - n0 : a.N - n0, end = a.bn < lim ? a.bn : lim;
-      float v0[32], v1[32];
-      if (half * 64 < end) tmem_load32(v0, d + half * 64);
-      for (int u = half * 64; u < end; u += 128) {
-        if constexpr (MODE != kProduct) {
-          __syncwarp();
-          bias_s[lane] = u < 128 ? bq[0] : bq[2];
-          bias_s[lane + 32] = u < 128 ? bq[1] : bq[3];
-          __syncwarp();
-        }
-        const bool two = u + 32 < a.bn;  // a tile of 32 columns has no second half
-        tmem_wait(v0);
-        if (two) tmem_load32(v1, d + u + 32);
-        chunk(v0, u, 0);
-        if (two) {
-          tmem_wait(v1);
-          if (u + 128 < end) tmem_load32(v0, d + u + 128);
-          chunk(v1, u + 32, 1);
-        } else if constexpr (MODE == kDlogits) {  // zeros fill the unit
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v1[i] = 0.f;
-          stage_16<T>(buf, lane, v1, 1);
-        }
-        if constexpr (MODE == kDlogits)
-          flush_rows<T>(buf, lane, (T*)a.out, a.ldo, (long long)row, n0 + u, (int)a.ldo, true);
-        if constexpr (MODE == kProduct) {
-          if (sg.slot < 0 && a.last) flush_rows<T>(buf, lane, (T*)a.out, a.ldo, orow, n0 + u, a.N, a.vec);
-        }
+        __syncwarp();
       }
       if constexpr (MODE == kStats)
-        if (row < mrows) a.part[((long long)sg.n * 2 + half) * a.part_ld + row] = make_float2(bm, bs);
+        if (u < a.bn && row < mrows) a.part[((long long)sg.n * part_slots(a.bn) + u / 64) * a.part_ld + row] = make_float2(bm, bs);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * as);
@@ -533,17 +543,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) tmem_dealloc<CG>(tmem, kTmemCols);
 }
 
-// The shares of every tile of the split wave, added in the order of K, and the
+// ---------------------------------------------------------------- what is left after the products
+
+// The shares of a tile of the split wave, added in the order of K, and the
 // tile's output written: a block per 32 rows and 64 columns, 8 columns a warp
 // (16 bytes of each row), two shares' loads in flight.
-template <class T, int CG>
-__global__ void __launch_bounds__(256) k_join(const GemmArgs a, int workers) {
-  __shared__ __align__(16) char buf[kStageBuf];
-  pdl_wait();
+template <class T>
+__device__ void join_tile(const GemmArgs& a, int cg, int workers, int r, int unit, char* buf) {
   Sched sc;
-  sc.init(a, CG, 0, workers);
+  sc.init(a, cg, 0, workers);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.x, unit = blockIdx.y;
   if (r >= sc.rem) return;
   const int lo = r * sc.ks, hi = lo + sc.ks;
   int w = (int)((long long)lo * sc.nw / ((long long)sc.rem * sc.ks));
@@ -552,7 +561,7 @@ __global__ void __launch_bounds__(256) k_join(const GemmArgs a, int workers) {
   if (sc.share(w) <= lo && sc.share(w + 1) >= hi) return;  // one share: written by the matrix kernel
   Seg sg;
   sc.place(sc.dp + r, sg);
-  const int q = unit & 3, rank = (unit >> 2) % CG, u = (unit >> 2) / CG * 64;
+  const int q = unit & 3, rank = (unit >> 2) % cg, u = (unit >> 2) / cg * 64;
   const int n0 = sg.n * a.bn;
   if (n0 + u >= a.N) return;
   const int rows = a.rows_dev ? *a.rows_dev : a.rows;
@@ -562,7 +571,7 @@ __global__ void __launch_bounds__(256) k_join(const GemmArgs a, int workers) {
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  auto slot_of = [&](int x) { return a.slots + ((2ll * x + (r - sc.share(x) / sc.ks)) * CG + rank) * tile + at; };
+  auto slot_of = [&](int x) { return a.slots + ((2ll * x + (r - sc.share(x) / sc.ks)) * cg + rank) * tile + at; };
   for (int x = w; x < sc.nw && sc.share(x) < hi; x += 2) {
     const bool two = x + 1 < sc.nw && sc.share(x + 1) < hi;
     const float *o = slot_of(x), *p = two ? slot_of(x + 1) : o;
@@ -575,7 +584,7 @@ __global__ void __launch_bounds__(256) k_join(const GemmArgs a, int workers) {
     for (int i = 0; i < 8; ++i) v[i] = (v[i] + e[i]) + f[i];
   }
   if (a.acc) {
-    float* o = a.acc + ((long long)sg.tile * CG + rank) * tile + at;
+    float* o = a.acc + ((long long)sg.tile * cg + rank) * tile + at;
     if (!a.first) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += o[i * 128];
@@ -589,17 +598,18 @@ __global__ void __launch_bounds__(256) k_join(const GemmArgs a, int workers) {
   const float f = *a.scale;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] *= f;
-  *reinterpret_cast<uint4*>(buf + stage_at(lane, warp)) = pack8<T>(v);
+  // 32 rows of 128 bytes, the 16-byte chunks permuted by the row
+  *reinterpret_cast<uint4*>(buf + lane * 128 + ((warp ^ (lane & 7)) << 4)) = pack8<T>(v);
   __syncthreads();
   // four rows a warp
   T* const out = (T*)a.out;
   const int rr = warp * 4 + (lane >> 3);
-  const int mine = (sg.m * CG + rank) * 128 + q * 32 + rr;
+  const int mine = (sg.m * cg + rank) * 128 + q * 32 + rr;
   if (mine >= mrows) return;
   const long long orow = a.rowmap ? a.rowmap[mine] : mine;
   if (a.vec) {
     const int col = n0 + u + (lane & 7) * 8;
-    const uint4 p = *reinterpret_cast<const uint4*>(buf + stage_at(rr, lane & 7));
+    const uint4 p = *reinterpret_cast<const uint4*>(buf + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
     if (col + 8 <= a.N) {
       *reinterpret_cast<uint4*>(out + orow * a.ldo + col) = p;
     } else {
@@ -611,10 +621,60 @@ __global__ void __launch_bounds__(256) k_join(const GemmArgs a, int workers) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // 8 lanes a row, neighbouring columns
       const int c = (lane & 7) + 8 * i;
-      const T e = *reinterpret_cast<const T*>(buf + stage_at(rr, c >> 3) + (c & 7) * 2);
+      const T e = *reinterpret_cast<const T*>(buf + rr * 128 + (((c >> 3) ^ (rr & 7)) << 4) + (c & 7) * 2);
       if (n0 + u + c < a.N) out[orow * a.ldo + n0 + u + c] = e;
     }
   }
+}
+
+struct FinishArgs {
+  GemmArgs g[2];               // the two products, for their joins
+  int cg[2], workers[2], units[2], blocks[2];
+  // db of a piece: the column sums of d over the row tiles
+  const float* dbp;
+  long long ld;
+  const int* rows_dev;
+  int per, cols, col0, type, bias_blocks;
+  const float* scale;
+  void* db;
+};
+
+// One launch for what the products of a piece leave: db (a block per 32
+// columns, 8 slices of the rows, eight loads of a slice in flight) and the
+// joins of dx and dw.
+template <class T>
+__global__ void __launch_bounds__(256) k_finish(const FinishArgs f) {
+  __shared__ __align__(16) char buf[4096];
+  pdl_wait();
+  pdl_next();
+  int b = blockIdx.x;
+  if (b < f.bias_blocks) {
+    float(*red)[32] = reinterpret_cast<float(*)[32]>(buf);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c = b * 32 + lane;
+    int n = (*f.rows_dev + 128 * f.per - 1) / (128 * f.per);
+    n = (n < 1 ? 1 : n) * 4 * f.per;
+    float s = 0.f;
+    if (c < f.cols)
+      for (int j = warp; j < n; j += 64) {
+        float p[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) p[k] = j + 8 * k < n ? f.dbp[(long long)(j + 8 * k) * f.ld + c] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += p[k];
+      }
+    red[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < f.cols) {
+      for (int w = 1; w < 8; ++w) s += red[w][lane];
+      store_elem(f.db, f.type, (long long)f.col0 + c, s * *f.scale);
+    }
+    return;
+  }
+  b -= f.bias_blocks;
+  const int i = b < f.blocks[0] ? 0 : 1;
+  if (i) b -= f.blocks[0];
+  join_tile<T>(f.g[i], f.cg[i], f.workers[i], b / f.units[i], b % f.units[i], buf);
 }
 
 // ---------------------------------------------------------------- rows
@@ -888,34 +948,6 @@ __global__ void __launch_bounds__(32 * kSlices) k_combine(const CombineArgs a) {
   }
 }
 
-// db of a piece: the column sums of d over the row tiles, in order.
-__global__ void __launch_bounds__(256) k_bias_grad(const float* __restrict__ dbp, long long ld, const int* rows_dev,
-                                                   int per, const float* __restrict__ scale, void* db, int type, int col0,
-                                                   int cols) {
-  __shared__ float red[8][32];
-  pdl_wait();
-  pdl_next();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  int n = (*rows_dev + 128 * per - 1) / (128 * per);
-  n = (n < 1 ? 1 : n) * 4 * per;
-  float s = 0.f;
-  if (c < cols)
-    for (int j = warp; j < n; j += 64) {
-      float p[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) p[k] = j + 8 * k < n ? dbp[(long long)(j + 8 * k) * ld + c] : 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s += p[k];
-    }
-  red[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < cols) {
-    for (int w = 1; w < 8; ++w) s += red[w][lane];
-    store_elem(db, type, (long long)col0 + c, s * *scale);
-  }
-}
-
 // ---------------------------------------------------------------- host side
 
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -953,7 +985,6 @@ cudaError_t launch_gemm_t(const CUtensorMap& ma, const CUtensorMap& mb, const Ge
   if (e != cudaSuccess) return e;
   return launch(kern, dim3(blocks), kThreads, kSmem, s, CG, ma, mb, a);
 }
-
 template <int MODE, bool AMN, bool BMN>
 cudaError_t launch_gemm(int type, int cg, const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& a, int blocks,
                         cudaStream_t s) {
@@ -1056,7 +1087,7 @@ LogpLayout logp_layout(long long N, int V, int H) {
   l.Hp = (int)up_to(H, 8);
   l.Np = up_to(N > 0 ? N : 1, 256);
   Taker t;
-  l.o_part = t.take((size_t)l.nt * 2 * l.Np * 8);
+  l.o_part = t.take((size_t)l.nt * part_slots(l.bn) * l.Np * 8);
   l.o_lse = t.take((size_t)l.Np * 4);
   l.o_x = t.take((size_t)N * l.Hp * 2);  // rows that no tiled copy can read are laid out here
   l.o_w = t.take((size_t)V * l.Hp * 2);
@@ -1069,7 +1100,7 @@ struct CeLayout {
   long long Np;
   size_t o_ctl, o_map, o_tgt, o_xg, o_w;
   size_t o_part, o_zt, o_sums;
-  size_t o_lse, o_rs, o_d, o_dbp, o_slots, o_acc, total;
+  size_t o_lse, o_rs, o_d, o_dbp, o_slots[2], o_acc, total;
 };
 CeLayout ce_layout(long long N, int V, int H, bool backward) {
   CeLayout l{};
@@ -1084,7 +1115,7 @@ CeLayout ce_layout(long long N, int V, int H, bool backward) {
   l.bn = logits_bn(N, V);
   if (!backward) {
     l.nt = (V + l.bn - 1) / l.bn;
-    l.o_part = t.take((size_t)l.nt * 2 * l.Np * 8);
+    l.o_part = t.take((size_t)l.nt * part_slots(l.bn) * l.Np * 8);
     l.o_zt = t.take((size_t)l.Np * 4);
     l.o_sums = t.take((size_t)(l.Np / 32) * 4);
   } else {
@@ -1101,28 +1132,19 @@ CeLayout ce_layout(long long N, int V, int H, bool backward) {
     l.o_rs = t.take((size_t)l.Np * 4);
     l.o_d = t.take((size_t)l.Np * l.piece * 2);
     l.o_dbp = t.take((size_t)mt * 4 * l.piece * 4);
-    l.o_slots = t.take((size_t)2 * kWorkers * 128 * l.pbn * 4);
+    for (auto& o : l.o_slots) o = t.take((size_t)2 * kWorkers * 128 * l.pbn * 4);
     l.o_acc = t.take(l.pieces > 1 ? (size_t)mt * nt * 128 * l.pbn * 4 : 0);
   }
   l.total = align_up(t.off, 256);
   return l;
 }
 
-template <class T, int CG>
-cudaError_t launch_join_t(const GemmArgs& a, long long max_tiles, int workers, cudaStream_t s) {
-  const int units = CG * 4 * ((a.bn + 63) / 64);
+// Blocks of k_finish that join a product's tiles: as many tiles as its last
+// wave may hold (the row count is on the device), none if nothing is split.
+int join_blocks(const GemmArgs& a, int cg, long long max_tiles, int workers) {
   const long long r = max_tiles < workers - 1 ? max_tiles : workers - 1;
   const long long depth = a.M > 0 ? a.rows : a.K;
-  if (r < 1 || depth <= 64 * (kSplitDepth - 1)) return cudaSuccess;  // nothing can be split
-  return launch(k_join<T, CG>, dim3((unsigned)r, units), 256, 0, s, 1, a, workers);
-}
-
-cudaError_t launch_join(int type, int cg, const GemmArgs& a, long long max_tiles, int workers, cudaStream_t s) {
-  if (cg == 2)
-    return type == CTCPB_BF16 ? launch_join_t<__nv_bfloat16, 2>(a, max_tiles, workers, s)
-                              : launch_join_t<__half, 2>(a, max_tiles, workers, s);
-  return type == CTCPB_BF16 ? launch_join_t<__nv_bfloat16, 1>(a, max_tiles, workers, s)
-                            : launch_join_t<__half, 1>(a, max_tiles, workers, s);
+  return depth <= 64 * (kSplitDepth - 1) ? 0 : (int)(r * cg * 4 * ((a.bn + 63) / 64));
 }
 
 }  // namespace
@@ -1191,7 +1213,7 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   c.rows = (int)N;
   c.part = a.part;
   c.part_ld = l.Np;
-  c.slots = 2 * l.nt;
+  c.slots = part_slots(l.bn) * l.nt;
   c.lse = (float*)(b + l.o_lse);
   TRY(launch(k_combine, (unsigned)((N + 31) / 32), 32 * kSlices, 0, s, 1, c));
   a.factor = factor_of(H, 1.0);
@@ -1294,7 +1316,7 @@ int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, con
   c.rows_dev = r.nv;
   c.part = a.part;
   c.part_ld = l.Np;
-  c.slots = 2 * l.nt;
+  c.slots = part_slots(l.bn) * l.nt;
   c.lse = lse;
   c.rowmap = r.rowmap;
   c.zt = a.zt;
@@ -1365,10 +1387,27 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
     a.status = r.status;
     long long tiles = l.Np / (128 * cg) * ((cols + l.bn - 1) / l.bn);
     TRY((launch_gemm<kDlogits, false, false>(type, cg, ma, mb, a, cg * (int)(tiles < sms / cg ? tiles : sms / cg), s)));
+    FinishArgs f{};
+    f.units[0] = f.units[1] = 1;
     if (dbias) {
-      TRY(launch(k_bias_grad, (unsigned)((cols + 31) / 32), 256, 0, s, 1, (const float*)a.dbp, (long long)l.piece,
-                 (const int*)r.nv, cg, (const float*)r.scale, dbias, bias_type, v0, cols));
+      f.dbp = a.dbp;
+      f.ld = l.piece;
+      f.rows_dev = r.nv;
+      f.per = cg;
+      f.cols = cols;
+      f.col0 = v0;
+      f.type = bias_type;
+      f.bias_blocks = (cols + 31) / 32;
+      f.scale = r.scale;
+      f.db = dbias;
     }
+    auto join = [&](int i, const GemmArgs& g, int cgp, long long max_tiles) {
+      f.g[i] = g;
+      f.cg[i] = cgp;
+      f.workers[i] = sms / cgp;
+      f.units[i] = cgp * 4 * ((g.bn + 63) / 64);
+      f.blocks[i] = join_blocks(g, cgp, max_tiles, sms / cgp);
+    };
     if (dx && N > 0) {  // dx (+)= d w[piece]
       const int cgp = pair_of(N, l.pbn);
       if (!make_map(&ma, type, b + l.o_d, l.piece, l.Np, l.piece, 128) || !make_map(&mb, type, weight, H, V, ldw, 64))
@@ -1388,14 +1427,14 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
       g.vec = rows_aligned(dx, lddx);
       g.scale = r.scale;
       g.rowmap = r.rowmap;
-      g.slots = (float*)(b + l.o_slots);
+      g.slots = (float*)(b + l.o_slots[0]);
       g.acc = l.pieces > 1 ? (float*)(b + l.o_acc) : nullptr;
       g.first = p == 0;
       g.last = p == l.pieces - 1;
       g.status = r.status;
       TRY((launch_gemm<kProduct, false, true>(type, cgp, ma, mb, g, sms / cgp * cgp, s)));
       tiles = l.Np / (128 * cgp) * ((H + l.pbn - 1) / l.pbn);
-      TRY(launch_join(type, cgp, g, tiles, sms / cgp, s));
+      join(0, g, cgp, tiles);
     }
     if (dweight) {  // dw[piece] = d^T x
       const int cgp = pair_of(cols, l.pbn);
@@ -1414,13 +1453,17 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
       g.ldo = lddw;
       g.vec = rows_aligned(g.out, lddw);
       g.scale = r.scale;
-      g.slots = (float*)(b + l.o_slots);
+      g.slots = (float*)(b + l.o_slots[1]);
       g.first = g.last = 1;
       g.status = r.status;
       TRY((launch_gemm<kProduct, true, true>(type, cgp, ma, mb, g, sms / cgp * cgp, s)));
       tiles = (long long)((cols + 128 * cgp - 1) / (128 * cgp)) * ((H + l.pbn - 1) / l.pbn);
-      TRY(launch_join(type, cgp, g, tiles, sms / cgp, s));
+      join(1, g, cgp, tiles);
     }
+    const int left = f.bias_blocks + f.blocks[0] + f.blocks[1];
+    if (left > 0)
+      TRY(type == CTCPB_BF16 ? launch(k_finish<__nv_bfloat16>, left, 256, 0, s, 1, f)
+                             : launch(k_finish<__half>, left, 256, 0, s, 1, f));
   }
   return CTCPB_OK;
 }

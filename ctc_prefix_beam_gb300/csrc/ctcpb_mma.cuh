@@ -127,13 +127,12 @@ __device__ __forceinline__ void mbar_expect(u32 bar, u32 bytes) {
 }
 // arrive on a barrier of any block of the cluster
 __device__ __forceinline__ void mbar_arrive_cluster(u32 bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool mbar_test_cluster(u32 bar, u32 parity) {
+__device__ __forceinline__ bool mbar_test_at(u32 bar, u32 parity) {
   u32 ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 2000;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
       : "memory");
