@@ -26,8 +26,8 @@ enum Mode { kStats = 0, kLogp = 1, kDlogits = 2, kProduct = 3 };
 constexpr int kEpiWarps = 16;      // 4 for each quarter of a tile's 256 columns
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kMaxStages = 8;
-constexpr int kTileBytes = 196608;  // operand tiles
-constexpr int kStageBuf = 2048;     // per epilogue warp: 32 rows of 64 bytes
+constexpr int kTileBytes = 163840;  // operand tiles
+constexpr int kStageBuf = 4096;     // per epilogue warp: 32 rows of 128 bytes
 constexpr int kEpiBytes = kEpiWarps * (kStageBuf + 32 * 4);  // ... and 32 biases
 constexpr int kCtlBytes = 512;      // barriers, the tensor-memory address, the give-up flag
 constexpr int kSmem = kTileBytes + kEpiBytes + kCtlBytes;
@@ -53,6 +53,7 @@ struct GemmArgs {
   const float* lse;
   const float* rs;      // per-row factor of d
   int per_row;          // ... which differs from row to row
+  float one_r, log2_r;  // ... or is this, and its log2
   float factor;         // of the accumulator: log2(e) (kLogp: 1), times what truncation lost
   float* zt;
   float2* part;
@@ -62,6 +63,7 @@ struct GemmArgs {
   void* out;
   long long ldo;
   int vec;              // rows of `out` start on 16-byte boundaries
+  int tiled;            // ... and tiled copies may write them (map_o)
   const float* scale;
   const int* rowmap;
   float* slots;         // partial tiles of the split wave
@@ -145,29 +147,42 @@ struct Sched {
 
 // ---------------------------------------------------------------- writing rows through shared memory
 //
-// A thread holds 32 columns of its own row.  The warp puts 64 bytes of each row
-// into a 2 KB buffer, its 16-byte chunks permuted by (row / 2) & 3 so that
-// neither side has bank conflicts, and then writes whole row pieces.
+// A thread holds 32 columns of its own row.  The warp puts 128 bytes of each row
+// into a 4 KB buffer, its 16-byte chunks permuted by row & 7: neither side has
+// bank conflicts, and a tiled copy with the 128-byte swizzle reads it as it is.
+// Such a copy writes whole lines without a thread's help (log-probabilities of
+// 16000 frames: 91 us with the warps' own 64-byte stores); rows that it cannot
+// take are written by the warp, a row's 128 bytes side by side.
 
-__device__ __forceinline__ u32 stage_at(int row, int chunk) { return (u32)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4)); }
+__device__ __forceinline__ u32 stage_at(int row, int chunk) { return (u32)(row * 128 + ((chunk ^ (row & 7)) << 4)); }
 
 template <class T>
 __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(Elem<T>::pack(v[0], v[1]), Elem<T>::pack(v[2], v[3]), Elem<T>::pack(v[4], v[5]),
                     Elem<T>::pack(v[6], v[7]));
 }
-// Write the buffer's rows (64 / sizeof(E) columns from c0 on, those below
+__device__ __forceinline__ void stage_f32(char* buf, int lane, const float (&v)[32]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<float4*>(buf + stage_at(lane, c)) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+template <class T>
+__device__ __forceinline__ void stage_16(char* buf, int lane, const float (&v)[32], int half) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(buf + stage_at(lane, 4 * half + c)) = pack8<T>(v + 8 * c);
+}
+// Write the buffer's rows (128 / sizeof(E) columns from c0 on, those below
 // `cols`) to the output; orow is this lane's output row, -1 for none.
 template <class E>
 __device__ __forceinline__ void flush_rows(const char* buf, int lane, E* out, long long ldo, int orow, int c0, int cols,
                                            bool vec) {
-  constexpr int per = 16 / (int)sizeof(E), width = 64 / (int)sizeof(E);  // elements of a chunk, of a row piece
+  constexpr int per = 16 / (int)sizeof(E);  // elements of a chunk
   __syncwarp();
   if (vec) {
-    const int c = lane & 3, col = c0 + c * per;
+    const int c = lane & 7, col = c0 + c * per;
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int row = it * 8 + (lane >> 2);
+    for (int it = 0; it < 8; ++it) {
+      const int row = it * 4 + (lane >> 3);
       const int r = __shfl_sync(0xffffffffu, orow, row);
       const uint4 p = *reinterpret_cast<const uint4*>(buf + stage_at(row, c));
       if (r >= 0 && col < cols) {
@@ -183,36 +198,17 @@ __device__ __forceinline__ void flush_rows(const char* buf, int lane, E* out, lo
       }
     }
   } else {
-    constexpr int rows = 32 / width;  // rows a warp writes at once
-    const int c = lane % width;
 #pragma unroll 4
-    for (int it = 0; it < 32; it += rows) {
-      const int row = it + lane / width;
+    for (int row = 0; row < 32; ++row) {
       const int r = __shfl_sync(0xffffffffu, orow, row);
-      const E e = *reinterpret_cast<const E*>(buf + stage_at(row, c / per) + (c % per) * (int)sizeof(E));
-      if (r >= 0 && c0 + c < cols) out[(long long)r * ldo + c0 + c] = e;
+#pragma unroll
+      for (int c = lane; c < 8 * per; c += 32) {
+        const E e = *reinterpret_cast<const E*>(buf + stage_at(row, c / per) + (c % per) * (int)sizeof(E));
+        if (r >= 0 && c0 + c < cols) out[(long long)r * ldo + c0 + c] = e;
+      }
     }
   }
   __syncwarp();
-}
-// 32 columns of a thread's row to the output
-__device__ __forceinline__ void write_f32(char* buf, int lane, const float (&v)[32], float* out, long long ldo, int orow,
-                                          int c0, int cols, bool vec) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<float4*>(buf + stage_at(lane, c)) =
-          make_float4(v[16 * h + 4 * c], v[16 * h + 4 * c + 1], v[16 * h + 4 * c + 2], v[16 * h + 4 * c + 3]);
-    flush_rows<float>(buf, lane, out, ldo, orow, c0 + 16 * h, cols, vec);
-  }
-}
-template <class T>
-__device__ __forceinline__ void write_16(char* buf, int lane, const float (&v)[32], T* out, long long ldo, int orow, int c0,
-                                         int cols, bool vec) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(buf + stage_at(lane, c)) = pack8<T>(v + 8 * c);
-  flush_rows<T>(buf, lane, out, ldo, orow, c0, cols, vec);
 }
 
 // Sum of column l over the warp's rows, in lane l: at each halving a lane
@@ -236,7 +232,8 @@ __device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
 // barriers.
 template <int MODE, class T, bool AMN, bool BMN, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const GemmArgs a) {
+    k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+           const __grid_constant__ CUtensorMap map_o, const GemmArgs a) {
   extern __shared__ __align__(1024) char smem[];
   char* const ctl = smem + kTileBytes + kEpiBytes;
   const u32 s_tiles = saddr(smem);
@@ -254,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     tma_prefetch_map(&map_a);
     tma_prefetch_map(&map_b);
+    if ((MODE == kLogp || MODE == kDlogits) && a.tiled) tma_prefetch_map(&map_o);
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init_n(s_full + 8 * i, 1);
       mbar_init_n(s_empty + 8 * i, 1);
@@ -364,43 +362,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     const u32 tempty0 = CG == 2 ? cluster_addr(s_tempty, 0) : s_tempty;
     const int rows = a.rows_dev ? *a.rows_dev : a.rows;
     const int mrows = a.M > 0 ? a.M : rows;
+    const bool store_tiled = (MODE == kLogp || MODE == kDlogits) && a.tiled;
+    // what a tile's rows and columns bring, read while the tile before it is worked on
+    struct Given {
+      float bias[2], lse, rs;
+      int tgt, orow;
+    };
+    auto read = [&](const Seg& g) {
+      Given w{{0.f, 0.f}, 0.f, 0.f, -1, -1};
+      const int row = (g.m * CG + (int)rank) * 128 + q * 32 + lane, n0 = g.n * a.bn;
+      if (row < mrows) w.orow = row;
+      if constexpr (MODE == kProduct) {
+        if (a.rowmap && row < mrows) w.orow = a.rowmap[row];
+      } else {
+        // a column past the vocabulary gets -inf, so that its exponential is 0
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int col = n0 + u + 32 * i + lane;
+          w.bias[i] = u < a.bn && col < a.N ? (a.bias ? load_elem(a.bias, a.bias_type, (long long)a.col0 + col) : 0.f) : -INFINITY;
+        }
+        if (row < mrows) {
+          if (MODE != kLogp && a.tgt) w.tgt = a.tgt[row];
+          if (MODE != kStats) w.lse = a.lse[row];
+          if (MODE == kDlogits) w.rs = a.rs[row];
+        }
+      }
+      return w;
+    };
     int as = 0;
     u32 aph = 0;
-    while (ok && sc.next(sg)) {
+    bool more = sc.next(sg);
+    Given w = more ? read(sg) : Given{};
+    while (more) {
       const int mtile = sg.m * CG + (int)rank;
-      const int row = mtile * 128 + q * 32 + lane, n0 = sg.n * a.bn;
+      const int row0 = mtile * 128 + q * 32, row = row0 + lane, n0 = sg.n * a.bn;
       // the columns that this tile writes end here (kDlogits fills its piece's width)
       const int lim = MODE == kDlogits ? (int)a.ldo - n0 : a.N - n0;
       const bool busy = u < a.bn && u < lim;
+      const int tile = sg.tile, slot = sg.slot, stat = sg.n * part_slots(a.bn) + u / 64;
       float bm = -INFINITY, bs = 0.f;  // running max and sum of the row
-      float lse = 0.f, rs = 0.f, bq[2] = {0.f, 0.f};
-      int tgt = -1, orow = row < mrows ? row : -1;
-      if constexpr (MODE != kProduct) {
-        if (busy) {
-          // a column past the vocabulary gets -inf, so that its exponential is 0
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int col = n0 + u + 32 * i + lane;
-            bq[i] = col < a.N ? (a.bias ? load_elem(a.bias, a.bias_type, (long long)a.col0 + col) * (MODE == kLogp ? 1.f : kLog2e)
-                                        : 0.f)
-                              : -INFINITY;
-          }
-          if (row < mrows) {
-            if (a.tgt) tgt = a.tgt[row] - a.col0 - n0;
-            if (MODE == kLogp) lse = a.lse[row];
-            if (MODE == kDlogits) {
-              // d = exp(z - lse) r: a factor r that all rows share is in the exponent
-              rs = a.rs[row];
-              lse = __fmaf_rn(a.lse[row], kLog2e, a.per_row ? 0.f : -log2f(rs));
-            }
-          }
-        }
-      } else if (a.rowmap && orow >= 0) {
-        orow = a.rowmap[row];
+      const int orow = w.orow, tgt = w.tgt - a.col0 - n0;  // (no target: below every column)
+      const float rs = w.rs;
+      float lse = w.lse, bq[2] = {w.bias[0], w.bias[1]};
+      if (MODE == kStats || MODE == kDlogits) {
+        bq[0] *= kLog2e;
+        bq[1] *= kLog2e;
       }
+      // d = exp(z - lse) r: a factor r that all rows share is in the exponent
+      if (MODE == kDlogits) lse = __fmaf_rn(lse, kLog2e, a.per_row ? 0.f : -a.log2_r);
       if (!(ok = __all_sync(0xffffffffu, wait(s_tfull + 8 * as, aph)))) break;
       tc_fence_after();
+      more = sc.next(sg);
+      if (more) w = read(sg);
       const u32 d = tmem + 256u * as + ((u32)(q * 32) << 16);
+      if (store_tiled) {  // the last copy out of the buffer has read it
+        if (lane == 0) tma_store_wait();
+        __syncwarp();
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int c0 = u + 32 * j;
@@ -459,7 +477,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if constexpr (MODE == kLogp) {
 #pragma unroll
           for (int i = 0; i < 32; i += 2) add2(v[i], v[i + 1], -lse);
-          write_f32(buf, lane, v, (float*)a.out, a.ldo, orow, n0 + c0, a.N, a.vec);
+          if (store_tiled && j) {
+            if (lane == 0) tma_store_wait();
+            __syncwarp();
+          }
+          stage_f32(buf, lane, v);
+          // a tiled copy cuts a row off at 16 bytes only
+          if (store_tiled && (a.N % 4 == 0 || c0 + 32 <= lim)) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0 && row0 < mrows) tma_store(&map_o, n0 + c0, row0, saddr(buf));
+          } else {
+            flush_rows<float>(buf, lane, (float*)a.out, a.ldo, orow, n0 + c0, a.N, a.vec);
+          }
         } else if constexpr (MODE == kDlogits) {
           if (c0 < a.bn) {
 #pragma unroll
@@ -470,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int tr = tgt - c0;
             if (__any_sync(0xffffffffu, (u32)tr < 32u)) {
-              const float one = a.per_row ? 1.f : rs;
+              const float one = a.per_row ? 1.f : a.one_r;
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] -= tr == i ? one : 0.f;
             }
@@ -483,20 +513,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 32; ++i) v[i] = row < mrows ? v[i] : 0.f;
             }
           }
-          write_16<T>(buf, lane, v, (T*)a.out, a.ldo, row, n0 + c0, (int)a.ldo, true);
+          stage_16<T>(buf, lane, v, j);
           if (a.dbp) {
             const float cs = column_sums(v, lane);
             if (c0 + lane < lim) a.dbp[((long long)mtile * 4 + q) * a.ldo + n0 + c0 + lane] = cs;
           }
         } else {
-          const long long at = (long long)c0 * 128 + q * 32 + lane, tile = 128ll * a.bn;
-          if (sg.slot >= 0) {  // a share of the depth: to its slot, a column's rows side by side
-            float* o = a.slots + ((long long)sg.slot * CG + rank) * tile + at;
+          const long long at = (long long)c0 * 128 + q * 32 + lane, size = 128ll * a.bn;
+          if (slot >= 0) {  // a share of the depth: to its slot, a column's rows side by side
+            float* o = a.slots + ((long long)slot * CG + rank) * size + at;
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i * 128] = v[i];
           } else {
             if (a.acc) {
-              float* o = a.acc + ((long long)sg.tile * CG + rank) * tile + at;
+              float* o = a.acc + ((long long)tile * CG + rank) * size + at;
               if (!a.first) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] += o[i * 128];
@@ -510,14 +540,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float f = *a.scale;
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] *= f;
-              write_16<T>(buf, lane, v, (T*)a.out, a.ldo, orow, n0 + c0, a.N, a.vec);
+              stage_16<T>(buf, lane, v, j);
             }
           }
         }
         __syncwarp();
       }
       if constexpr (MODE == kStats)
-        if (u < a.bn && row < mrows) a.part[((long long)sg.n * part_slots(a.bn) + u / 64) * a.part_ld + row] = make_float2(bm, bs);
+        if (u < a.bn && row < mrows) a.part[(long long)stat * a.part_ld + row] = make_float2(bm, bs);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * as);
@@ -525,7 +555,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         as = 0;
         aph ^= 1;
       }
+      // 64 columns of 16 bits are a buffer's worth
+      if constexpr (MODE == kDlogits) {
+        if (busy) {
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) tma_store(&map_o, n0 + u, row0, saddr(buf));
+        }
+      }
+      if constexpr (MODE == kProduct) {
+        if (busy && slot < 0 && a.last) flush_rows<T>(buf, lane, (T*)a.out, a.ldo, orow, n0 + u, a.N, a.vec);
+      }
     }
+    if (store_tiled && lane == 0) tma_store_done();
+    __syncwarp();
   }
   __syncthreads();
   if (*dead) {
@@ -598,8 +641,7 @@ __device__ void join_tile(const GemmArgs& a, int cg, int workers, int r, int uni
   const float f = *a.scale;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] *= f;
-  // 32 rows of 128 bytes, the 16-byte chunks permuted by the row
-  *reinterpret_cast<uint4*>(buf + lane * 128 + ((warp ^ (lane & 7)) << 4)) = pack8<T>(v);
+  *reinterpret_cast<uint4*>(buf + stage_at(lane, warp)) = pack8<T>(v);
   __syncthreads();
   // four rows a warp
   T* const out = (T*)a.out;
@@ -609,7 +651,7 @@ __device__ void join_tile(const GemmArgs& a, int cg, int workers, int r, int uni
   const long long orow = a.rowmap ? a.rowmap[mine] : mine;
   if (a.vec) {
     const int col = n0 + u + (lane & 7) * 8;
-    const uint4 p = *reinterpret_cast<const uint4*>(buf + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+    const uint4 p = *reinterpret_cast<const uint4*>(buf + stage_at(rr, lane & 7));
     if (col + 8 <= a.N) {
       *reinterpret_cast<uint4*>(out + orow * a.ldo + col) = p;
     } else {
@@ -621,7 +663,7 @@ __device__ void join_tile(const GemmArgs& a, int cg, int workers, int r, int uni
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // 8 lanes a row, neighbouring columns
       const int c = (lane & 7) + 8 * i;
-      const T e = *reinterpret_cast<const T*>(buf + rr * 128 + (((c >> 3) ^ (rr & 7)) << 4) + (c & 7) * 2);
+      const T e = *reinterpret_cast<const T*>(buf + stage_at(rr, c >> 3) + (c & 7) * 2);
       if (n0 + u + c < a.N) out[orow * a.ldo + n0 + u + c] = e;
     }
   }
@@ -966,33 +1008,38 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// A [outer, inner] matrix of 16-bit elements, in boxes of 64 x box_outer.
+// An [outer, inner] matrix, rows of ld elements, in boxes of 128 bytes x box_outer.
 bool make_map(CUtensorMap* m, int type, const void* base, long long inner, long long outer, long long ld, int box_outer) {
+  const int size = type == CTCPB_F32 ? 4 : 2;
   const EncodeFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
-  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_outer}, es[2] = {1, 1};
-  return fn(m, type == CTCPB_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * size};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_outer}, es[2] = {1, 1};
+  const CUtensorMapDataType dt = type == CTCPB_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : type == CTCPB_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return fn(m, dt, 2,
             const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int MODE, class T, bool AMN, bool BMN, int CG>
-cudaError_t launch_gemm_t(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& a, int blocks, cudaStream_t s) {
+cudaError_t launch_gemm_t(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const GemmArgs& a, int blocks,
+                          cudaStream_t s) {
   constexpr auto kern = k_gemm<MODE, T, AMN, BMN, CG>;
   cudaError_t e = smem_optin<kern>(kSmem);
   if (e != cudaSuccess) return e;
-  return launch(kern, dim3(blocks), kThreads, kSmem, s, CG, ma, mb, a);
+  return launch(kern, dim3(blocks), kThreads, kSmem, s, CG, ma, mb, mo, a);
 }
 template <int MODE, bool AMN, bool BMN>
-cudaError_t launch_gemm(int type, int cg, const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& a, int blocks,
-                        cudaStream_t s) {
+cudaError_t launch_gemm(int type, int cg, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
+                        const GemmArgs& a, int blocks, cudaStream_t s) {
   if (cg == 2)
-    return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, AMN, BMN, 2>(ma, mb, a, blocks, s)
-                              : launch_gemm_t<MODE, __half, AMN, BMN, 2>(ma, mb, a, blocks, s);
-  return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, AMN, BMN, 1>(ma, mb, a, blocks, s)
-                            : launch_gemm_t<MODE, __half, AMN, BMN, 1>(ma, mb, a, blocks, s);
+    return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, AMN, BMN, 2>(ma, mb, mo, a, blocks, s)
+                              : launch_gemm_t<MODE, __half, AMN, BMN, 2>(ma, mb, mo, a, blocks, s);
+  return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, AMN, BMN, 1>(ma, mb, mo, a, blocks, s)
+                            : launch_gemm_t<MODE, __half, AMN, BMN, 1>(ma, mb, mo, a, blocks, s);
 }
 
 constexpr int kWorkers = 152;  // SMs; the split wave's slots are sized by it
@@ -1039,6 +1086,8 @@ constexpr double kLog2ed = 1.4426950408889634;
 float factor_of(int K, double f) { return (float)(f * (1.0 + 0.26 * ((K + 15) / 16) * (1.0 / 16777216.0))); }
 
 bool rows_aligned(const void* p, long long ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
+// Rows that tiled copies may read: they fill what lies past H only from the next 16 bytes on.
+bool rows_tiled(const void* p, long long ld, int H) { return rows_aligned(p, ld) && H % 8 == 0; }
 
 cudaError_t copy_rows(const void* in, long long ldi, void* out, int ldo, long long n, int H, cudaStream_t s) {
   const long long b = (n + 7) / 8;
@@ -1174,19 +1223,19 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   if ((rc = check_ws(ws, ws_bytes, l.total))) return rc;
   cudaStream_t s = (cudaStream_t)stream;
   char* b = (char*)ws;
-  if (!rows_aligned(x, ldx)) {
+  if (!rows_tiled(x, ldx, H)) {
     TRY(copy_rows(x, ldx, b + l.o_x, l.Hp, N, H, s));
     x = b + l.o_x;
     ldx = l.Hp;
   }
-  if (!rows_aligned(weight, ldw)) {
+  if (!rows_tiled(weight, ldw, H)) {
     TRY(copy_rows(weight, ldw, b + l.o_w, l.Hp, V, H, s));
     weight = b + l.o_w;
     ldw = l.Hp;
   }
   const int cg = pair_of(N, l.bn);
-  CUtensorMap ma, mb;
-  if (!make_map(&ma, type, x, H, N, ldx, 128) || !make_map(&mb, type, weight, H, V, ldw, l.bn / cg)) return CTCPB_ECUDA;
+  CUtensorMap ma, mb, mo = {};
+  if (!make_map(&ma, type, x, l.Hp, N, ldx, 128) || !make_map(&mb, type, weight, l.Hp, V, ldw, l.bn / cg)) return CTCPB_ECUDA;
   GemmArgs a{};
   a.rows = (int)N;
   a.N = V;
@@ -1203,11 +1252,12 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   a.out = out;
   a.ldo = ldo;
   a.vec = ((uintptr_t)out & 15) == 0 && ldo % 4 == 0;
+  a.tiled = a.vec && make_map(&mo, CTCPB_F32, out, V, N, ldo, 32);
   a.status = &((Header*)ws)->status;
   a.reset_status = 1;
   const long long tiles = (N + 128 * cg - 1) / (128 * cg) * l.nt;
   const int sms = sm_count(), blocks = cg * (int)(tiles < sms / cg ? tiles : sms / cg);
-  TRY((launch_gemm<kStats, false, false>(type, cg, ma, mb, a, blocks, s)));
+  TRY((launch_gemm<kStats, false, false>(type, cg, ma, mb, ma, a, blocks, s)));
   a.reset_status = 0;
   CombineArgs c{};
   c.rows = (int)N;
@@ -1217,7 +1267,7 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   c.lse = (float*)(b + l.o_lse);
   TRY(launch(k_combine, (unsigned)((N + 31) / 32), 32 * kSlices, 0, s, 1, c));
   a.factor = factor_of(H, 1.0);
-  TRY((launch_gemm<kLogp, false, false>(type, cg, ma, mb, a, blocks, s)));
+  TRY((launch_gemm<kLogp, false, false>(type, cg, ma, mb, mo, a, blocks, s)));
   return CTCPB_OK;
 }
 
@@ -1244,7 +1294,7 @@ int ce_rows(int type, const void* x, int64_t ldx, const int32_t* targets, int64_
   r.ignore = ignore_index;
   r.x = (const u16*)x;
   r.ldx = ldx;
-  r.vec = rows_aligned(x, ldx) && H % 8 == 0;
+  r.vec = rows_tiled(x, ldx, H);
   r.xg = (u16*)(b + l.o_xg);
   r.ldg = l.Hp;
   r.rowmap = (int*)(b + l.o_map);
@@ -1284,14 +1334,14 @@ int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, con
   if (reduction == CTCPB_REDUCE_NONE) r.loss = loss;
   r.lse = lse;
   if ((rc = ce_rows(type, x, ldx, targets, N, V, H, ignore_index, reduction, l, b, r, s))) return rc;
-  if (!rows_aligned(weight, ldw)) {
+  if (!rows_tiled(weight, ldw, H)) {
     TRY(copy_rows(weight, ldw, b + l.o_w, l.Hp, V, H, s));
     weight = b + l.o_w;
     ldw = l.Hp;
   }
   const int cg = pair_of(N, l.bn);
   CUtensorMap ma, mb;
-  if (!make_map(&ma, type, r.xg, l.Hp, l.Np, l.Hp, 128) || !make_map(&mb, type, weight, H, V, ldw, l.bn / cg))
+  if (!make_map(&ma, type, r.xg, l.Hp, l.Np, l.Hp, 128) || !make_map(&mb, type, weight, l.Hp, V, ldw, l.bn / cg))
     return CTCPB_ECUDA;
   GemmArgs a{};
   a.rows_dev = r.nv;
@@ -1311,7 +1361,7 @@ int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, con
   a.status = r.status;
   const long long tiles = l.Np / (128 * cg) * l.nt;
   const int sms = sm_count();
-  TRY((launch_gemm<kStats, false, false>(type, cg, ma, mb, a, cg * (int)(tiles < sms / cg ? tiles : sms / cg), s)));
+  TRY((launch_gemm<kStats, false, false>(type, cg, ma, mb, ma, a, cg * (int)(tiles < sms / cg ? tiles : sms / cg), s)));
   CombineArgs c{};
   c.rows_dev = r.nv;
   c.part = a.part;
@@ -1353,7 +1403,7 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
   r.dx = (u16*)dx;
   r.lddx = lddx;
   if ((rc = ce_rows(type, x, ldx, targets, N, V, H, ignore_index, reduction, l, b, r, s))) return rc;
-  if (!rows_aligned(weight, ldw)) {
+  if (!rows_tiled(weight, ldw, H)) {
     TRY(copy_rows(weight, ldw, b + l.o_w, l.Hp, V, H, s));
     weight = b + l.o_w;
     ldw = l.Hp;
@@ -1361,9 +1411,10 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
   const int cg = pair_of(N, l.bn), sms = sm_count();
   for (int p = 0; p < l.pieces; ++p) {
     const int v0 = p * l.piece, cols = V - v0 < l.piece ? V - v0 : l.piece;
-    CUtensorMap ma, mb;
+    CUtensorMap ma, mb, mo;
     // d
-    if (!make_map(&ma, type, r.xg, l.Hp, l.Np, l.Hp, 128) || !make_map(&mb, type, weight, H, V, ldw, l.bn / cg))
+    if (!make_map(&ma, type, r.xg, l.Hp, l.Np, l.Hp, 128) || !make_map(&mb, type, weight, l.Hp, V, ldw, l.bn / cg) ||
+        !make_map(&mo, type, b + l.o_d, l.piece, l.Np, l.piece, 32))
       return CTCPB_ECUDA;
     GemmArgs a{};
     a.rows_dev = r.nv;
@@ -1380,13 +1431,16 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
     a.lse = r.lse_c;
     a.rs = r.rs;
     a.per_row = reduction == CTCPB_REDUCE_NONE;
+    a.log2_r = type == CTCPB_F16 ? 15.f : 0.f;  // see k_rows
+    a.one_r = type == CTCPB_F16 ? 32768.f : 1.f;
     a.factor = factor_of(H, kLog2ed);
     a.out = b + l.o_d;
     a.ldo = l.piece;
+    a.tiled = 1;
     a.dbp = dbias ? (float*)(b + l.o_dbp) : nullptr;
     a.status = r.status;
     long long tiles = l.Np / (128 * cg) * ((cols + l.bn - 1) / l.bn);
-    TRY((launch_gemm<kDlogits, false, false>(type, cg, ma, mb, a, cg * (int)(tiles < sms / cg ? tiles : sms / cg), s)));
+    TRY((launch_gemm<kDlogits, false, false>(type, cg, ma, mb, mo, a, cg * (int)(tiles < sms / cg ? tiles : sms / cg), s)));
     FinishArgs f{};
     f.units[0] = f.units[1] = 1;
     if (dbias) {
@@ -1410,7 +1464,7 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
     };
     if (dx && N > 0) {  // dx (+)= d w[piece]
       const int cgp = pair_of(N, l.pbn);
-      if (!make_map(&ma, type, b + l.o_d, l.piece, l.Np, l.piece, 128) || !make_map(&mb, type, weight, H, V, ldw, 64))
+      if (!make_map(&ma, type, b + l.o_d, l.piece, l.Np, l.piece, 128) || !make_map(&mb, type, weight, l.Hp, V, ldw, 64))
         return CTCPB_ECUDA;
       GemmArgs g{};
       g.rows_dev = r.nv;
@@ -1432,7 +1486,7 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
       g.first = p == 0;
       g.last = p == l.pieces - 1;
       g.status = r.status;
-      TRY((launch_gemm<kProduct, false, true>(type, cgp, ma, mb, g, sms / cgp * cgp, s)));
+      TRY((launch_gemm<kProduct, false, true>(type, cgp, ma, mb, ma, g, sms / cgp * cgp, s)));
       tiles = l.Np / (128 * cgp) * ((H + l.pbn - 1) / l.pbn);
       join(0, g, cgp, tiles);
     }
@@ -1456,7 +1510,7 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
       g.slots = (float*)(b + l.o_slots[1]);
       g.first = g.last = 1;
       g.status = r.status;
-      TRY((launch_gemm<kProduct, true, true>(type, cgp, ma, mb, g, sms / cgp * cgp, s)));
+      TRY((launch_gemm<kProduct, true, true>(type, cgp, ma, mb, ma, g, sms / cgp * cgp, s)));
       tiles = (long long)((cols + 128 * cgp - 1) / (128 * cgp)) * ((H + l.pbn - 1) / l.pbn);
       join(1, g, cgp, tiles);
     }

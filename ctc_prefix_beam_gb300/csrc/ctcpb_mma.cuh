@@ -173,6 +173,17 @@ __device__ __forceinline__ void tma_load(u32 dst, const CUtensorMap* map, int x,
         "l"(map), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
+// Copy a box from shared memory to (x, y) of a tensor map (what lies outside
+// the tensor is dropped); one group a thread at a time, whose memory may be
+// written again once tma_store_wait has returned.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, u32 src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map), "r"(x), "r"(y),
+               "r"(src)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
 }

@@ -98,6 +98,26 @@ def test_log_probs_strides_and_offsets():
     assert torch.equal(got, want) and (off[:, 301:] == 7.0).all()
 
 
+def test_what_lies_past_a_row_is_not_read():
+    """Rows on 16-byte boundaries whose width is no multiple of 16 bytes: the
+    next elements, NaN here, take no part; and outputs end where they should."""
+    x, w, b, t = inputs(200, 301, 93, BF)
+    want = head.log_probs(x, w, b)
+    wx = torch.full((200, 160), float("nan"), dtype=BF, device="cuda")
+    wx[:, :93] = x
+    ww = torch.full((301, 96), float("nan"), dtype=BF, device="cuda")
+    ww[:, :93] = w
+    pad = torch.full((200, 304), 7.0, device="cuda")
+    assert torch.equal(head.log_probs(wx[:, :93], ww[:, :93], b, out=pad[:, :301]), want) and (pad[:, 301:] == 7.0).all()
+    loss, lse = head.cross_entropy(x, w, t, b)
+    loss2, lse2 = head.cross_entropy(wx[:, :93], ww[:, :93], t, b)
+    assert torch.equal(loss, loss2) and torch.equal(lse, lse2)
+    one = torch.ones((), device="cuda")
+    for p, q in zip(head.cross_entropy_backward(one, x, w, t, lse, b),
+                    head.cross_entropy_backward(one, wx[:, :93], ww[:, :93], t, lse, b)):
+        assert torch.equal(p, q)
+
+
 def test_log_probs_labels_taken_out_and_special_values():
     x, w, b, _ = inputs(140, 300, 64, BF)
     b[::3] = -float("inf")
