@@ -7,6 +7,8 @@
 //   z = x w^T + b                        [rows, V], never stored as such
 //   kStats    per row and column tile (max z, sum exp(z - max)), z[target]
 //   kLogp     z - lse, float32           the decoder's log_prob
+//   kBand     both at once: a band of rows stays in the tensor memory of the
+//             blocks that share it until its lse is known
 //   kDlogits  d = (exp(z - lse) - [c = target]) r   16 bits, a piece of V
 //   kProduct  dx += d w  and  dw = d^T x
 //
@@ -21,7 +23,7 @@
 namespace ctcpb {
 namespace {
 
-enum Mode { kStats = 0, kLogp = 1, kDlogits = 2, kProduct = 3 };
+enum Mode { kStats = 0, kLogp = 1, kDlogits = 2, kProduct = 3, kBand = 4 };
 
 constexpr int kEpiWarps = 16;      // 4 for each quarter of a tile's 256 columns
 constexpr int kThreads = 128 + 32 * kEpiWarps;
@@ -71,6 +73,8 @@ struct GemmArgs {
   int first, last;      // of the pieces
   u32* status;
   int reset_status;
+  // kBand
+  int members, bands;   // workers that share a row tile; row tiles worked on at once
 };
 
 // ---------------------------------------------------------------- tiles and their split
@@ -85,6 +89,7 @@ struct Seg {
 struct Sched {
   int mt, nt, ks, group, tiles, dp, rem, nw, w, G, t, first;
   int u, u1;
+  int members, band, bands;  // kBand: this worker's column tile is w % members; the next row tile, and the step
   __device__ int share(int i) const { return (int)((long long)rem * ks * i / nw); }
   __device__ void init(const GemmArgs& a, int cg, int worker, int workers) {
     const int rows = a.rows_dev ? *a.rows_dev : a.rows;
@@ -115,6 +120,11 @@ struct Sched {
     u = w < nw ? share(w) : 0;
     u1 = w < nw ? share(w + 1) : 0;
     first = ks > 0 ? u / ks : 0;
+    members = a.members;
+    if (members > 0) {
+      bands = a.bands;
+      band = w < members * bands ? w / members : mt;
+    }
   }
   __device__ void place(int tile, Seg& s) const {
     const int per = group * nt, g = tile / per, in = tile - g * per;
@@ -124,6 +134,17 @@ struct Sched {
     s.m = g * group + in - s.n * gs;
   }
   __device__ bool next(Seg& s) {
+    if (members > 0) {
+      if (band >= mt) return false;
+      s.m = band;
+      s.n = w % members;
+      s.tile = 0;
+      s.k0 = 0;
+      s.k1 = ks;
+      s.slot = -1;
+      band += bands;
+      return true;
+    }
     if (t < dp) {
       place(t, s);
       s.k0 = 0;
@@ -226,6 +247,200 @@ __device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
   return v[0];
 }
 
+// ---------------------------------------------------------------- log-probabilities in one pass
+//
+// The members of a band (blocks, or pairs of blocks) hold its logits in tensor
+// memory, a column tile each.  A member publishes each row's (max, sum), waits
+// for the others', and writes z - lse: the product is made once and the output
+// written once.  The next band's product runs meanwhile into the other half of
+// tensor memory.  A published pair is one 64-bit store over a mark that no pair
+// can be, so that it is its own flag: whoever needs it reads until it is there
+// (with a counter, its fence and two barriers an exchange took 6600 cycles, 12200
+// a band).  Every member must be resident (a cooperative launch); the wait for
+// the others is bounded.  A wait that gives up makes every later one return at
+// once, so that the warps go through the same barriers to the end.
+
+constexpr int kBandTile = kTileBytes - 2 * 512 * 8;  // operand tiles; the rest holds the rows' sums
+constexpr int kPairSpins = 1 << 20;                  // of about 0.5 us
+constexpr u64 kNoPair = ~0ull;                       // two NaNs that no arithmetic makes
+
+__device__ __forceinline__ void epi_sync() {
+  asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kEpiWarps) : "memory");
+}
+__device__ __forceinline__ float2 join_sums(float2 p, float2 q) {
+  const float m = fmaxf(p.x, q.x), mm = m == -INFINITY ? 0.f : m;
+  return make_float2(m, __fmaf_rn(p.y, ex2(p.x - mm), q.y * ex2(q.x - mm)));
+}
+
+template <int CG, class W>
+__device__ void band_epilogue(const GemmArgs& a, Sched& sc, char* smem, u32 tmem, u32 s_tfull, u32 s_tempty,
+                                              u32 rank, const CUtensorMap* map_o, volatile u32* dead, W& wait) {
+  const int warp = (int)threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = warp & 3, eg = (warp - 4) >> 2, u = eg * 64;
+  char* const buf = smem + kTileBytes + (warp - 4) * kStageBuf;
+  float* const bias_s = reinterpret_cast<float*>(smem + kTileBytes + kEpiWarps * kStageBuf);  // the member's 256
+  float2* const own = reinterpret_cast<float2*>(smem + kBandTile);  // [4][128]: the column groups' sums
+  float2* const all = own + 512;                                    // [4][128]: the members', a quarter each
+  const u32 tempty0 = CG == 2 ? cluster_addr(s_tempty, 0) : s_tempty;
+  const int r128 = q * 32 + lane, G = a.members;
+  const u32 lanes = (u32)(q * 32) << 16;
+  int n0 = 0, end = 0, lim = 0;  // the member's columns: the first, how many, how many up to the last label
+
+  // a band's sums: this warp's columns', the tile's, published
+  auto sums = [&](const Seg& g, int as) {
+    float bm = -INFINITY, bs = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c0 = u + 32 * j;
+      if (c0 >= end) break;
+      float v[32];
+      tmem_load32(v, tmem + 256u * as + lanes + c0);
+      tmem_wait(v);
+      const float4* b4 = reinterpret_cast<const float4*>(bias_s + c0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 b = b4[i];
+        fma2(v[4 * i], v[4 * i + 1], a.factor, b.x, b.y);
+        fma2(v[4 * i + 2], v[4 * i + 3], a.factor, b.z, b.w);
+      }
+      // a tile's width is a multiple of 16 columns: the rest of a chunk is other memory
+      if (c0 + 32 > a.bn) {
+#pragma unroll
+        for (int i = 16; i < 32; ++i) v[i] = -INFINITY;
+      }
+      float m4[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m4[i] = fmaxf(v[i], v[i + 4]);
+#pragma unroll
+      for (int i = 8; i < 32; i += 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], fmaxf(v[i + k], v[i + k + 4]));
+      }
+      const float mn = fmaxf(fmaxf(bm, kLog2e * fmaxf(m4[0], m4[1])), kLog2e * fmaxf(m4[2], m4[3]));
+      const float mm = mn == -INFINITY ? 0.f : mn;
+      float s[4] = {bs * ex2(bm - mm), 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        fma2(v[i], v[i + 1], kLog2e, -mm, -mm);
+        fma2(v[i + 2], v[i + 3], kLog2e, -mm, -mm);
+        add2(s[0], s[1], ex2(v[i]), ex2(v[i + 1]));
+        add2(s[2], s[3], ex2(v[i + 2]), ex2(v[i + 3]));
+      }
+      bm = mn;
+      bs = (s[0] + s[1]) + (s[2] + s[3]);
+    }
+    own[eg * 128 + r128] = make_float2(bm, bs);
+    epi_sync();
+    float2 sum = own[r128];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) sum = join_sums(sum, own[i * 128 + r128]);
+    if (G > 1 && eg == 0)
+      asm volatile("st.relaxed.gpu.global.u64 [%0], %1;\n" ::"l"(reinterpret_cast<u64*>(a.part) +
+                                                                (((long long)g.m * CG + rank) * G + g.n) * 128 + r128),
+                   "l"(pair(sum.x, sum.y))
+                   : "memory");
+    return sum;  // the row's lse, if the member has every column
+  };
+  // a band's output, once every member's sums are there
+  auto finish = [&](const Seg& g, int as, float2 sum) {
+    const int row0 = (g.m * CG + (int)rank) * 128 + q * 32, row = row0 + lane;
+    if (G > 1) {  // a quarter of the members each
+      const u64* const part = reinterpret_cast<const u64*>(a.part) + ((long long)g.m * CG + rank) * G * 128 + r128;
+      sum = make_float2(-INFINITY, 0.f);
+      for (int i = eg; i < G; i += 32) {
+        u64 p[8];
+        int spin = 0;
+        bool there;
+        do {
+          there = true;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            p[k] = 0;
+            if (i + 4 * k < G)
+              asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];\n"
+                           : "=l"(p[k])
+                           : "l"(part + (long long)(i + 4 * k) * 128)
+                           : "memory");
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) there = there && p[k] != kNoPair;
+        } while (!there && ++spin < kPairSpins && !*dead);
+        if (!there) *dead = 1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i + 4 * k < G) {
+            float2 f;
+            unpair(f.x, f.y, p[k]);
+            sum = join_sums(sum, f);
+          }
+      }
+      all[eg * 128 + r128] = sum;
+      epi_sync();
+      sum = all[r128];
+#pragma unroll
+      for (int i = 1; i < 4; ++i) sum = join_sums(sum, all[i * 128 + r128]);
+    }
+    const float lse = ((sum.x == -INFINITY ? 0.f : sum.x) + log2f(sum.y)) * kLn2;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c0 = u + 32 * j;
+      if (c0 >= end) break;
+      float v[32];
+      tmem_load32(v, tmem + 256u * as + lanes + c0);
+      if (a.tiled) {  // the last copy out of the buffer has read it
+        if (lane == 0) tma_store_wait();
+        __syncwarp();
+      }
+      tmem_wait(v);
+      const float4* b4 = reinterpret_cast<const float4*>(bias_s + c0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 b = b4[i];
+        fma2(v[4 * i], v[4 * i + 1], a.factor, b.x - lse, b.y - lse);
+        fma2(v[4 * i + 2], v[4 * i + 3], a.factor, b.z - lse, b.w - lse);
+      }
+      stage_f32(buf, lane, v);
+      // a tiled copy writes 32 columns, and cuts a row off at 16 bytes only
+      if (a.tiled && c0 + 32 <= a.bn && (a.N % 4 == 0 || c0 + 32 <= lim)) {
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0 && row0 < a.rows) tma_store(map_o, n0 + c0, row0, saddr(buf));
+      } else {
+        flush_rows<float>(buf, lane, (float*)a.out, a.ldo, row < a.rows ? row : -1, n0 + c0, n0 + end, a.vec);
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * as);
+  };
+
+  Seg sg;
+  bool first = true;
+  int as = 0;
+  u32 aph = 0;
+  while (sc.next(sg)) {
+    if (first) {  // the member's biases; a column past the vocabulary gets -inf
+      n0 = sg.n * a.bn;
+      lim = a.N - n0;
+      end = a.bn < lim ? a.bn : lim;
+      const int c = (int)threadIdx.x - 128;
+      if (c < 256) bias_s[c] = c < end ? (a.bias ? load_elem(a.bias, a.bias_type, n0 + c) : 0.f) : -INFINITY;
+      epi_sync();
+      first = false;
+    }
+    __all_sync(0xffffffffu, wait(s_tfull + 8 * as, aph));
+    tc_fence_after();
+    finish(sg, as, sums(sg, as));
+    if (G == 1) epi_sync();  // the next band's sums go where these were read
+    if (++as == 2) {
+      as = 0;
+      aph ^= 1;
+    }
+  }
+  if (a.tiled && lane == 0) tma_store_done();
+  __syncwarp();
+}
+
 // ---------------------------------------------------------------- the matrix kernel
 
 // Shared memory: a ring of operand tiles, the epilogue warps' buffers, the
@@ -251,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     tma_prefetch_map(&map_a);
     tma_prefetch_map(&map_b);
-    if ((MODE == kLogp || MODE == kDlogits) && a.tiled) tma_prefetch_map(&map_o);
+    if ((MODE == kLogp || MODE == kDlogits || MODE == kBand) && a.tiled) tma_prefetch_map(&map_o);
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init_n(s_full + 8 * i, 1);
       mbar_init_n(s_empty + 8 * i, 1);
@@ -355,7 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {  // ---- epilogue: a warp's 32 rows and 64 columns of a tile
+  } else if (MODE == kBand && warp >= 4) {
+    band_epilogue<CG>(a, sc, smem, tmem, s_tfull, s_tempty, rank, &map_o, dead, wait);
+  } else if (MODE != kBand && warp >= 4) {  // ---- epilogue: a warp's 32 rows and 64 columns of a tile
     const int q = warp & 3, u = ((warp - 4) >> 2) * 64;
     char* const buf = smem + kTileBytes + (warp - 4) * kStageBuf;
     float* const bias_s = reinterpret_cast<float*>(smem + kTileBytes + kEpiWarps * kStageBuf) + (warp - 4) * 32;
@@ -759,6 +976,14 @@ __global__ void __launch_bounds__(256) k_copy_rows(const u16* __restrict__ in, l
     copy_row(in + r * ldi, out + r * ldo, H, ldo, false, threadIdx.x & 31);
 }
 
+// Marks every pair of a one-pass call as not there, and clears the status.
+__global__ void __launch_bounds__(256) k_no_pairs(uint4* part, long long n, u32* status) {
+  pdl_wait();
+  pdl_next();
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) part[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
+}
+
 struct RowArgs {
   const int* targets;
   int N, V, H, ignore;
@@ -1030,7 +1255,7 @@ cudaError_t launch_gemm_t(const CUtensorMap& ma, const CUtensorMap& mb, const CU
   constexpr auto kern = k_gemm<MODE, T, AMN, BMN, CG>;
   cudaError_t e = smem_optin<kern>(kSmem);
   if (e != cudaSuccess) return e;
-  return launch(kern, dim3(blocks), kThreads, kSmem, s, CG, ma, mb, mo, a);
+  return launch_as(MODE == kBand, kern, dim3(blocks), kThreads, kSmem, s, CG, ma, mb, mo, a);
 }
 template <int MODE, bool AMN, bool BMN>
 cudaError_t launch_gemm(int type, int cg, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
@@ -1066,8 +1291,8 @@ int product_bn(int N) { return N > 128 ? 256 : N > 64 ? 128 : 64; }
 // 65536 x 2048 with its gradients 6.21 -> 5.78 ms, 12800 x 32000 x 1024 568 ->
 // 549 us; rows that fill half a pair's tile stay with single SMs.
 int pair_of(long long rows, int bn) { return bn == 256 && rows > 128 ? 2 : 1; }
-int stages_of(int bn, int cg) {
-  const int n = kTileBytes / (16384 + bn / cg * 128);
+int stages_of(int bn, int cg, int bytes = kTileBytes) {
+  const int n = bytes / (16384 + bn / cg * 128);
   return n < kMaxStages ? n : kMaxStages;
 }
 // Row tiles whose operand rows fit in half of L2 sweep the columns together.
@@ -1124,19 +1349,50 @@ struct Taker {
   }
 };
 
+// How a call is made in one pass: `members` workers share a row tile (a band),
+// `bands` of them at once; members == 0: more columns than tensor memory holds.
+// The tile's width is the one whose rounds cost least: a round takes a time
+// that grows with the width, and one that does not (the members' exchange, about
+// as long as 128 columns, and the reading of a sum from each member).
+struct BandPlan {
+  int cg, bn, members, bands;
+};
+BandPlan band_plan(long long N, int V) {
+  BandPlan best{N > 128 ? 2 : 1, 0, 0, 0};
+  const int W = kWorkers / best.cg;
+  const long long mt = (N + 128 * best.cg - 1) / (128 * best.cg);
+  long long cost = 0;
+  for (int bn = 32; bn <= 256; bn += 16) {
+    const int G = (V + bn - 1) / bn;
+    if (G > W) continue;
+    const int bands = (int)(W / G < mt ? W / G : mt);
+    const long long c = (mt + bands - 1) / bands * (bn + (G > 1 ? 128 + G : 0));
+    if (best.members == 0 || c < cost) {
+      best.bn = bn;
+      best.members = G;
+      best.bands = bands;
+      cost = c;
+    }
+  }
+  return best;
+}
+
 struct LogpLayout {
+  BandPlan band;
   int bn, nt, Hp;
   long long Np;
   size_t o_part, o_lse, o_x, o_w, total;
 };
 LogpLayout logp_layout(long long N, int V, int H) {
   LogpLayout l{};
+  l.band = band_plan(N, V);
   l.bn = logits_bn(N, V);
   l.nt = (V + l.bn - 1) / l.bn;
   l.Hp = (int)up_to(H, 8);
   l.Np = up_to(N > 0 ? N : 1, 256);
+  const size_t two = (size_t)l.nt * part_slots(l.bn), one = (size_t)l.band.members;
   Taker t;
-  l.o_part = t.take((size_t)l.nt * part_slots(l.bn) * l.Np * 8);
+  l.o_part = t.take((two > one ? two : one) * l.Np * 8);
   l.o_lse = t.take((size_t)l.Np * 4);
   l.o_x = t.take((size_t)N * l.Hp * 2);  // rows that no tiled copy can read are laid out here
   l.o_w = t.take((size_t)V * l.Hp * 2);
@@ -1233,30 +1489,49 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
     weight = b + l.o_w;
     ldw = l.Hp;
   }
-  const int cg = pair_of(N, l.bn);
   CUtensorMap ma, mb, mo = {};
-  if (!make_map(&ma, type, x, l.Hp, N, ldx, 128) || !make_map(&mb, type, weight, l.Hp, V, ldw, l.bn / cg)) return CTCPB_ECUDA;
   GemmArgs a{};
   a.rows = (int)N;
   a.N = V;
   a.K = H;
-  a.bn = l.bn;
-  a.stages = stages_of(l.bn, cg);
-  a.group = group_of(H, cg);
   a.bias = bias;
   a.bias_type = bias_type;
   a.part = (float2*)(b + l.o_part);
-  a.part_ld = l.Np;
-  a.factor = factor_of(H, kLog2ed);
-  a.lse = (float*)(b + l.o_lse);
   a.out = out;
   a.ldo = ldo;
   a.vec = ((uintptr_t)out & 15) == 0 && ldo % 4 == 0;
   a.tiled = a.vec && make_map(&mo, CTCPB_F32, out, V, N, ldo, 32);
   a.status = &((Header*)ws)->status;
+  if (!make_map(&ma, type, x, l.Hp, N, ldx, 128)) return CTCPB_ECUDA;
+  const int sms = sm_count();
+  const BandPlan& p = l.band;
+  if (p.members > 0 && sms == kWorkers) {
+    if (!make_map(&mb, type, weight, l.Hp, V, ldw, p.bn / p.cg)) return CTCPB_ECUDA;
+    a.bn = p.bn;
+    a.stages = stages_of(p.bn, p.cg, kBandTile);
+    a.factor = factor_of(H, 1.0);
+    a.members = p.members;
+    a.bands = p.bands;
+    const long long marks = p.members > 1 ? (long long)l.Np * p.members / 2 : 0, mb256 = (marks + 255) / 256;
+    TRY(launch(k_no_pairs, (unsigned)(mb256 < 1 ? 1 : mb256 < 608 ? mb256 : 608), 256, 0, s, 1, (uint4*)a.part, marks,
+               a.status));
+    const cudaError_t e = launch_gemm<kBand, false, false>(type, p.cg, ma, mb, mo, a, p.cg * p.members * p.bands, s);
+    if (e == cudaSuccess) return CTCPB_OK;
+    if (e != cudaErrorCooperativeLaunchTooLarge && e != cudaErrorNotSupported) return CTCPB_ECUDA;
+    (void)cudaGetLastError();  // the blocks cannot all be resident here: two passes
+    a.members = 0;
+  }
+  const int cg = pair_of(N, l.bn);
+  if (!make_map(&mb, type, weight, l.Hp, V, ldw, l.bn / cg)) return CTCPB_ECUDA;
+  a.bn = l.bn;
+  a.stages = stages_of(l.bn, cg);
+  a.group = group_of(H, cg);
+  a.part_ld = l.Np;
+  a.factor = factor_of(H, kLog2ed);
+  a.lse = (float*)(b + l.o_lse);
   a.reset_status = 1;
   const long long tiles = (N + 128 * cg - 1) / (128 * cg) * l.nt;
-  const int sms = sm_count(), blocks = cg * (int)(tiles < sms / cg ? tiles : sms / cg);
+  const int blocks = cg * (int)(tiles < sms / cg ? tiles : sms / cg);
   TRY((launch_gemm<kStats, false, false>(type, cg, ma, mb, ma, a, blocks, s)));
   a.reset_status = 0;
   CombineArgs c{};
@@ -1267,6 +1542,7 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   c.lse = (float*)(b + l.o_lse);
   TRY(launch(k_combine, (unsigned)((N + 31) / 32), 32 * kSlices, 0, s, 1, c));
   a.factor = factor_of(H, 1.0);
+  a.group = 1;  // neighbours write neighbouring columns
   TRY((launch_gemm<kLogp, false, false>(type, cg, ma, mb, mo, a, blocks, s)));
   return CTCPB_OK;
 }
