@@ -16,7 +16,10 @@
 // thread feeds 128-byte swizzled operand tiles by tiled bulk copies, one
 // issues tcgen05 matrix instructions into tensor memory, eight warps run the
 // epilogue of the previous tile meanwhile (two accumulators).
+#include <atomic>
 #include <mutex>
+
+#include <cooperative_groups.h>
 
 #include "ctcpb_head.cuh"
 
@@ -255,10 +258,10 @@ __device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
 // written once.  The next band's product runs meanwhile into the other half of
 // tensor memory.  A published pair is one 64-bit store over a mark that no pair
 // can be, so that it is its own flag: whoever needs it reads until it is there
-// (with a counter, its fence and two barriers an exchange took 6600 cycles, 12200
-// a band).  Every member must be resident (a cooperative launch); the wait for
-// the others is bounded.  A wait that gives up makes every later one return at
-// once, so that the warps go through the same barriers to the end.
+// (with a counter, its fence and two barriers an exchange took 6600 cycles,
+// 12200 a band).  Every member must be resident (a cooperative launch); the wait
+// for the others is bounded.  A wait that gives up makes every later one return
+// at once, so that the warps go through the same barriers to the end.
 
 constexpr int kBandTile = kTileBytes - 2 * 512 * 8;  // operand tiles; the rest holds the rows' sums
 constexpr int kPairSpins = 1 << 20;                  // of about 0.5 us
@@ -504,6 +507,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   sc.init(a, CG, worker, workers);
   Seg sg;
   bool ok = true;
+
+  if constexpr (MODE == kBand) {
+    if (a.members > 1) {  // nobody reads a pair before its owner has marked it as not there
+      Sched mine = sc;
+      while (mine.next(sg))
+        if (threadIdx.x < 128)
+          reinterpret_cast<u64*>(a.part)[(((long long)sg.m * CG + rank) * a.members + sg.n) * 128 + threadIdx.x] = kNoPair;
+      cooperative_groups::this_grid().sync();
+    }
+  }
 
   if (warp == 0) {
     if (lane == 0) {  // ---- operand tiles
@@ -976,14 +989,6 @@ __global__ void __launch_bounds__(256) k_copy_rows(const u16* __restrict__ in, l
     copy_row(in + r * ldi, out + r * ldo, H, ldo, false, threadIdx.x & 31);
 }
 
-// Marks every pair of a one-pass call as not there, and clears the status.
-__global__ void __launch_bounds__(256) k_no_pairs(uint4* part, long long n, u32* status) {
-  pdl_wait();
-  pdl_next();
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) part[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
-}
-
 struct RowArgs {
   const int* targets;
   int N, V, H, ignore;
@@ -1270,10 +1275,14 @@ cudaError_t launch_gemm(int type, int cg, const CUtensorMap& ma, const CUtensorM
 constexpr int kWorkers = 152;  // SMs; the split wave's slots are sized by it
 
 int sm_count() {
+  static std::atomic<int> known[128];  // by device
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return kWorkers;
-  return n < kWorkers ? n : kWorkers;
+  if (cudaGetDevice(&dev) != cudaSuccess) return kWorkers;
+  if (dev < 128 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return kWorkers;
+  if (n > kWorkers) n = kWorkers;
+  if (dev < 128) known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 long long up_to(long long x, long long a) { return (x + a - 1) / a * a; }
@@ -1512,14 +1521,13 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
     a.factor = factor_of(H, 1.0);
     a.members = p.members;
     a.bands = p.bands;
-    const long long marks = p.members > 1 ? (long long)l.Np * p.members / 2 : 0, mb256 = (marks + 255) / 256;
-    TRY(launch(k_no_pairs, (unsigned)(mb256 < 1 ? 1 : mb256 < 608 ? mb256 : 608), 256, 0, s, 1, (uint4*)a.part, marks,
-               a.status));
+    a.reset_status = 1;
     const cudaError_t e = launch_gemm<kBand, false, false>(type, p.cg, ma, mb, mo, a, p.cg * p.members * p.bands, s);
     if (e == cudaSuccess) return CTCPB_OK;
     if (e != cudaErrorCooperativeLaunchTooLarge && e != cudaErrorNotSupported) return CTCPB_ECUDA;
     (void)cudaGetLastError();  // the blocks cannot all be resident here: two passes
     a.members = 0;
+    a.reset_status = 0;
   }
   const int cg = pair_of(N, l.bn);
   if (!make_map(&mb, type, weight, l.Hp, V, ldw, l.bn / cg)) return CTCPB_ECUDA;

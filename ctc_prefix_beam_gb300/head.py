@@ -82,36 +82,35 @@ def _rows(t: torch.Tensor, what: str, dtype=None):
     return t, N, H, ld
 
 
-def _matrix(w: torch.Tensor, dtype, device, what: str) -> torch.Tensor:
-    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.dtype != dtype or w.device != device:
-        raise ValueError(f"{what} must be a {dtype} tensor [V, H] on {device}")
-    if w.shape[1] > 1 and w.stride(1) != 1 or w.shape[0] > 1 and w.stride(0) < w.shape[1]:
-        w = w.contiguous()
-    return w
+def _matrix(w: torch.Tensor, H: int, dtype, device, what: str):
+    """``w`` [V, H], rows at one stride: (tensor, V, row stride)."""
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.dtype != dtype or w.device != device or w.shape[1] != H:
+        raise ValueError(f"{what} must be a {dtype} tensor [V, {H}] on {device}")
+    V = w.shape[0]
+    if w.is_contiguous():
+        return w, V, H
+    if H > 1 and w.stride(1) != 1 or V > 1 and w.stride(0) < H:
+        return w.contiguous(), V, H
+    return w, V, w.stride(0) if V > 1 else H
 
 
-def _ld(w: torch.Tensor) -> int:
-    return w.stride(0) if w.shape[0] > 1 else w.shape[1]
-
-
-def _params(dtype, n: int, device, **named):
-    """The parameter vectors (contiguous) and their common type."""
-    kind = None
-    out = []
-    for name, p in named.items():
-        if p is not None:
-            if not isinstance(p, torch.Tensor) or p.device != device or p.shape != (n,) or \
-                    p.dtype not in (dtype, torch.float32) or (kind is not None and p.dtype != kind):
-                raise ValueError(f"{name} must be a {dtype} or float32 tensor [{n}] on {device}, "
-                                 "the parameters of one type")
-            kind = p.dtype
-            p = p.contiguous()
-        out.append(p)
-    return out, kind if kind is not None else dtype
+def _params(dtype, n: int, device, first: str, p, second: str = "", q=None):
+    """One or two parameter vectors (contiguous) and their type."""
+    for name, v in ((first, p), (second, q)):
+        if v is not None and (not isinstance(v, torch.Tensor) or v.shape != (n,) or v.device != device or
+                              (v.dtype != dtype and v.dtype != torch.float32)):
+            raise ValueError(f"{name} must be a {dtype} or float32 tensor [{n}] on {device}")
+    if p is not None and q is not None and p.dtype != q.dtype:
+        raise ValueError(f"{first} and {second} must be of one type")
+    if p is not None and not p.is_contiguous():
+        p = p.contiguous()
+    if q is not None and not q.is_contiguous():
+        q = q.contiguous()
+    return p, q, dtype if p is None and q is None else (p if p is not None else q).dtype
 
 
 def _given(t: torch.Tensor, shape, dtype, device, what: str) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device \
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.device != device \
             or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on {device}")
     return t
@@ -125,8 +124,8 @@ def _size(name: str, *args) -> int:
 
 
 def _workspace(ws, need: int, device):
-    if ws is None:
-        return D._alloc(need, device), need
+    if ws is None:  # PyTorch's allocations start on 512-byte boundaries
+        return torch.empty(need, dtype=torch.uint8, device=device), need
     return ws, D._check_buf(ws, need, device, "workspace")
 
 
@@ -163,7 +162,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     [...] float32); ``outputs``: the three to write."""
     xr, N, H, ldx = _rows(x, "x")
     dev, dt = xr.device, xr.dtype
-    (w, b), pt = _params(dt, H, dev, weight=weight, bias=bias)
+    w, b, pt = _params(dt, H, dev, "weight", weight, "bias", bias)
     lead = x.shape[:-1]
     if outputs is None:
         y = torch.empty(x.shape, dtype=dt, device=dev)
@@ -195,7 +194,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
     lead = x.shape[:-1]
     _given(mean, lead, torch.float32, dev, "mean")
     _given(rstd, lead, torch.float32, dev, "rstd")
-    (w,), pt = _params(dt, H, dev, weight=weight)
+    w, _, pt = _params(dt, H, dev, "weight", weight)
     if weight is None and param_dtype is not None:
         if param_dtype not in (dt, torch.float32):
             raise ValueError(f"param_dtype must be {dt} or float32")
@@ -212,12 +211,9 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torc
 def _head_args(x, weight, bias):
     xr, N, H, ldx = _rows(x, "x")
     dev, dt = xr.device, xr.dtype
-    w = _matrix(weight, dt, dev, "weight")
-    V = w.shape[0]
-    if w.shape[1] != H:
-        raise ValueError(f"weight must be [V, {H}]")
-    (b,), bt = _params(dt, V, dev, bias=bias)
-    return xr, N, H, ldx, dev, dt, w, V, b, bt
+    w, V, ldw = _matrix(weight, H, dt, dev, "weight")
+    b, _, bt = _params(dt, V, dev, "bias", bias)
+    return xr, N, H, ldx, dev, dt, w, V, ldw, b, bt
 
 
 def log_probs_workspace_size(dtype, N: int, V: int, H: int) -> int:
@@ -229,17 +225,19 @@ def log_probs(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor
     """The decoder's input, log_softmax(x weight^T + bias): float32 [..., V].
     x and weight are bfloat16 or float16.  ``out``: a tensor [..., V] to write,
     its rows at one stride (the padded rows of a wider tensor, for instance)."""
-    xr, N, H, ldx, dev, dt, w, V, b, bt = _head_args(x, weight, bias)
-    shape = (*x.shape[:-1], V)
+    xr, N, H, ldx, dev, dt, w, V, ldw, b, bt = _head_args(x, weight, bias)
+    shape = (N, V) if x.dim() == 2 else (*x.shape[:-1], V)
+    ldo = V
     if out is None:
         out = torch.empty(shape, dtype=torch.float32, device=dev)
-    if tuple(out.shape) != shape or out.dtype != torch.float32 or out.device != dev:
-        raise ValueError(f"out must be a float32 tensor {list(shape)} on {dev}")
-    o, _, _, ldo = _rows(out, "out")
-    if o is not out:
-        raise ValueError("out's rows must lie at one stride, their labels contiguous")
+    else:
+        if not isinstance(out, torch.Tensor) or out.shape != shape or out.dtype != torch.float32 or out.device != dev:
+            raise ValueError(f"out must be a float32 tensor {list(shape)} on {dev}")
+        o, _, _, ldo = _rows(out, "out")
+        if o is not out:
+            raise ValueError("out's rows must lie at one stride, their labels contiguous")
     ws, nbytes = _workspace(workspace, log_probs_workspace_size(dt, N, V, H), dev)
-    _run(dev, "ctcpb_log_probs", _TYPES[dt], _TYPES[bt], _p(xr), ldx, _p(w), _ld(w), _p(b), N, V, H, _p(out), ldo,
+    _run(dev, "ctcpb_log_probs", _TYPES[dt], _TYPES[bt], _p(xr), ldx, _p(w), ldw, _p(b), N, V, H, _p(out), ldo,
          _p(ws), nbytes)
     return out
 
@@ -268,13 +266,13 @@ def cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, 
     no part.  Returns (loss, lse [...]): float32, the loss a scalar or [...]
     (reduction "none").  ``D.read_status(workspace)`` holds ``DEV_TARGET`` if a
     target was out of range (such a row is ignored)."""
-    xr, N, H, ldx, dev, dt, w, V, b, bt = _head_args(x, weight, bias)
+    xr, N, H, ldx, dev, dt, w, V, ldw, b, bt = _head_args(x, weight, bias)
     t, red = _targets(targets, x, dev), _reduction(reduction)
     lead = x.shape[:-1]
     loss = torch.empty(lead if red == NONE else (), dtype=torch.float32, device=dev)
     lse = torch.empty(lead, dtype=torch.float32, device=dev)
     ws, nbytes = _workspace(workspace, cross_entropy_workspace_size(dt, N, V, H, False), dev)
-    _run(dev, "ctcpb_cross_entropy", _TYPES[dt], _TYPES[bt], _p(xr), ldx, _p(w), _ld(w), _p(b), _p(t), N, V, H,
+    _run(dev, "ctcpb_cross_entropy", _TYPES[dt], _TYPES[bt], _p(xr), ldx, _p(w), ldw, _p(b), _p(t), N, V, H,
          ignore_index, red, _p(loss), _p(lse), _p(ws), nbytes)
     return loss, lse
 
@@ -285,7 +283,7 @@ def cross_entropy_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Te
     """Gradients of ``cross_entropy`` for the loss's gradient ``grad`` (float32,
     a scalar, or [...] for reduction "none"): (dx like x, dweight, dbias; dbias
     is None without a bias)."""
-    xr, N, H, ldx, dev, dt, w, V, b, bt = _head_args(x, weight, bias)
+    xr, N, H, ldx, dev, dt, w, V, ldw, b, bt = _head_args(x, weight, bias)
     t, red = _targets(targets, x, dev), _reduction(reduction)
     lead = x.shape[:-1]
     _given(lse, lead, torch.float32, dev, "lse")
@@ -294,6 +292,6 @@ def cross_entropy_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Te
     dw = torch.empty((V, H), dtype=dt, device=dev)
     db = torch.empty((V,), dtype=bt, device=dev) if bias is not None else None
     ws, nbytes = _workspace(workspace, cross_entropy_workspace_size(dt, N, V, H, True), dev)
-    _run(dev, "ctcpb_cross_entropy_backward", _TYPES[dt], _TYPES[bt], _p(grad), _p(xr), ldx, _p(w), _ld(w), _p(b),
+    _run(dev, "ctcpb_cross_entropy_backward", _TYPES[dt], _TYPES[bt], _p(grad), _p(xr), ldx, _p(w), ldw, _p(b),
          _p(t), _p(lse), N, V, H, ignore_index, red, _p(dx), H, _p(dw), H, _p(db), _p(ws), nbytes)
     return dx, dw, db
