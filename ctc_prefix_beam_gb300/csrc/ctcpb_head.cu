@@ -93,7 +93,12 @@ struct Sched {
   int mt, nt, ks, group, tiles, dp, rem, nw, w, G, t, first;
   int u, u1;
   int members, band, bands;  // kBand: this worker's column tile is w % members; the next row tile, and the step
-  __device__ int share(int i) const { return (int)((long long)rem * ks * i / nw); }
+  int part, odd;  // a share's slices: part + 1 for the first `odd` workers, then part
+  __device__ int share(int i) const { return part * i + (i < odd ? i : odd); }  // the first slice of worker i's share
+  __device__ int worker_of(int slice) const {
+    const int big = odd * (part + 1);
+    return slice < big ? slice / (part + 1) : odd + (slice - big) / part;
+  }
   __device__ void init(const GemmArgs& a, int cg, int worker, int workers) {
     const int rows = a.rows_dev ? *a.rows_dev : a.rows;
     const bool rows_k = a.M > 0;  // M given: the rows are the depth
@@ -119,6 +124,8 @@ struct Sched {
       if (nw < rem) nw = rem;
       if (nw < 1) nw = 1;
     }
+    part = rem * ks / nw;
+    odd = rem * ks - part * nw;
     t = w;
     u = w < nw ? share(w) : 0;
     u1 = w < nw ? share(w + 1) : 0;
@@ -822,15 +829,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // tile's output written: a block per 32 rows and 64 columns, 8 columns a warp
 // (16 bytes of each row), two shares' loads in flight.
 template <class T>
-__device__ void join_tile(const GemmArgs& a, int cg, int workers, int r, int unit, char* buf) {
-  Sched sc;
-  sc.init(a, cg, 0, workers);
+__device__ void join_tile(const GemmArgs& a, const Sched& sc, int cg, int r, int unit, char* buf) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (r >= sc.rem) return;
   const int lo = r * sc.ks, hi = lo + sc.ks;
-  int w = (int)((long long)lo * sc.nw / ((long long)sc.rem * sc.ks));
-  while (w > 0 && sc.share(w) > lo) --w;
-  while (sc.share(w + 1) <= lo) ++w;
+  const int w = sc.worker_of(lo);
   if (sc.share(w) <= lo && sc.share(w + 1) >= hi) return;  // one share: written by the matrix kernel
   Seg sg;
   sc.place(sc.dp + r, sg);
@@ -841,6 +843,11 @@ __device__ void join_tile(const GemmArgs& a, int cg, int workers, int r, int uni
   const int mrows = a.M > 0 ? a.M : rows;
   const int c0 = u + 8 * warp;  // bn is a multiple of 64
   const long long at = (long long)c0 * 128 + q * 32 + lane, tile = 128ll * a.bn;
+  // the output rows (four a warp) and the scale, on their way with the shares
+  const int rr = warp * 4 + (lane >> 3);
+  const int mine = (sg.m * cg + rank) * 128 + q * 32 + rr;
+  const int orow = mine < mrows ? (a.rowmap ? a.rowmap[mine] : mine) : -1;
+  const float f = a.last ? *a.scale : 0.f;
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.f;
@@ -868,85 +875,92 @@ __device__ void join_tile(const GemmArgs& a, int cg, int workers, int r, int uni
     }
   }
   if (!a.last) return;
-  const float f = *a.scale;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] *= f;
   *reinterpret_cast<uint4*>(buf + stage_at(lane, warp)) = pack8<T>(v);
   __syncthreads();
-  // four rows a warp
-  T* const out = (T*)a.out;
-  const int rr = warp * 4 + (lane >> 3);
-  const int mine = (sg.m * cg + rank) * 128 + q * 32 + rr;
-  if (mine >= mrows) return;
-  const long long orow = a.rowmap ? a.rowmap[mine] : mine;
+  if (orow < 0) return;
+  T* const out = (T*)a.out + (long long)orow * a.ldo;
   if (a.vec) {
     const int col = n0 + u + (lane & 7) * 8;
     const uint4 p = *reinterpret_cast<const uint4*>(buf + stage_at(rr, lane & 7));
     if (col + 8 <= a.N) {
-      *reinterpret_cast<uint4*>(out + orow * a.ldo + col) = p;
+      *reinterpret_cast<uint4*>(out + col) = p;
     } else {
       const T* e = reinterpret_cast<const T*>(&p);
       for (int i = 0; i < 8; ++i)
-        if (col + i < a.N) out[orow * a.ldo + col + i] = e[i];
+        if (col + i < a.N) out[col + i] = e[i];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // 8 lanes a row, neighbouring columns
       const int c = (lane & 7) + 8 * i;
       const T e = *reinterpret_cast<const T*>(buf + stage_at(rr, c >> 3) + (c & 7) * 2);
-      if (n0 + u + c < a.N) out[orow * a.ldo + n0 + u + c] = e;
+      if (n0 + u + c < a.N) out[n0 + u + c] = e;
     }
   }
 }
 
 struct FinishArgs {
   GemmArgs g[2];               // the two products, for their joins
-  int cg[2], workers[2], units[2], blocks[2];
+  int cg[2], workers[2], units[2];  // units of a tile (0: nothing to join)
   // db of a piece: the column sums of d over the row tiles
   const float* dbp;
   long long ld;
   const int* rows_dev;
-  int per, cols, col0, type, bias_blocks;
+  int per, cols, col0, type, bias_units;
   const float* scale;
   void* db;
 };
 
 // One launch for what the products of a piece leave: db (a block per 32
 // columns, 8 slices of the rows, eight loads of a slice in flight) and the
-// joins of dx and dw.
+// joins of dx and dw.  How many tiles were split is known here only, so the
+// blocks go through the units.
 template <class T>
-__global__ void __launch_bounds__(256) k_finish(const FinishArgs f) {
-  __shared__ __align__(16) char buf[4096];
+__global__ void __launch_bounds__(256, 5) k_finish(const FinishArgs f) {
+  __shared__ __align__(16) char buf[kStageBuf];
   pdl_wait();
   pdl_next();
-  int b = blockIdx.x;
-  if (b < f.bias_blocks) {
-    float(*red)[32] = reinterpret_cast<float(*)[32]>(buf);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = b * 32 + lane;
-    int n = (*f.rows_dev + 128 * f.per - 1) / (128 * f.per);
-    n = (n < 1 ? 1 : n) * 4 * f.per;
-    float s = 0.f;
-    if (c < f.cols)
-      for (int j = warp; j < n; j += 64) {
-        float p[8];
+  Sched sc[2];
+  int joins[2] = {0, 0};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) p[k] = j + 8 * k < n ? f.dbp[(long long)(j + 8 * k) * f.ld + c] : 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s += p[k];
-      }
-    red[warp][lane] = s;
-    __syncthreads();
-    if (warp == 0 && c < f.cols) {
-      for (int w = 1; w < 8; ++w) s += red[w][lane];
-      store_elem(f.db, f.type, (long long)f.col0 + c, s * *f.scale);
+  for (int i = 0; i < 2; ++i)
+    if (f.units[i] > 0) {
+      sc[i].init(f.g[i], f.cg[i], 0, f.workers[i]);
+      joins[i] = sc[i].rem * f.units[i];
     }
-    return;
+  for (int b = blockIdx.x; b < f.bias_units + joins[0] + joins[1]; b += gridDim.x) {
+    if (b < f.bias_units) {
+      float(*red)[32] = reinterpret_cast<float(*)[32]>(buf);
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+      const int c = b * 32 + lane;
+      int n = (*f.rows_dev + 128 * f.per - 1) / (128 * f.per);
+      n = (n < 1 ? 1 : n) * 4 * f.per;
+      float s = 0.f;
+      if (c < f.cols)
+        for (int j = warp; j < n; j += 64) {
+          float p[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) p[k] = j + 8 * k < n ? f.dbp[(long long)(j + 8 * k) * f.ld + c] : 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) s += p[k];
+        }
+      red[warp][lane] = s;
+      __syncthreads();
+      if (warp == 0 && c < f.cols) {
+        for (int w = 1; w < 8; ++w) s += red[w][lane];
+        store_elem(f.db, f.type, (long long)f.col0 + c, s * *f.scale);
+      }
+    } else if (b < f.bias_units + joins[0]) {
+      const int k = b - f.bias_units;
+      join_tile<T>(f.g[0], sc[0], f.cg[0], k / f.units[0], k % f.units[0], buf);
+    } else {
+      const int k = b - f.bias_units - joins[0];
+      join_tile<T>(f.g[1], sc[1], f.cg[1], k / f.units[1], k % f.units[1], buf);
+    }
+    __syncthreads();  // the buffer is used again
   }
-  b -= f.bias_blocks;
-  const int i = b < f.blocks[0] ? 0 : 1;
-  if (i) b -= f.blocks[0];
-  join_tile<T>(f.g[i], f.cg[i], f.workers[i], b / f.units[i], b % f.units[i], buf);
 }
 
 // ---------------------------------------------------------------- rows
@@ -1017,7 +1031,7 @@ struct RowArgs {
   int dx_vec;
 };
 
-constexpr int kRowBlocks = 1024;  // blocks of k_rows at most
+constexpr int kRowBlocks = 512;  // blocks of k_rows at most
 
 __device__ __forceinline__ int block_sum(int v, int* red) {
   v = __reduce_add_sync(0xffffffffu, v);
@@ -1045,17 +1059,36 @@ __global__ void __launch_bounds__(256) k_rows(const RowArgs a, int per) {
   const int end = base + per < a.N ? base + per : a.N;
   const bool last = blockIdx.x == gridDim.x - 1;
   auto kept = [&](int t) { return t >= 0 && t < a.V && t != a.ignore; };
+  const int t_first = base + (int)threadIdx.x < end ? a.targets[base + (int)threadIdx.x] : a.ignore;
   int before = 0, bad = 0;
-  for (int i = threadIdx.x; i < base; i += 256 * 8) {
+  auto count = [&](int t) {
+    const bool in = kept(t);
+    before += in;
+    bad |= !in && t != a.ignore;
+  };
+  int done = 0;  // `base` is a multiple of 16
+  if (((uintptr_t)a.targets & 15) == 0) {
+    const int4* const t4 = reinterpret_cast<const int4*>(a.targets);
+    for (int i = threadIdx.x; i < base / 4; i += 256 * 8) {
+      int4 t[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) t[k] = i + 256 * k < base / 4 ? t4[i + 256 * k] : make_int4(a.ignore, a.ignore, a.ignore, a.ignore);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        count(t[k].x);
+        count(t[k].y);
+        count(t[k].z);
+        count(t[k].w);
+      }
+    }
+    done = base;
+  }
+  for (int i = done + threadIdx.x; i < base; i += 256 * 8) {
     int t[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) t[k] = i + 256 * k < base ? a.targets[i + 256 * k] : a.ignore;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const bool in = kept(t[k]);
-      before += in;
-      bad |= !in && t[k] != a.ignore;
-    }
+    for (int k = 0; k < 8; ++k) count(t[k]);
   }
   before = block_sum(before, red);
   // the largest |grad| (float16 only): d is scaled by it to stay in range
@@ -1072,7 +1105,7 @@ __global__ void __launch_bounds__(256) k_rows(const RowArgs a, int per) {
   const float up = a.type == CTCPB_F16 ? 32768.f : 1.f;  // float16: |d| <= 1 is stored as |d| 2^15
   for (int r0 = base; r0 < end; r0 += 256) {  // 256 rows at a time
     const int row = r0 + (int)threadIdx.x;
-    const int t = row < end ? a.targets[row] : a.ignore;
+    const int t = r0 == base ? t_first : row < end ? a.targets[row] : a.ignore;
     const bool in = kept(t);
     bad |= !in && t != a.ignore;
     const u32 m = __ballot_sync(0xffffffffu, in);
@@ -1151,7 +1184,7 @@ struct CombineArgs {
 
 // lse = m + log(sum_j s_j exp(m_j - m)) over a row's tiles (m, s and z[target]
 // are to base 2, see kStats), and the losses: a block per 32 rows, 16 slices of
-// the tiles, four of a slice's loads in flight.
+// the tiles, eight of a slice's loads in flight.
 constexpr int kSlices = 16;
 __global__ void __launch_bounds__(32 * kSlices) k_combine(const CombineArgs a) {
   __shared__ float2 red[kSlices][32];
@@ -1161,18 +1194,26 @@ __global__ void __launch_bounds__(32 * kSlices) k_combine(const CombineArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = a.rows_dev ? *a.rows_dev : a.rows;
   const int i = blockIdx.x * 32 + lane;
-  float m = -INFINITY, s = 0.f;
+  float m = -INFINITY, s = 0.f, zt = 0.f;
+  int row = i;
   if (i < rows) {
-    for (int j = warp; j < a.slots; j += 4 * kSlices) {
-      float2 p[4];
+    if (warp == 0 && a.rowmap) {
+      row = a.rowmap[i];
+      zt = a.zt[i];
+    }
+    for (int j = warp; j < a.slots; j += 8 * kSlices) {
+      float2 p[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 8; ++k)
         p[k] = j + k * kSlices < a.slots ? a.part[(long long)(j + k * kSlices) * a.part_ld + i]
                                          : make_float2(-INFINITY, 0.f);
-      const float mn = fmaxf(fmaxf(m, fmaxf(p[0].x, p[1].x)), fmaxf(p[2].x, p[3].x)), mm = mn == -INFINITY ? 0.f : mn;
+      float mn = m;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mn = fmaxf(mn, p[k].x);
+      const float mm = mn == -INFINITY ? 0.f : mn;
       s *= ex2(m - mm);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s = __fmaf_rn(p[k].y, ex2(p[k].x - mm), s);
+      for (int k = 0; k < 8; ++k) s = __fmaf_rn(p[k].y, ex2(p[k].x - mm), s);
       m = mn;
     }
   }
@@ -1185,10 +1226,9 @@ __global__ void __launch_bounds__(32 * kSlices) k_combine(const CombineArgs a) {
     s = 0.f;
     for (int w = 0; w < kSlices; ++w) s = __fmaf_rn(red[w][lane].y, ex2(red[w][lane].x - mm), s);
     const float lse2 = mm + log2f(s);
-    const int row = a.rowmap ? a.rowmap[i] : i;
     a.lse[row] = lse2 * kLn2;
     if (a.rowmap) {
-      loss = (lse2 - a.zt[i]) * kLn2;
+      loss = (lse2 - zt) * kLn2;
       if (a.reduction == CTCPB_REDUCE_NONE) a.loss[row] = loss;
     }
   }
@@ -1205,17 +1245,15 @@ __global__ void __launch_bounds__(32 * kSlices) k_combine(const CombineArgs a) {
   __syncthreads();
   if (!fin) return;
   __threadfence();
-  __shared__ double dred[32 * kSlices];
+  __shared__ double dred[kSlices];
   double d = 0.0;
   for (int k = threadIdx.x; k < (int)gridDim.x; k += 32 * kSlices) d += (double)((volatile float*)a.sums)[k];
-  dred[threadIdx.x] = d;
+  for (int k = 16; k > 0; k >>= 1) d += __shfl_xor_sync(0xffffffffu, d, k);
+  if (lane == 0) dred[warp] = d;
   __syncthreads();
-  for (int k = 16 * kSlices; k > 0; k >>= 1) {
-    if ((int)threadIdx.x < k) dred[threadIdx.x] += dred[threadIdx.x + k];
-    __syncthreads();
-  }
   if (threadIdx.x == 0) {
-    *a.loss = (float)(a.reduction == CTCPB_REDUCE_MEAN ? dred[0] / (double)rows : dred[0]);
+    for (int k = 1; k < kSlices; ++k) d += dred[k];
+    *a.loss = (float)(a.reduction == CTCPB_REDUCE_MEAN ? d / (double)rows : d);
     *a.ticket = 0;
   }
 }
@@ -1453,12 +1491,10 @@ CeLayout ce_layout(long long N, int V, int H, bool backward) {
   return l;
 }
 
-// Blocks of k_finish that join a product's tiles: as many tiles as its last
-// wave may hold (the row count is on the device), none if nothing is split.
-int join_blocks(const GemmArgs& a, int cg, long long max_tiles, int workers) {
-  const long long r = max_tiles < workers - 1 ? max_tiles : workers - 1;
-  const long long depth = a.M > 0 ? a.rows : a.K;
-  return depth <= 64 * (kSplitDepth - 1) ? 0 : (int)(r * cg * 4 * ((a.bn + 63) / 64));
+// Whether a product may leave shares to join, by the most tiles and the most
+// depth it can have (its row count is on the device).
+bool may_split(const GemmArgs& a, long long max_tiles) {
+  return max_tiles > 0 && (a.M > 0 ? a.rows : a.K) > 64 * (kSplitDepth - 1);
 }
 
 }  // namespace
@@ -1590,8 +1626,8 @@ int ce_rows(int type, const void* x, int64_t ldx, const int32_t* targets, int64_
   r.type = type;
   r.reduction = reduction;
   r.dx_vec = r.dx && rows_aligned(r.dx, r.lddx) && H % 8 == 0;
-  long long per = up_to((N + kRowBlocks - 1) / kRowBlocks, 32);
-  if (per < 32) per = 32;
+  long long per = up_to((N + kRowBlocks - 1) / kRowBlocks, 16);
+  if (per < 16) per = 16;
   const long long blocks = N > 0 ? (N + per - 1) / per : 1;
   TRY(launch(k_rows, (unsigned)blocks, 256, 0, s, 1, r, (int)per));
   return CTCPB_OK;
@@ -1726,7 +1762,6 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
     long long tiles = l.Np / (128 * cg) * ((cols + l.bn - 1) / l.bn);
     TRY((launch_gemm<kDlogits, false, false>(type, cg, ma, mb, mo, a, cg * (int)(tiles < sms / cg ? tiles : sms / cg), s)));
     FinishArgs f{};
-    f.units[0] = f.units[1] = 1;
     if (dbias) {
       f.dbp = a.dbp;
       f.ld = l.piece;
@@ -1735,16 +1770,18 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
       f.cols = cols;
       f.col0 = v0;
       f.type = bias_type;
-      f.bias_blocks = (cols + 31) / 32;
+      f.bias_units = (cols + 31) / 32;
       f.scale = r.scale;
       f.db = dbias;
     }
+    long long left = f.bias_units;
     auto join = [&](int i, const GemmArgs& g, int cgp, long long max_tiles) {
+      if (!may_split(g, max_tiles)) return;
       f.g[i] = g;
       f.cg[i] = cgp;
       f.workers[i] = sms / cgp;
       f.units[i] = cgp * 4 * ((g.bn + 63) / 64);
-      f.blocks[i] = join_blocks(g, cgp, max_tiles, sms / cgp);
+      left += (max_tiles < f.workers[i] ? max_tiles : f.workers[i]) * f.units[i];
     };
     if (dx && N > 0) {  // dx (+)= d w[piece]
       const int cgp = pair_of(N, l.pbn);
@@ -1798,10 +1835,10 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
       tiles = (long long)((cols + 128 * cgp - 1) / (128 * cgp)) * ((H + l.pbn - 1) / l.pbn);
       join(1, g, cgp, tiles);
     }
-    const int left = f.bias_blocks + f.blocks[0] + f.blocks[1];
+    const unsigned most = 10u * kWorkers, blocks = left < most ? (unsigned)left : most;
     if (left > 0)
-      TRY(type == CTCPB_BF16 ? launch(k_finish<__nv_bfloat16>, left, 256, 0, s, 1, f)
-                             : launch(k_finish<__half>, left, 256, 0, s, 1, f));
+      TRY(type == CTCPB_BF16 ? launch(k_finish<__nv_bfloat16>, blocks, 256, 0, s, 1, f)
+                             : launch(k_finish<__half>, blocks, 256, 0, s, 1, f));
   }
   return CTCPB_OK;
 }
