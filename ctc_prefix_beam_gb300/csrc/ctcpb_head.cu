@@ -136,6 +136,11 @@ struct Sched {
       band = w < members * bands ? w / members : mt;
     }
   }
+  // kBand: every other band, from the second on if `turn`
+  __device__ void take_turns(int turn) {
+    band += turn * bands;
+    bands *= 2;
+  }
   __device__ void place(int tile, Seg& s) const {
     const int per = group * nt, g = tile / per, in = tile - g * per;
     const int gs = mt - g * group < group ? mt - g * group : group;
@@ -271,40 +276,64 @@ __device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
 // at once, so that the warps go through the same barriers to the end.
 
 constexpr int kBandTile = kTileBytes - 2 * 512 * 8;  // operand tiles; the rest holds the rows' sums
+constexpr int kSetWarps = kEpiWarps / 2;             // of the two sets, one for each half of tensor memory
 constexpr int kPairSpins = 1 << 20;                  // of about 0.5 us
 constexpr u64 kNoPair = ~0ull;                       // two NaNs that no arithmetic makes
 
-__device__ __forceinline__ void epi_sync() {
-  asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kEpiWarps) : "memory");
+__device__ __forceinline__ void set_sync(int set) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(1 + set), "n"(32 * kSetWarps) : "memory");
 }
-__device__ __forceinline__ float2 join_sums(float2 p, float2 q) {
-  const float m = fmaxf(p.x, q.x), mm = m == -INFINITY ? 0.f : m;
-  return make_float2(m, __fmaf_rn(p.y, ex2(p.x - mm), q.y * ex2(q.x - mm)));
+// (max, sum) pairs into one: the maxima first, so that the exponentials do not wait for one another
+template <int K>
+__device__ __forceinline__ float2 join_sums(const float2 (&p)[K]) {
+  float m = p[0].x;
+#pragma unroll
+  for (int k = 1; k < K; ++k) m = fmaxf(m, p[k].x);
+  const float mm = m == -INFINITY ? 0.f : m;
+  float s = 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) s = __fmaf_rn(p[k].y, ex2(p[k].x - mm), s);
+  return make_float2(m, s);
 }
 
 template <int CG, class W>
-__device__ void band_epilogue(const GemmArgs& a, Sched& sc, char* smem, u32 tmem, u32 s_tfull, u32 s_tempty,
-                                              u32 rank, const CUtensorMap* map_o, volatile u32* dead, W& wait) {
+__device__ void band_epilogue(const GemmArgs& a, Sched sc, char* smem, u32 tmem, u32 s_tfull, u32 s_tempty, u32 rank,
+                              const CUtensorMap* map_o, volatile u32* dead, W& wait) {
+  // two sets of eight warps take the bands in turn: one's waits and copies are
+  // under the other's arithmetic.  A warp has 32 rows and half the columns.
   const int warp = (int)threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q = warp & 3, eg = (warp - 4) >> 2, u = eg * 64;
+  const int set = (warp - 4) / kSetWarps, half = ((warp - 4) >> 2) & 1, q = warp & 3, u = half * 128;
   char* const buf = smem + kTileBytes + (warp - 4) * kStageBuf;
-  float* const bias_s = reinterpret_cast<float*>(smem + kTileBytes + kEpiWarps * kStageBuf);  // the member's 256
-  float2* const own = reinterpret_cast<float2*>(smem + kBandTile);  // [4][128]: the column groups' sums
-  float2* const all = own + 512;                                    // [4][128]: the members', a quarter each
-  const u32 tempty0 = CG == 2 ? cluster_addr(s_tempty, 0) : s_tempty;
+  float* const bias_s = reinterpret_cast<float*>(smem + kTileBytes + kEpiWarps * kStageBuf) + set * 256;  // the member's
+  float2* const own = reinterpret_cast<float2*>(smem + kBandTile) + set * 512;  // [2][128]: the halves' sums
+  float2* const all = own + 256;                                                // [2][128]: half the members' each
   const int r128 = q * 32 + lane, G = a.members;
-  const u32 lanes = (u32)(q * 32) << 16;
+  const u32 tfull = s_tfull + 8 * set, tempty = (CG == 2 ? cluster_addr(s_tempty, 0) : s_tempty) + 8 * set;
+  const u32 d = tmem + 256u * set + ((u32)(q * 32) << 16);
+  sc.take_turns(set);
+  Seg sg;
+  bool first = true;
   int n0 = 0, end = 0, lim = 0;  // the member's columns: the first, how many, how many up to the last label
-
-  // a band's sums: this warp's columns', the tile's, published
-  auto sums = [&](const Seg& g, int as) {
+  u32 ph = 0;
+  while (sc.next(sg)) {
+    if (first) {  // the member's biases; a column past the vocabulary gets -inf
+      n0 = sg.n * a.bn;
+      lim = a.N - n0;
+      end = a.bn < lim ? a.bn : lim;
+      const int c = (int)threadIdx.x - 128 - set * 256;
+      bias_s[c] = c < end ? (a.bias ? load_elem(a.bias, a.bias_type, n0 + c) : 0.f) : -INFINITY;
+      set_sync(set);
+      first = false;
+    }
+    __all_sync(0xffffffffu, wait(tfull, ph));
+    ph ^= 1;
+    tc_fence_after();
+    // 1. the sums of the warp's columns, of the tile's
     float bm = -INFINITY, bs = 0.f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c0 = u + 32 * j;
-      if (c0 >= end) break;
+#pragma unroll 1
+    for (int c0 = u; c0 < end && c0 < u + 128; c0 += 32) {
       float v[32];
-      tmem_load32(v, tmem + 256u * as + lanes + c0);
+      tmem_load32(v, d + c0);
       tmem_wait(v);
       const float4* b4 = reinterpret_cast<const float4*>(bias_s + c0);
 #pragma unroll
@@ -339,25 +368,18 @@ __device__ void band_epilogue(const GemmArgs& a, Sched& sc, char* smem, u32 tmem
       bm = mn;
       bs = (s[0] + s[1]) + (s[2] + s[3]);
     }
-    own[eg * 128 + r128] = make_float2(bm, bs);
-    epi_sync();
-    float2 sum = own[r128];
-#pragma unroll
-    for (int i = 1; i < 4; ++i) sum = join_sums(sum, own[i * 128 + r128]);
-    if (G > 1 && eg == 0)
-      asm volatile("st.relaxed.gpu.global.u64 [%0], %1;\n" ::"l"(reinterpret_cast<u64*>(a.part) +
-                                                                (((long long)g.m * CG + rank) * G + g.n) * 128 + r128),
-                   "l"(pair(sum.x, sum.y))
-                   : "memory");
-    return sum;  // the row's lse, if the member has every column
-  };
-  // a band's output, once every member's sums are there
-  auto finish = [&](const Seg& g, int as, float2 sum) {
-    const int row0 = (g.m * CG + (int)rank) * 128 + q * 32, row = row0 + lane;
-    if (G > 1) {  // a quarter of the members each
-      const u64* const part = reinterpret_cast<const u64*>(a.part) + ((long long)g.m * CG + rank) * G * 128 + r128;
+    own[half * 128 + r128] = make_float2(bm, bs);
+    set_sync(set);
+    const float2 mine[2] = {own[r128], own[128 + r128]};
+    float2 sum = join_sums(mine);
+    if (G > 1) {
+      // 2. publish the member's, read all of them as they come, half the members each
+      u64* const part = reinterpret_cast<u64*>(a.part) + ((long long)sg.m * CG + rank) * G * 128 + r128;
+      if (half == 0)
+        asm volatile("st.relaxed.gpu.global.u64 [%0], %1;\n" ::"l"(part + (long long)sg.n * 128), "l"(pair(sum.x, sum.y))
+                     : "memory");
       sum = make_float2(-INFINITY, 0.f);
-      for (int i = eg; i < G; i += 32) {
+      for (int i = half; i < G; i += 16) {
         u64 p[8];
         int spin = 0;
         bool there;
@@ -365,38 +387,37 @@ __device__ void band_epilogue(const GemmArgs& a, Sched& sc, char* smem, u32 tmem
           there = true;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            p[k] = 0;
-            if (i + 4 * k < G)
+            p[k] = pair(-INFINITY, 0.f);
+            if (i + 2 * k < G)
               asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];\n"
                            : "=l"(p[k])
-                           : "l"(part + (long long)(i + 4 * k) * 128)
+                           : "l"(part + (long long)(i + 2 * k) * 128)
                            : "memory");
           }
 #pragma unroll
           for (int k = 0; k < 8; ++k) there = there && p[k] != kNoPair;
         } while (!there && ++spin < kPairSpins && !*dead);
         if (!there) *dead = 1;
+        float2 f[9];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (i + 4 * k < G) {
-            float2 f;
-            unpair(f.x, f.y, p[k]);
-            sum = join_sums(sum, f);
-          }
+        for (int k = 0; k < 8; ++k) unpair(f[k].x, f[k].y, p[k]);
+        f[8] = sum;
+        sum = join_sums(f);
       }
-      all[eg * 128 + r128] = sum;
-      epi_sync();
-      sum = all[r128];
-#pragma unroll
-      for (int i = 1; i < 4; ++i) sum = join_sums(sum, all[i * 128 + r128]);
+      all[half * 128 + r128] = sum;
+    }
+    set_sync(set);  // (with one member: its sums have been read)
+    if (G > 1) {
+      const float2 both[2] = {all[r128], all[128 + r128]};
+      sum = join_sums(both);
     }
     const float lse = ((sum.x == -INFINITY ? 0.f : sum.x) + log2f(sum.y)) * kLn2;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c0 = u + 32 * j;
-      if (c0 >= end) break;
+    // 3. z - lse
+    const int row0 = (sg.m * CG + (int)rank) * 128 + q * 32, row = row0 + lane;
+#pragma unroll 1
+    for (int c0 = u; c0 < end && c0 < u + 128; c0 += 32) {
       float v[32];
-      tmem_load32(v, tmem + 256u * as + lanes + c0);
+      tmem_load32(v, d + c0);
       if (a.tiled) {  // the last copy out of the buffer has read it
         if (lane == 0) tma_store_wait();
         __syncwarp();
@@ -421,31 +442,7 @@ __device__ void band_epilogue(const GemmArgs& a, Sched& sc, char* smem, u32 tmem
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * as);
-  };
-
-  Seg sg;
-  bool first = true;
-  int as = 0;
-  u32 aph = 0;
-  while (sc.next(sg)) {
-    if (first) {  // the member's biases; a column past the vocabulary gets -inf
-      n0 = sg.n * a.bn;
-      lim = a.N - n0;
-      end = a.bn < lim ? a.bn : lim;
-      const int c = (int)threadIdx.x - 128;
-      if (c < 256) bias_s[c] = c < end ? (a.bias ? load_elem(a.bias, a.bias_type, n0 + c) : 0.f) : -INFINITY;
-      epi_sync();
-      first = false;
-    }
-    __all_sync(0xffffffffu, wait(s_tfull + 8 * as, aph));
-    tc_fence_after();
-    finish(sg, as, sums(sg, as));
-    if (G == 1) epi_sync();  // the next band's sums go where these were read
-    if (++as == 2) {
-      as = 0;
-      aph ^= 1;
-    }
+    if (lane == 0) mbar_arrive_cluster(tempty);
   }
   if (a.tiled && lane == 0) tma_store_done();
   __syncwarp();
@@ -483,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init_n(s_tfull + 8 * i, 1);
-      mbar_init_n(s_tempty + 8 * i, kEpiWarps * CG);
+      mbar_init_n(s_tempty + 8 * i, (MODE == kBand ? kSetWarps : kEpiWarps) * CG);
     }
     *dead = 0;
     mbar_init_fence();
