@@ -5,7 +5,7 @@
 //   dx = rstd (t - mean(t) - xh mean(t xh)),  dw = sum_rows dy xh,  db = sum_rows dy
 //
 // Bound by HBM: forward reads x and writes y, backward reads x and dy and
-// writes dx.  A row is worked on by the fewest warps that hold it, 16 or 32
+// writes dx.  A row is worked on by the fewest warps that hold it, 8 to 32
 // elements a thread, in pairs (one instruction for two); the next rows are on their way into shared memory meanwhile, each
 // thread copying just what it will read itself, so a row costs no barrier but
 // the sums' own.  The sums over rows for dw and db stay in the registers of the
@@ -16,7 +16,7 @@
 namespace ctcpb {
 namespace {
 
-constexpr int kLnBlocks = 304;  // two blocks an SM; also the number of partial column sums
+constexpr int kLnBlocks = 456;  // three blocks an SM; also the number of partial column sums
 
 __host__ __device__ constexpr int threads_of(int wpr) { return wpr > 8 ? wpr * 32 : 256; }  // of a block
 
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(threads_of(WPR), WPR <= 8 && VEC ? 2 : 1) k_ln
 }
 
 template <class T, bool VEC, int WPR, int E>
-__global__ void __launch_bounds__(threads_of(WPR), WPR <= 8 && VEC ? 2 : 1) k_ln_bwd(const NormArgs a) {
+__global__ void __launch_bounds__(threads_of(WPR), WPR > 8 || !VEC ? 1 : E == 8 ? 3 : 2) k_ln_bwd(const NormArgs a) {
   extern __shared__ __align__(16) char smem[];
   __shared__ float2 red[2][32];
   constexpr int tpr = 32 * WPR, per = threads_of(WPR) / tpr;
@@ -408,20 +408,23 @@ __global__ void __launch_bounds__(1024) k_ln_cols(const float* __restrict__ part
 }
 
 // Elements of a row a thread holds.  Forward, 32 where 16 would take a second
-// warp and 32 do not: the sums then need no barrier.  Backward always 16: its
-// registers also hold the weights and both column sums.
-int per_thread(int H, bool vec, bool bwd) { return !bwd && vec && H > 512 && H <= 1024 ? 32 : 16; }
+// warp and 32 do not: the sums then need no barrier (64000 rows of 1024: 48 us
+// with 16, 42 with 32).  Backward its registers also hold the weights and both
+// column sums: 8 let three blocks share an SM (76 us with 16, 69 with 8), as
+// long as eight warps hold the row.
+int per_thread(int H, bool vec, bool bwd) { return bwd ? (H <= 2048 ? 8 : 16) : vec && H > 512 && H <= 1024 ? 32 : 16; }
 
 struct Shape {
   int wpr, threads, blocks;
 };
-Shape shape_of(long long N, int H, int per_thread) {
+Shape shape_of(long long N, int H, bool vec, bool bwd) {
   Shape s{1, 256, 0};
-  while (s.wpr * 32 * per_thread < H) s.wpr *= 2;
+  const int each = per_thread(H, vec, bwd);
+  while (s.wpr * 32 * each < H) s.wpr *= 2;
   s.threads = threads_of(s.wpr);
-  const int per = s.threads / 32 / s.wpr;
+  const int per = s.threads / 32 / s.wpr, most = bwd && vec && each == 8 ? kLnBlocks : kLnBlocks / 3 * 2;
   const long long b = (N + per - 1) / per;
-  s.blocks = (int)(b < kLnBlocks ? b : kLnBlocks);
+  s.blocks = (int)(b < most ? b : most);
   return s;
 }
 
@@ -437,6 +440,14 @@ cudaError_t run_fwd(const NormArgs& a, const Shape& s, cudaStream_t st) {
   cudaError_t e = smem_optin<kern>(smem);
   return e != cudaSuccess ? e : launch(kern, s.blocks, s.threads, smem, st, 1, a);
 }
+template <class T, bool VEC, int WPR, int E>
+cudaError_t run_bwd(const NormArgs& a, const Shape& s, cudaStream_t st) {
+  const size_t sums = a.part ? (size_t)2 * a.H * 4 : 0, ring = Ahead<T, VEC, E, WPR, 2>::bytes;
+  const size_t smem = sums > ring ? sums : ring;
+  constexpr auto kern = k_ln_bwd<T, VEC, WPR, E>;
+  cudaError_t e = smem_optin<kern>(smem);
+  return e != cudaSuccess ? e : launch(kern, s.blocks, s.threads, smem, st, 1, a);
+}
 template <class T, bool VEC, int WPR>
 cudaError_t run_t(bool bwd, const NormArgs& a, const Shape& s, cudaStream_t st) {
   if (!bwd) {
@@ -445,11 +456,11 @@ cudaError_t run_t(bool bwd, const NormArgs& a, const Shape& s, cudaStream_t st) 
     }
     return run_fwd<T, VEC, WPR, 16>(a, s, st);
   }
-  const size_t sums = a.part ? (size_t)2 * a.H * 4 : 0, ring = Ahead<T, VEC, 16, WPR, 2>::bytes;
-  const size_t smem = sums > ring ? sums : ring;
-  constexpr auto kern = k_ln_bwd<T, VEC, WPR, 16>;
-  cudaError_t e = smem_optin<kern>(smem);
-  return e != cudaSuccess ? e : launch(kern, s.blocks, s.threads, smem, st, 1, a);
+  if constexpr (WPR >= 8) {
+    if (per_thread(a.H, VEC, true) == 16) return run_bwd<T, VEC, WPR, 16>(a, s, st);
+  }
+  if constexpr (WPR <= 8) return run_bwd<T, VEC, WPR, 8>(a, s, st);
+  return cudaErrorInvalidValue;  // no width leads here
 }
 template <class T, bool VEC>
 cudaError_t run_w(bool bwd, const NormArgs& a, const Shape& s, cudaStream_t st) {
@@ -504,7 +515,7 @@ int ctcpb_layer_norm(int type, int param_type, const void* x, int64_t ldx, const
   a.N = N;
   a.H = H;
   const bool vec = H % (type == CTCPB_F32 ? 4 : 8) == 0 && vec_ok(type, x, ldx) && vec_ok(type, y, ldy);
-  const Shape s = shape_of(N, H, per_thread(H, vec, false));
+  const Shape s = shape_of(N, H, vec, false);
   a.y = y;
   a.ldy = ldy;
   a.mean = mean;
@@ -516,7 +527,7 @@ int ctcpb_layer_norm_workspace_size(int64_t N, int H, size_t* bytes) {
   int rc = check(CTCPB_F32, CTCPB_F32, N, H);
   if (rc) return rc;
   if (!bytes) return CTCPB_ENULL;
-  const Shape s = shape_of(N, H, 16);
+  const Shape s = shape_of(N, H, true, true);  // the most blocks of either kind
   *bytes = align_up((size_t)(s.blocks > 0 ? s.blocks : 1) * 2 * H * 4, 256);
   return CTCPB_OK;
 }
@@ -538,7 +549,9 @@ int ctcpb_layer_norm_backward(int type, int param_type, const void* dy, int64_t 
     if (((uintptr_t)ws & 255u) != 0) return CTCPB_EALIGN;
     if (ws_bytes < need) return CTCPB_ESIZE;
   }
-  const Shape s = shape_of(N, H, 16);
+  const bool vec = H % (type == CTCPB_F32 ? 4 : 8) == 0 && vec_ok(type, x, ldx) && vec_ok(type, dy, lddy) &&
+                   (!dx || vec_ok(type, dx, lddx));
+  const Shape s = shape_of(N, H, vec, true);
   cudaStream_t st = (cudaStream_t)stream;
   if (N > 0) {
     NormArgs a{};
@@ -555,8 +568,6 @@ int ctcpb_layer_norm_backward(int type, int param_type, const void* dy, int64_t 
     a.mean = const_cast<float*>(mean);
     a.rstd = const_cast<float*>(rstd);
     a.part = cols ? (float*)ws : nullptr;
-    const bool vec = H % (type == CTCPB_F32 ? 4 : 8) == 0 && vec_ok(type, x, ldx) && vec_ok(type, dy, lddy) &&
-                     (!dx || vec_ok(type, dx, lddx));
     if (run(type, true, vec, a, s, st) != cudaSuccess) return CTCPB_ECUDA;
   }
   if (cols) {
