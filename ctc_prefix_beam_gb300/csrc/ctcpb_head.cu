@@ -26,7 +26,9 @@
 namespace ctcpb {
 namespace {
 
-enum Mode { kStats = 0, kLogp = 1, kDlogits = 2, kProduct = 3, kBand = 4 };
+enum Mode { kStats = 0, kLogp = 1, kDlogits = 2, kProduct = 3, kBand = 4, kDx = 5, kDw = 6 };
+// kDx, kDw: one of the two products
+__host__ __device__ constexpr bool is_product(int mode) { return mode == kProduct || mode == kDx || mode == kDw; }
 
 constexpr int kEpiWarps = 16;      // 4 for each quarter of a tile's 256 columns
 constexpr int kThreads = 128 + 32 * kEpiWarps;
@@ -47,9 +49,9 @@ struct GemmArgs {
   int rows;             // ... or its bound
   int M, N, K;          // output rows and columns, depth; the row count replaces M (K in d^T x)
   int bn;               // columns of a tile
+  int none;             // 1: this gradient is not wanted, 2: not of this launch
   int stages;
   int group;            // row tiles that share a sweep over the columns
-  int split;            // share the last, partial wave of tiles along K
   int col0;             // first vocabulary entry of the piece
   // logits
   const void* bias;
@@ -80,60 +82,76 @@ struct GemmArgs {
   int members, bands;   // workers that share a row tile; row tiles worked on at once
 };
 
+// What a launch works on: one product, or dx and dw.  The maps are of the
+// operands and of the output, where tiled copies write it.
+template <int MODE>
+struct Params {
+  static constexpr int kProblems = is_product(MODE) ? 2 : 1;
+  CUtensorMap a[kProblems], b[kProblems], o;
+  GemmArgs g[kProblems];
+};
+
 // ---------------------------------------------------------------- tiles and their split
 
-// A worker (block or pair) takes whole tiles in waves; the last wave, if it
-// would leave workers idle, is cut along K into equal shares instead.  A share
-// is at most one tile's depth, so it touches at most two tiles; its sums go to
-// slots 2w, 2w+1, and k_finish adds a tile's shares in order.
+// A worker (block or pair) takes whole tiles in waves.  dx and dw may be one
+// launch: the tiles of the second follow those of the first.  What is left of
+// either, less than a wave, would leave workers idle: it is laid end to end and
+// cut along K into equal shares.  A share begins or ends inside a tile at most
+// once each; its sums there go to slots 2w (the part it begins with) and 2w + 1,
+// and k_finish adds a tile's parts in order.
 struct Seg {
-  int m, n, tile, k0, k1, slot;  // slot -1: the whole depth
+  int p, m, n, tile, k0, k1, slot;  // problem; slot -1: the whole depth
 };
+template <int P>
 struct Sched {
-  int mt, nt, ks, group, tiles, dp, rem, nw, w, G, t, first;
-  int u, u1;
-  int members, band, bands;  // kBand: this worker's column tile is w % members; the next row tile, and the step
-  int part, odd;  // a share's slices: part + 1 for the first `odd` workers, then part
+  int mt[P], nt[P], ks[P], group[P], dp[P], rem[P];
+  bool off[P];                  // not wanted: its tiles are passed over (the others' split stays what it is)
+  int w, G, t, u, u1, nw;
+  int part, odd;                // a share's slices: part + 1 for the first `odd` workers, then part
+  int members, band, bands;     // kBand: this worker's column tile is w % members; the next row tile, and the step
   __device__ int share(int i) const { return part * i + (i < odd ? i : odd); }  // the first slice of worker i's share
   __device__ int worker_of(int slice) const {
     const int big = odd * (part + 1);
     return slice < big ? slice / (part + 1) : odd + (slice - big) / part;
   }
-  __device__ void init(const GemmArgs& a, int cg, int worker, int workers) {
-    const int rows = a.rows_dev ? *a.rows_dev : a.rows;
-    const bool rows_k = a.M > 0;  // M given: the rows are the depth
-    const int M = rows_k ? a.M : rows, K = rows_k ? rows : a.K;
-    mt = (M + 128 * cg - 1) / (128 * cg);
-    if (mt < 1) mt = 1;
-    nt = (a.N + a.bn - 1) / a.bn;
-    ks = (K + 63) / 64;
-    if (ks < 1) ks = 1;
-    group = a.group < mt ? a.group : mt;
-    tiles = mt * nt;
+  __device__ void init(const GemmArgs (&g)[P], int cg, int worker, int workers) {
     G = workers;
     w = worker;
-    dp = tiles;
-    rem = 0;
-    nw = 1;
-    if (a.split && ks >= kSplitDepth) {
-      rem = tiles % G;
-      if (5 * rem > 4 * G) rem = 0;  // a nearly full wave: joining would cost more than it gives
-      dp = tiles - rem;
-      nw = rem * ks / 4;  // at least 4 slices of K a share
-      if (nw > G) nw = G;
-      if (nw < rem) nw = rem;
-      if (nw < 1) nw = 1;
+    int slices = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const GemmArgs& a = g[i];
+      off[i] = a.none != 0;
+      dp[i] = rem[i] = 0;
+      mt[i] = nt[i] = ks[i] = group[i] = 1;
+      if (a.none == 2) continue;
+      const int rows = a.rows_dev ? *a.rows_dev : a.rows;
+      const bool rows_k = a.M > 0;  // M given: the rows are the depth
+      const int M = rows_k ? a.M : rows, K = rows_k ? rows : a.K;
+      mt[i] = M > 0 ? (M + 128 * cg - 1) / (128 * cg) : 1;
+      nt[i] = (a.N + a.bn - 1) / a.bn;
+      ks[i] = K > 0 ? (K + 63) / 64 : 1;
+      group[i] = a.group < mt[i] ? a.group : mt[i];
+      const int tiles = mt[i] * nt[i];
+      if (P > 1 && ks[i] >= kSplitDepth) {
+        rem[i] = tiles % G;
+        if (5 * rem[i] > 4 * G) rem[i] = 0;  // a nearly full wave: joining would cost more than it gives
+      }
+      dp[i] = tiles - rem[i];
+      slices += rem[i] * ks[i];
     }
-    part = rem * ks / nw;
-    odd = rem * ks - part * nw;
+    nw = slices / 4;  // at least 4 slices of K a share
+    if (nw > G) nw = G;
+    if (nw < 1) nw = 1;
+    part = slices / nw;
+    odd = slices - part * nw;
     t = w;
     u = w < nw ? share(w) : 0;
     u1 = w < nw ? share(w + 1) : 0;
-    first = ks > 0 ? u / ks : 0;
-    members = a.members;
+    members = g[0].members;
     if (members > 0) {
-      bands = a.bands;
-      band = w < members * bands ? w / members : mt;
+      bands = g[0].bands;
+      band = w < members * bands ? w / members : mt[0];
     }
   }
   // kBand: every other band, from the second on if `turn`
@@ -141,40 +159,53 @@ struct Sched {
     band += turn * bands;
     bands *= 2;
   }
-  __device__ void place(int tile, Seg& s) const {
-    const int per = group * nt, g = tile / per, in = tile - g * per;
-    const int gs = mt - g * group < group ? mt - g * group : group;
+  __device__ void place(int i, int tile, Seg& s) const {
+    const int per = group[i] * nt[i], g = tile / per, in = tile - g * per;
+    const int gs = mt[i] - g * group[i] < group[i] ? mt[i] - g * group[i] : group[i];
+    s.p = i;
     s.tile = tile;
     s.n = in / gs;
-    s.m = g * group + in - s.n * gs;
+    s.m = g * group[i] + in - s.n * gs;
   }
+  // the first slice of problem i's tile r of those that are cut
+  __device__ int slice_of(int i, int r) const { return (i ? rem[0] * ks[0] : 0) + r * ks[i]; }
   __device__ bool next(Seg& s) {
-    if (members > 0) {
-      if (band >= mt) return false;
+    s.slot = -1;
+    s.k0 = 0;
+    if (P == 1 && members > 0) {
+      if (band >= mt[0]) return false;
+      s.p = s.tile = 0;
       s.m = band;
       s.n = w % members;
-      s.tile = 0;
-      s.k0 = 0;
-      s.k1 = ks;
-      s.slot = -1;
+      s.k1 = ks[0];
       band += bands;
       return true;
     }
-    if (t < dp) {
-      place(t, s);
-      s.k0 = 0;
-      s.k1 = ks;
-      s.slot = -1;
+    const int whole = P > 1 ? dp[0] + dp[P - 1] : dp[0];
+    while (t < whole) {
+      const int i = P > 1 && t >= dp[0] ? 1 : 0, tile = i ? t - dp[0] : t;
       t += G;
+      if (off[i ? P - 1 : 0]) continue;
+      if (i)
+        place(P - 1, tile, s);
+      else
+        place(0, tile, s);
+      s.k1 = i ? ks[P - 1] : ks[0];
       return true;
     }
-    if (u < u1) {
-      const int r = u / ks;
-      place(dp + r, s);
-      s.k0 = u - r * ks;
-      s.k1 = s.k0 + (u1 - u) < ks ? s.k0 + (u1 - u) : ks;
-      s.slot = (s.k0 == 0 && s.k1 == ks) ? -1 : 2 * w + (r - first);
+    while (u < u1) {
+      const int i = P > 1 && u >= rem[0] * ks[0] ? 1 : 0;
+      const int at = i ? u - rem[0] * ks[0] : u, depth = i ? ks[P - 1] : ks[0], r = at / depth;
+      const int begin = u;
+      s.k0 = at - r * depth;
+      s.k1 = s.k0 + (u1 - u) < depth ? s.k0 + (u1 - u) : depth;
       u += s.k1 - s.k0;
+      if (off[i ? P - 1 : 0]) continue;
+      if (i)
+        place(P - 1, dp[P - 1] + r, s);
+      else
+        place(0, dp[0] + r, s);
+      if (s.k0 > 0 || s.k1 < depth) s.slot = 2 * w + (begin == share(w) ? 0 : 1);
       return true;
     }
     return false;
@@ -297,7 +328,7 @@ __device__ __forceinline__ float2 join_sums(const float2 (&p)[K]) {
 }
 
 template <int CG, class W>
-__device__ void band_epilogue(const GemmArgs& a, Sched sc, char* smem, u32 tmem, u32 s_tfull, u32 s_tempty, u32 rank,
+__device__ void band_epilogue(const GemmArgs& a, Sched<1> sc, char* smem, u32 tmem, u32 s_tfull, u32 s_tempty, u32 rank,
                               const CUtensorMap* map_o, volatile u32* dead, W& wait) {
   // two sets of eight warps take the bands in turn: one's waits and copies are
   // under the other's arithmetic.  A warp has 32 rows and half the columns.
@@ -452,10 +483,13 @@ __device__ void band_epilogue(const GemmArgs& a, Sched sc, char* smem, u32 tmem,
 
 // Shared memory: a ring of operand tiles, the epilogue warps' buffers, the
 // barriers.
-template <int MODE, class T, bool AMN, bool BMN, int CG>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-           const __grid_constant__ CUtensorMap map_o, const GemmArgs a) {
+template <int MODE, class T, int CG>
+__global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Params<MODE> prm) {
+  constexpr int P = Params<MODE>::kProblems;
+  constexpr bool BMN = is_product(MODE);  // the second operand has its rows along K
+  auto problem = [](const Seg& g) { return MODE == kDx || P == 1 ? 0 : MODE == kDw ? 1 : g.p; };
+  const GemmArgs& a = prm.g[0];           // (what both products share)
+  const CUtensorMap& map_o = prm.o;
   extern __shared__ __align__(1024) char smem[];
   char* const ctl = smem + kTileBytes + kEpiBytes;
   const u32 s_tiles = saddr(smem);
@@ -471,8 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const u32 stage_bytes = 16384u + (u32)bnb * 128u;
 
   if (threadIdx.x == 0) {
-    tma_prefetch_map(&map_a);
-    tma_prefetch_map(&map_b);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      tma_prefetch_map(&prm.a[i]);
+      tma_prefetch_map(&prm.b[i]);
+    }
     if ((MODE == kLogp || MODE == kDlogits || MODE == kBand) && a.tiled) tma_prefetch_map(&map_o);
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init_n(s_full + 8 * i, 1);
@@ -507,14 +544,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     return false;
   };
 
-  Sched sc;
-  sc.init(a, CG, worker, workers);
+  Sched<P> sc;
+  sc.init(prm.g, CG, worker, workers);
   Seg sg;
   bool ok = true;
 
   if constexpr (MODE == kBand) {
     if (a.members > 1) {  // nobody reads a pair before its owner has marked it as not there
-      Sched mine = sc;
+      Sched<P> mine = sc;
       while (mine.next(sg))
         if (threadIdx.x < 128)
           reinterpret_cast<u64*>(a.part)[(((long long)sg.m * CG + rank) * a.members + sg.n) * 128 + threadIdx.x] = kNoPair;
@@ -528,21 +565,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       u32 ph = 1;
       const u32 full0 = CG == 2 ? cluster_addr(s_full, 0) : s_full;
       while (ok && sc.next(sg)) {
-        const int m0 = (sg.m * CG + (int)rank) * 128, n0 = sg.n * a.bn + (int)rank * bnb;
+        const int m0 = (sg.m * CG + (int)rank) * 128, n0 = sg.n * a.bn + (int)rank * bnb, col0 = prm.g[problem(sg)].col0;
+        const CUtensorMap *map_a = &prm.a[problem(sg)], *map_b = &prm.b[problem(sg)];
+        const bool amn = problem(sg) == 1;  // d^T: its columns are the rows, and contiguous
         for (int k = sg.k0; k < sg.k1; ++k) {
           if (!(ok = wait(s_empty + 8 * st, ph))) break;
           const u32 at = s_tiles + (u32)st * stage_bytes, bt = at + 16384u, bar = full0 + 8 * st;
           if (rank == 0) mbar_expect(s_full + 8 * st, stage_bytes * CG);
-          if constexpr (!AMN) {
-            tma_load<CG>(at, &map_a, k * 64, m0, bar);
+          if (!amn) {
+            tma_load<CG>(at, map_a, k * 64, m0, bar);
           } else {
-            tma_load<CG>(at, &map_a, m0, k * 64, bar);
-            tma_load<CG>(at + 8192u, &map_a, m0 + 64, k * 64, bar);
+            tma_load<CG>(at, map_a, m0, k * 64, bar);
+            tma_load<CG>(at + 8192u, map_a, m0 + 64, k * 64, bar);
           }
           if constexpr (!BMN) {
-            tma_load<CG>(bt, &map_b, k * 64, a.col0 + n0, bar);
+            tma_load<CG>(bt, map_b, k * 64, col0 + n0, bar);
           } else {
-            for (int j = 0; j < bnb; j += 64) tma_load<CG>(bt + (u32)j * 128u, &map_b, n0 + j, a.col0 + k * 64, bar);
+            for (int j = 0; j < bnb; j += 64) tma_load<CG>(bt + (u32)j * 128u, map_b, n0 + j, col0 + k * 64, bar);
           }
           if (++st == a.stages) {
             st = 0;
@@ -556,21 +595,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && rank == 0) {  // ---- matrix instructions
       int st = 0, as = 0;
       u32 ph = 0, aph = 1;
-      const u32 idesc = mma_idesc(Elem<T>::kFormat, AMN, BMN, 128 * CG, a.bn);
-      constexpr u64 kStepA = AMN ? 2048 >> 4 : 32 >> 4, kStepB = BMN ? 2048 >> 4 : 32 >> 4;
+      constexpr u64 kStepB = BMN ? 2048 >> 4 : 32 >> 4;
       bool more = sc.next(sg);
       while (more) {
         if (!(ok = wait(s_tempty + 8 * as, aph))) break;
         tc_fence_after();
         const u32 d = tmem + 256u * as;
         const int k0 = sg.k0, k1 = sg.k1;
+        const bool amn = problem(sg) == 1;
+        const u32 idesc = mma_idesc(Elem<T>::kFormat, amn, BMN, 128 * CG, a.bn);
+        const u64 step_a = amn ? 2048 >> 4 : 32 >> 4;
         for (int k = k0; k < k1; ++k) {
           if (!(ok = wait(s_full + 8 * st, ph))) break;
           tc_fence_after();
           const u32 at = s_tiles + (u32)st * stage_bytes;
-          const u64 da = smem_desc(at, AMN ? 8192 : 16), db = smem_desc(at + 16384u, BMN ? 8192 : 16);
+          const u64 da = smem_desc(at, amn ? 8192 : 16), db = smem_desc(at + 16384u, BMN ? 8192 : 16);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma_f16<CG>(d, da + i * kStepA, db + i * kStepB, idesc, k > k0 || i > 0);
+          for (int i = 0; i < 4; ++i) mma_f16<CG>(d, da + i * step_a, db + i * kStepB, idesc, k > k0 || i > 0);
           mma_commit<CG>(s_empty + 8 * st);
           if (++st == a.stages) {
             st = 0;
@@ -588,14 +629,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (MODE == kBand && warp >= 4) {
-    band_epilogue<CG>(a, sc, smem, tmem, s_tfull, s_tempty, rank, &map_o, dead, wait);
+    if constexpr (MODE == kBand) band_epilogue<CG>(a, sc, smem, tmem, s_tfull, s_tempty, rank, &map_o, dead, wait);
   } else if (MODE != kBand && warp >= 4) {  // ---- epilogue: a warp's 32 rows and 64 columns of a tile
     const int q = warp & 3, u = ((warp - 4) >> 2) * 64;
     char* const buf = smem + kTileBytes + (warp - 4) * kStageBuf;
     float* const bias_s = reinterpret_cast<float*>(smem + kTileBytes + kEpiWarps * kStageBuf) + (warp - 4) * 32;
     const u32 tempty0 = CG == 2 ? cluster_addr(s_tempty, 0) : s_tempty;
     const int rows = a.rows_dev ? *a.rows_dev : a.rows;
-    const int mrows = a.M > 0 ? a.M : rows;
     const bool store_tiled = (MODE == kLogp || MODE == kDlogits) && a.tiled;
     // what a tile's rows and columns bring, read while the tile before it is worked on
     struct Given {
@@ -605,9 +645,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto read = [&](const Seg& g) {
       Given w{{0.f, 0.f}, 0.f, 0.f, -1, -1};
       const int row = (g.m * CG + (int)rank) * 128 + q * 32 + lane, n0 = g.n * a.bn;
+      const int mrows = problem(g) == 1 ? prm.g[P - 1].M : rows;
       if (row < mrows) w.orow = row;
-      if constexpr (MODE == kProduct) {
-        if (a.rowmap && row < mrows) w.orow = a.rowmap[row];
+      if constexpr (is_product(MODE)) {
+        const int* const rowmap = prm.g[problem(g)].rowmap;
+        if (rowmap && row < mrows) w.orow = rowmap[row];
       } else {
         // a column past the vocabulary gets -inf, so that its exponential is 0
 #pragma unroll
@@ -628,6 +670,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool more = sc.next(sg);
     Given w = more ? read(sg) : Given{};
     while (more) {
+      const GemmArgs& a = prm.g[problem(sg)];
+      const int mrows = rows;  // (of the logits; a product's rows are in orow)
       const int mtile = sg.m * CG + (int)rank;
       const int row0 = mtile * 128 + q * 32, row = row0 + lane, n0 = sg.n * a.bn;
       // the columns that this tile writes end here (kDlogits fills its piece's width)
@@ -660,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float v[32];
         if (c0 < a.bn) {
           tmem_load32(v, d + c0);
-          if constexpr (MODE != kProduct) {
+          if constexpr (!is_product(MODE)) {
             bias_s[lane] = bq[j];
             __syncwarp();
           }
@@ -669,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
-        if constexpr (MODE != kProduct) {
+        if constexpr (!is_product(MODE)) {
           // to base 2 (but for kLogp), so that exp and log cost nothing more: z log2(e) + b log2(e)
           if (c0 < a.bn) {
             const float4* b4 = reinterpret_cast<const float4*>(bias_s);
@@ -797,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) tma_store(&map_o, n0 + u, row0, saddr(buf));
         }
       }
-      if constexpr (MODE == kProduct) {
+      if constexpr (is_product(MODE)) {
         if (busy && slot < 0 && a.last) flush_rows<T>(buf, lane, (T*)a.out, a.ldo, orow, n0 + u, a.N, a.vec);
       }
     }
@@ -826,13 +870,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // tile's output written: a block per 32 rows and 64 columns, 8 columns a warp
 // (16 bytes of each row), two shares' loads in flight.
 template <class T>
-__device__ void join_tile(const GemmArgs& a, const Sched& sc, int cg, int r, int unit, char* buf) {
+__device__ void join_tile(const GemmArgs& a, const Sched<2>& sc, int i, int cg, int r, int unit, char* buf) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int lo = r * sc.ks, hi = lo + sc.ks;
+  const int lo = sc.slice_of(i, r), hi = lo + sc.ks[i];
   const int w = sc.worker_of(lo);
   if (sc.share(w) <= lo && sc.share(w + 1) >= hi) return;  // one share: written by the matrix kernel
   Seg sg;
-  sc.place(sc.dp + r, sg);
+  sc.place(i, sc.dp[i] + r, sg);
   const int q = unit & 3, rank = (unit >> 2) % cg, u = (unit >> 2) / cg * 64;
   const int n0 = sg.n * a.bn;
   if (n0 + u >= a.N) return;
@@ -848,7 +892,7 @@ __device__ void join_tile(const GemmArgs& a, const Sched& sc, int cg, int r, int
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  auto slot_of = [&](int x) { return a.slots + ((2ll * x + (r - sc.share(x) / sc.ks)) * cg + rank) * tile + at; };
+  auto slot_of = [&](int x) { return a.slots + ((2ll * x + (sc.share(x) >= lo ? 0 : 1)) * cg + rank) * tile + at; };
   for (int x = w; x < sc.nw && sc.share(x) < hi; x += 2) {
     const bool two = x + 1 < sc.nw && sc.share(x + 1) < hi;
     const float *o = slot_of(x), *p = two ? slot_of(x + 1) : o;
@@ -899,8 +943,8 @@ __device__ void join_tile(const GemmArgs& a, const Sched& sc, int cg, int r, int
 }
 
 struct FinishArgs {
-  GemmArgs g[2];               // the two products, for their joins
-  int cg[2], workers[2], units[2];  // units of a tile (0: nothing to join)
+  GemmArgs g[2][2];              // what each launch of the products worked on
+  int runs, cg, workers, units;  // launches (0: nothing to join), units of a tile
   // db of a piece: the column sums of d over the row tiles
   const float* dbp;
   long long ld;
@@ -919,15 +963,16 @@ __global__ void __launch_bounds__(256, 5) k_finish(const FinishArgs f) {
   __shared__ __align__(16) char buf[kStageBuf];
   pdl_wait();
   pdl_next();
-  Sched sc[2];
-  int joins[2] = {0, 0};
+  Sched<2> sc[2];
+  int joins[2][2] = {{0, 0}, {0, 0}}, total = f.bias_units;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (f.units[i] > 0) {
-      sc[i].init(f.g[i], f.cg[i], 0, f.workers[i]);
-      joins[i] = sc[i].rem * f.units[i];
+  for (int r = 0; r < 2; ++r)
+    if (r < f.runs) {
+      sc[r].init(f.g[r], f.cg, 0, f.workers);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) total += joins[r][i] = sc[r].off[i] ? 0 : sc[r].rem[i] * f.units;
     }
-  for (int b = blockIdx.x; b < f.bias_units + joins[0] + joins[1]; b += gridDim.x) {
+  for (int b = blockIdx.x; b < total; b += gridDim.x) {
     if (b < f.bias_units) {
       float(*red)[32] = reinterpret_cast<float(*)[32]>(buf);
       const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -949,12 +994,15 @@ __global__ void __launch_bounds__(256, 5) k_finish(const FinishArgs f) {
         for (int w = 1; w < 8; ++w) s += red[w][lane];
         store_elem(f.db, f.type, (long long)f.col0 + c, s * *f.scale);
       }
-    } else if (b < f.bias_units + joins[0]) {
-      const int k = b - f.bias_units;
-      join_tile<T>(f.g[0], sc[0], f.cg[0], k / f.units[0], k % f.units[0], buf);
     } else {
-      const int k = b - f.bias_units - joins[0];
-      join_tile<T>(f.g[1], sc[1], f.cg[1], k / f.units[1], k % f.units[1], buf);
+      int k = b - f.bias_units;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (k >= 0 && k < joins[r][i]) join_tile<T>(f.g[r][i], sc[r], i, f.cg, k / f.units, k % f.units, buf);
+          k -= joins[r][i];
+        }
     }
     __syncthreads();  // the buffer is used again
   }
@@ -1289,22 +1337,33 @@ bool make_map(CUtensorMap* m, int type, const void* base, long long inner, long 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, class T, bool AMN, bool BMN, int CG>
-cudaError_t launch_gemm_t(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo, const GemmArgs& a, int blocks,
-                          cudaStream_t s) {
-  constexpr auto kern = k_gemm<MODE, T, AMN, BMN, CG>;
+template <int MODE>
+Params<MODE> as_mode(const Params<kProduct>& p) {
+  return {{p.a[0], p.a[1]}, {p.b[0], p.b[1]}, p.o, {p.g[0], p.g[1]}};
+}
+template <int MODE, class T, int CG>
+cudaError_t launch_gemm_t(const Params<MODE>& prm, int blocks, cudaStream_t s) {
+  constexpr auto kern = k_gemm<MODE, T, CG>;
   cudaError_t e = smem_optin<kern>(kSmem);
   if (e != cudaSuccess) return e;
-  return launch_as(MODE == kBand, kern, dim3(blocks), kThreads, kSmem, s, CG, ma, mb, mo, a);
+  return launch_as(MODE == kBand, kern, dim3(blocks), kThreads, kSmem, s, CG, prm);
 }
-template <int MODE, bool AMN, bool BMN>
+template <int MODE>
+cudaError_t launch_gemm(int type, int cg, const Params<MODE>& prm, int blocks, cudaStream_t s) {
+  if (cg == 2)
+    return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, 2>(prm, blocks, s)
+                              : launch_gemm_t<MODE, __half, 2>(prm, blocks, s);
+  return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, 1>(prm, blocks, s) : launch_gemm_t<MODE, __half, 1>(prm, blocks, s);
+}
+template <int MODE>
 cudaError_t launch_gemm(int type, int cg, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
                         const GemmArgs& a, int blocks, cudaStream_t s) {
-  if (cg == 2)
-    return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, AMN, BMN, 2>(ma, mb, mo, a, blocks, s)
-                              : launch_gemm_t<MODE, __half, AMN, BMN, 2>(ma, mb, mo, a, blocks, s);
-  return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, AMN, BMN, 1>(ma, mb, mo, a, blocks, s)
-                            : launch_gemm_t<MODE, __half, AMN, BMN, 1>(ma, mb, mo, a, blocks, s);
+  Params<MODE> prm;
+  prm.a[0] = ma;
+  prm.b[0] = mb;
+  prm.o = mo;
+  prm.g[0] = a;
+  return launch_gemm<MODE>(type, cg, prm, blocks, s);
 }
 
 constexpr int kWorkers = 152;  // SMs; the split wave's slots are sized by it
@@ -1488,12 +1547,6 @@ CeLayout ce_layout(long long N, int V, int H, bool backward) {
   return l;
 }
 
-// Whether a product may leave shares to join, by the most tiles and the most
-// depth it can have (its row count is on the device).
-bool may_split(const GemmArgs& a, long long max_tiles) {
-  return max_tiles > 0 && (a.M > 0 ? a.rows : a.K) > 64 * (kSplitDepth - 1);
-}
-
 }  // namespace
 }  // namespace ctcpb
 
@@ -1555,7 +1608,7 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
     a.members = p.members;
     a.bands = p.bands;
     a.reset_status = 1;
-    const cudaError_t e = launch_gemm<kBand, false, false>(type, p.cg, ma, mb, mo, a, p.cg * p.members * p.bands, s);
+    const cudaError_t e = launch_gemm<kBand>(type, p.cg, ma, mb, mo, a, p.cg * p.members * p.bands, s);
     if (e == cudaSuccess) return CTCPB_OK;
     if (e != cudaErrorCooperativeLaunchTooLarge && e != cudaErrorNotSupported) return CTCPB_ECUDA;
     (void)cudaGetLastError();  // the blocks cannot all be resident here: two passes
@@ -1573,7 +1626,7 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   a.reset_status = 1;
   const long long tiles = (N + 128 * cg - 1) / (128 * cg) * l.nt;
   const int blocks = cg * (int)(tiles < sms / cg ? tiles : sms / cg);
-  TRY((launch_gemm<kStats, false, false>(type, cg, ma, mb, ma, a, blocks, s)));
+  TRY((launch_gemm<kStats>(type, cg, ma, mb, ma, a, blocks, s)));
   a.reset_status = 0;
   CombineArgs c{};
   c.rows = (int)N;
@@ -1584,7 +1637,7 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   TRY(launch(k_combine, (unsigned)((N + 31) / 32), 32 * kSlices, 0, s, 1, c));
   a.factor = factor_of(H, 1.0);
   a.group = 1;  // neighbours write neighbouring columns
-  TRY((launch_gemm<kLogp, false, false>(type, cg, ma, mb, mo, a, blocks, s)));
+  TRY((launch_gemm<kLogp>(type, cg, ma, mb, mo, a, blocks, s)));
   return CTCPB_OK;
 }
 
@@ -1678,7 +1731,7 @@ int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, con
   a.status = r.status;
   const long long tiles = l.Np / (128 * cg) * l.nt;
   const int sms = sm_count();
-  TRY((launch_gemm<kStats, false, false>(type, cg, ma, mb, ma, a, cg * (int)(tiles < sms / cg ? tiles : sms / cg), s)));
+  TRY((launch_gemm<kStats>(type, cg, ma, mb, ma, a, cg * (int)(tiles < sms / cg ? tiles : sms / cg), s)));
   CombineArgs c{};
   c.rows_dev = r.nv;
   c.part = a.part;
@@ -1757,8 +1810,9 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
     a.dbp = dbias ? (float*)(b + l.o_dbp) : nullptr;
     a.status = r.status;
     long long tiles = l.Np / (128 * cg) * ((cols + l.bn - 1) / l.bn);
-    TRY((launch_gemm<kDlogits, false, false>(type, cg, ma, mb, mo, a, cg * (int)(tiles < sms / cg ? tiles : sms / cg), s)));
+    TRY((launch_gemm<kDlogits>(type, cg, ma, mb, mo, a, cg * (int)(tiles < sms / cg ? tiles : sms / cg), s)));
     FinishArgs f{};
+    long long left = 0;
     if (dbias) {
       f.dbp = a.dbp;
       f.ld = l.piece;
@@ -1767,70 +1821,85 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
       f.cols = cols;
       f.col0 = v0;
       f.type = bias_type;
-      f.bias_units = (cols + 31) / 32;
+      left = f.bias_units = (cols + 31) / 32;
       f.scale = r.scale;
       f.db = dbias;
     }
-    long long left = f.bias_units;
-    auto join = [&](int i, const GemmArgs& g, int cgp, long long max_tiles) {
-      if (!may_split(g, max_tiles)) return;
-      f.g[i] = g;
-      f.cg[i] = cgp;
-      f.workers[i] = sms / cgp;
-      f.units[i] = cgp * 4 * ((g.bn + 63) / 64);
-      left += (max_tiles < f.workers[i] ? max_tiles : f.workers[i]) * f.units[i];
-    };
-    if (dx && N > 0) {  // dx (+)= d w[piece]
-      const int cgp = pair_of(N, l.pbn);
-      if (!make_map(&ma, type, b + l.o_d, l.piece, l.Np, l.piece, 128) || !make_map(&mb, type, weight, l.Hp, V, ldw, 64))
-        return CTCPB_ECUDA;
+    if ((dx && N > 0) || dweight) {
+      // pairs where either product fills their tiles
+      const int cgp = pair_of(N > cols ? N : cols, l.pbn), workers = sms / cgp;
+      Params<kProduct> prm{};
       GemmArgs g{};
       g.rows_dev = r.nv;
       g.rows = (int)N;
       g.N = H;
-      g.K = cols;
-      g.bn = l.pbn;
       g.stages = stages_of(l.pbn, cgp);
-      g.group = group_of(l.piece, cgp);
-      g.split = 1;
-      g.col0 = v0;
-      g.out = dx;
-      g.ldo = lddx;
-      g.vec = rows_aligned(dx, lddx);
       g.scale = r.scale;
-      g.rowmap = r.rowmap;
       g.slots = (float*)(b + l.o_slots[0]);
-      g.acc = l.pieces > 1 ? (float*)(b + l.o_acc) : nullptr;
-      g.first = p == 0;
-      g.last = p == l.pieces - 1;
       g.status = r.status;
-      TRY((launch_gemm<kProduct, false, true>(type, cgp, ma, mb, ma, g, sms / cgp * cgp, s)));
-      tiles = l.Np / (128 * cgp) * ((H + l.pbn - 1) / l.pbn);
-      join(0, g, cgp, tiles);
-    }
-    if (dweight) {  // dw[piece] = d^T x
-      const int cgp = pair_of(cols, l.pbn);
-      if (!make_map(&ma, type, b + l.o_d, l.piece, l.Np, l.piece, 64) || !make_map(&mb, type, r.xg, l.Hp, l.Np, l.Hp, 64))
-        return CTCPB_ECUDA;
-      GemmArgs g{};
-      g.rows_dev = r.nv;
-      g.rows = (int)N;
-      g.M = cols;
-      g.N = H;
       g.bn = l.pbn;
-      g.stages = stages_of(l.pbn, cgp);
-      g.group = 8;
-      g.split = 1;
-      g.out = (u16*)dweight + (long long)v0 * lddw;
-      g.ldo = lddw;
-      g.vec = rows_aligned(g.out, lddw);
-      g.scale = r.scale;
-      g.slots = (float*)(b + l.o_slots[1]);
-      g.first = g.last = 1;
-      g.status = r.status;
-      TRY((launch_gemm<kProduct, true, true>(type, cgp, ma, mb, ma, g, sms / cgp * cgp, s)));
-      tiles = (long long)((cols + 128 * cgp - 1) / (128 * cgp)) * ((H + l.pbn - 1) / l.pbn);
-      join(1, g, cgp, tiles);
+      prm.g[0] = prm.g[1] = g;
+      {  // dx (+)= d w[piece]
+        GemmArgs& q = prm.g[0];
+        q.none = !(dx && N > 0);
+        q.K = cols;
+        q.group = group_of(l.piece, cgp);
+        q.col0 = v0;
+        q.out = dx;
+        q.ldo = lddx;
+        q.vec = rows_aligned(dx, lddx);
+        q.rowmap = r.rowmap;
+        q.acc = l.pieces > 1 ? (float*)(b + l.o_acc) : nullptr;
+        q.first = p == 0;
+        q.last = p == l.pieces - 1;
+        if (!make_map(&prm.a[0], type, b + l.o_d, l.piece, l.Np, l.piece, 128) ||
+            !make_map(&prm.b[0], type, weight, l.Hp, V, ldw, 64))
+          return CTCPB_ECUDA;
+      }
+      {  // dw[piece] = d^T x
+        GemmArgs& q = prm.g[1];
+        q.none = !dweight;
+        q.M = cols;
+        q.group = 8;
+        q.out = dweight ? (u16*)dweight + (long long)v0 * lddw : nullptr;
+        q.ldo = lddw;
+        q.vec = rows_aligned(q.out, lddw);
+        q.first = q.last = 1;
+        if (!make_map(&prm.a[1], type, b + l.o_d, l.piece, l.Np, l.piece, 64) ||
+            !make_map(&prm.b[1], type, r.xg, l.Hp, l.Np, l.Hp, 64))
+          return CTCPB_ECUDA;
+      }
+      prm.o = prm.a[0];  // (not used)
+      // One launch where the tiles are few waves: one tail instead of two
+      // (12000 x 5000 x 512: 93 us apart, 88 together).  With more, each its own:
+      // the waves of either share what they read (8192 x 65536 x 2048 with all
+      // its gradients: 5.27 ms apart, 5.50 together).
+      const long long mt = (N > 0 ? N : 1), nt = (H + l.pbn - 1) / l.pbn, rows = 128 * cgp;
+      const bool apart = ((mt + rows - 1) / rows + (cols + rows - 1) / rows) * nt > 4ll * workers;
+      f.runs = 0;
+      for (int run = 0; run < (apart ? 2 : 1); ++run) {
+        Params<kProduct> q = prm;
+        if (apart) {
+          if (q.g[run].none) continue;
+          q.g[1 - run].none = 2;
+          q.g[run].slots = (float*)(b + l.o_slots[run]);
+        }
+        TRY(!apart     ? launch_gemm<kProduct>(type, cgp, q, workers * cgp, s)
+            : run == 0 ? launch_gemm<kDx>(type, cgp, as_mode<kDx>(q), workers * cgp, s)
+                       : launch_gemm<kDw>(type, cgp, as_mode<kDw>(q), workers * cgp, s));
+        f.g[f.runs][0] = q.g[0];
+        f.g[f.runs][1] = q.g[1];
+        ++f.runs;
+      }
+      // shares to join: none if neither depth (on the device, for d^T x) can be cut
+      if (cols > 64 * (kSplitDepth - 1) || N > 64 * (kSplitDepth - 1)) {
+        f.cg = cgp;
+        f.workers = workers;
+        f.units = cgp * 4 * ((l.pbn + 63) / 64);
+        left += 2ll * workers * f.units;
+      } else {
+        f.runs = 0;
+      }
     }
     const unsigned most = 10u * kWorkers, blocks = left < most ? (unsigned)left : most;
     if (left > 0)
