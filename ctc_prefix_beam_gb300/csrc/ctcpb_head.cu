@@ -10,12 +10,11 @@
 //   kBand     both at once: a band of rows stays in the tensor memory of the
 //             blocks that share it until its lse is known
 //   kDlogits  d = (exp(z - lse) - [c = target]) r   16 bits, a piece of V
-//   kProduct  dx += d w  and  dw = d^T x
+//   kProduct  dx += d w  and  dw = d^T x  (kDx, kDw: one of them)
 //
-// The matrix kernel is persistent, one block (or pair of blocks) per SM: one
-// thread feeds 128-byte swizzled operand tiles by tiled bulk copies, one
-// issues tcgen05 matrix instructions into tensor memory, eight warps run the
-// epilogue of the previous tile meanwhile (two accumulators).
+// Sums, maxima and exponentials are float32; d is rounded to the operands' 16
+// bits because the products that read it take no other: each of its entries
+// moves by half a unit at most, as the rounded gradients themselves do.
 #include <atomic>
 #include <mutex>
 
@@ -27,7 +26,6 @@ namespace ctcpb {
 namespace {
 
 enum Mode { kStats = 0, kLogp = 1, kDlogits = 2, kProduct = 3, kBand = 4, kDx = 5, kDw = 6 };
-// kDx, kDw: one of the two products
 __host__ __device__ constexpr bool is_product(int mode) { return mode == kProduct || mode == kDx || mode == kDw; }
 
 constexpr int kEpiWarps = 16;      // 4 for each quarter of a tile's 256 columns
@@ -305,6 +303,10 @@ __device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
 // 12200 a band).  Every member must be resident (a cooperative launch); the wait
 // for the others is bounded.  A wait that gives up makes every later one return
 // at once, so that the warps go through the same barriers to the end.
+//
+// 16000 x 5000 x 512: 110 us, 2.9 TB/s written (two passes: 145).  A round of 256
+// rows takes 9000 cycles: sums 2900, exchange 3000 to 4000, writes 5000 (the SM
+// sends some 25 bytes a cycle), under each other only as far as the two sets go.
 
 constexpr int kBandTile = kTileBytes - 2 * 512 * 8;  // operand tiles; the rest holds the rows' sums
 constexpr int kSetWarps = kEpiWarps / 2;             // of the two sets, one for each half of tensor memory
@@ -481,8 +483,19 @@ __device__ void band_epilogue(const GemmArgs& a, Sched<1> sc, char* smem, u32 tm
 
 // ---------------------------------------------------------------- the matrix kernel
 
-// Shared memory: a ring of operand tiles, the epilogue warps' buffers, the
-// barriers.
+// Persistent, one block (or pair of blocks, on a tile of 256 x 256) per SM.  One
+// thread feeds 128-byte swizzled operand tiles by tiled copies through a ring,
+// one issues tcgen05 matrix instructions into tensor memory, sixteen warps run
+// the epilogue of the tile before meanwhile (two accumulators of 256 columns).
+// Shared memory: the ring, the epilogue warps' buffers, the barriers.
+//
+// Bound by the tensor cores where K is long: kStats on 12800 x 32000 x 1024 runs
+// alone in 417 us, 2.0 PFLOP/s, the tensor pipe active 88% of the time; back to
+// back the power limit lowers the clock (495 us).  A tile's end costs some 1500
+// cycles, which K = 512 feels (12000 x 5000 x 512: kStats 46 us, 1.33 PFLOP/s, the
+// pipe active 60%; kDlogits 54 us, its epilogue also sums the columns and writes
+// 120 MB; dx and dw 88 us, which read d back from HBM).  The ring of 160 KB covers
+// the copies' latency.
 template <int MODE, class T, int CG>
 __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Params<MODE> prm) {
   constexpr int P = Params<MODE>::kProblems;
@@ -866,9 +879,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
 
 // ---------------------------------------------------------------- what is left after the products
 
-// The shares of a tile of the split wave, added in the order of K, and the
-// tile's output written: a block per 32 rows and 64 columns, 8 columns a warp
-// (16 bytes of each row), two shares' loads in flight.
+// The parts of a tile that was cut, added in the order of K, and the tile's
+// output written: a block per 32 rows and 64 columns, 8 columns a warp (16
+// bytes of each row), two parts' loads in flight.
 template <class T>
 __device__ void join_tile(const GemmArgs& a, const Sched<2>& sc, int i, int cg, int r, int unit, char* buf) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -956,8 +969,9 @@ struct FinishArgs {
 
 // One launch for what the products of a piece leave: db (a block per 32
 // columns, 8 slices of the rows, eight loads of a slice in flight) and the
-// joins of dx and dw.  How many tiles were split is known here only, so the
-// blocks go through the units.
+// joins of dx and dw.  How many tiles were cut is known here only, so the
+// blocks go through the units.  Bound by latency: some 45 MB, 21 us for 12000 x
+// 5000 x 512.
 template <class T>
 __global__ void __launch_bounds__(256, 5) k_finish(const FinishArgs f) {
   __shared__ __align__(16) char buf[kStageBuf];
@@ -1093,7 +1107,8 @@ __device__ __forceinline__ int block_sum(int v, int* red) {
 // sum.  Each block counts the kept rows before its own by reading the targets,
 // so one launch does it; `per` rows a block keep the blocks, and so the
 // targets read, in proportion to N.  The rows up to the next multiple of 64,
-// the depth that the last step of d^T x reads, are zeros.
+// the depth that the last step of d^T x reads, are zeros.  Bound by latency:
+// 16000 rows of 512, a quarter ignored, 12 us (28 MB).
 __global__ void __launch_bounds__(256) k_rows(const RowArgs a, int per) {
   __shared__ int red[8];
   __shared__ float fred[8];
@@ -1229,7 +1244,8 @@ struct CombineArgs {
 
 // lse = m + log(sum_j s_j exp(m_j - m)) over a row's tiles (m, s and z[target]
 // are to base 2, see kStats), and the losses: a block per 32 rows, 16 slices of
-// the tiles, eight of a slice's loads in flight.
+// the tiles, eight of a slice's loads in flight.  12000 rows of 80 pairs: 12 us,
+// half of it the mean's chain of block sums.
 constexpr int kSlices = 16;
 __global__ void __launch_bounds__(32 * kSlices) k_combine(const CombineArgs a) {
   __shared__ float2 red[kSlices][32];
@@ -1381,7 +1397,8 @@ int sm_count() {
 
 long long up_to(long long x, long long a) { return (x + a - 1) / a * a; }
 
-// Columns of a tile of the logits: as wide as leaves no SM idle.
+// Columns of a tile of the logits: as wide as leaves no SM idle (128 x 5000 x
+// 512 in two passes: kStats 9 us on 79 blocks of 64 columns).
 int logits_bn(long long rows, int V) {
   const long long mt = (rows + 127) / 128;
   for (int bn = 256; bn > 64; bn >>= 1)
