@@ -167,6 +167,15 @@ struct Sched {
   }
   // the first slice of problem i's tile r of those that are cut
   __device__ int slice_of(int i, int r) const { return (i ? rem[0] * ks[0] : 0) + r * ks[i]; }
+  // next() for who needs the depth alone: one problem's tiles all have the same
+  __device__ bool next_depth(Seg& s) {
+    if (P > 1 || members > 0) return next(s);
+    s.k0 = 0;
+    s.k1 = ks[0];
+    const bool more = t < dp[0];
+    t += G;
+    return more;
+  }
   __device__ bool next(Seg& s) {
     s.slot = -1;
     s.k0 = 0;
@@ -605,35 +614,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {  // ---- matrix instructions
+    if (rank == 0) {  // ---- matrix instructions
+      const u32 one = lane == 0;
       int st = 0, as = 0;
       u32 ph = 0, aph = 1;
       constexpr u64 kStepB = BMN ? 2048 >> 4 : 32 >> 4;
-      bool more = sc.next(sg);
+      // The epilogue's warps take most of the issue slots, and the queue in front of
+      // the tensor cores is short, so a slice's instructions are few: the warp runs
+      // this as one, a lane issues (12000 x 5000 x 512: kStats 42.4 us, 45.4 with a
+      // lane alone in here), and a stage's descriptors are the first stage's with its
+      // offset added (the address, in the lowest 14 bits, stays below 256 KB).
+      const u64 desc_b = smem_desc(s_tiles + 16384u, BMN ? 8192 : 16);
+      const u32 stage = stage_bytes >> 4;
+      bool more = sc.next_depth(sg);
       while (more) {
-        if (!(ok = wait(s_tempty + 8 * as, aph))) break;
+        if (!(ok = __all_sync(0xffffffffu, wait(s_tempty + 8 * as, aph)))) break;
         tc_fence_after();
         const u32 d = tmem + 256u * as;
-        const int k0 = sg.k0, k1 = sg.k1;
+        const int slices = sg.k1 - sg.k0;
         const bool amn = problem(sg) == 1;
         const u32 idesc = mma_idesc(Elem<T>::kFormat, amn, BMN, 128 * CG, a.bn);
-        const u64 step_a = amn ? 2048 >> 4 : 32 >> 4;
-        for (int k = k0; k < k1; ++k) {
-          if (!(ok = wait(s_full + 8 * st, ph))) break;
+        const u64 step_a = amn ? 2048 >> 4 : 32 >> 4, desc_a = smem_desc(s_tiles, amn ? 8192 : 16);
+        for (int k = 0; k < slices; ++k) {
+          if (!(ok = __all_sync(0xffffffffu, wait(s_full + 8 * st, ph)))) break;
           tc_fence_after();
-          const u32 at = s_tiles + (u32)st * stage_bytes;
-          const u64 da = smem_desc(at, amn ? 8192 : 16), db = smem_desc(at + 16384u, BMN ? 8192 : 16);
+          const u64 da = desc_a + (u32)st * stage, db = desc_b + (u32)st * stage;
+          mma_f16<CG>(d, da, db, idesc, k > 0, one);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma_f16<CG>(d, da + i * step_a, db + i * kStepB, idesc, k > k0 || i > 0);
-          mma_commit<CG>(s_empty + 8 * st);
+          for (int i = 1; i < 4; ++i) mma_f16<CG>(d, da + i * step_a, db + i * kStepB, idesc, true, one);
+          mma_commit<CG>(s_empty + 8 * st, one);
           if (++st == a.stages) {
             st = 0;
             ph ^= 1;
           }
-          if (k == k0) more = sc.next(sg);  // found while the tensor cores are busy
+          if (k == 0) more = sc.next_depth(sg);  // found while the tensor cores are busy
         }
         if (!ok) break;
-        mma_commit<CG>(s_tfull + 8 * as);
+        mma_commit<CG>(s_tfull + 8 * as, one);
         if (++as == 2) {
           as = 0;
           aph ^= 1;

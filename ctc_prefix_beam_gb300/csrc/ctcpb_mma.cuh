@@ -209,31 +209,39 @@ __device__ __forceinline__ void tmem_dealloc(u32 tmem, u32 cols) {
   else
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(cols));
 }
-// D (+)= A B on one K = 16 slice of 16-bit operands in shared memory
+// D (+)= A B on one K = 16 slice of 16-bit operands in shared memory.  The whole warp
+// calls with the same operands, and the lane with `one` set issues: operands that
+// are the warp's need no move to where the instruction takes them from.
 template <int CG>
-__device__ __forceinline__ void mma_f16(u32 d, u64 a, u64 b, u32 idesc, bool add) {
+__device__ __forceinline__ void mma_f16(u32 d, u64 a, u64 b, u32 idesc, bool add, u32 one) {
   if constexpr (CG == 1)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
-            d),
-        "l"(a), "l"(b), "r"(idesc), "r"((u32)add)
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((u32)add), "r"(one)
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
-            d),
-        "l"(a), "l"(b), "r"(idesc), "r"((u32)add)
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((u32)add), "r"(one)
         : "memory");
 }
 // arrive on a barrier (in both blocks of a pair) once the matrix instructions issued so far are done
 template <int CG>
-__device__ __forceinline__ void mma_commit(u32 bar) {
+__device__ __forceinline__ void mma_commit(u32 bar, u32 one) {
   if constexpr (CG == 1)
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+        "r"(one)
+        : "memory");
   else
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(bar),
-        "h"((unsigned short)3)
+        "{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n"
+        " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
+            bar),
+        "h"((unsigned short)3), "r"(one)
         : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
