@@ -494,17 +494,19 @@ __device__ void band_epilogue(const GemmArgs& a, Sched<1> sc, char* smem, u32 tm
 
 // Persistent, one block (or pair of blocks, on a tile of 256 x 256) per SM.  One
 // thread feeds 128-byte swizzled operand tiles by tiled copies through a ring,
-// one issues tcgen05 matrix instructions into tensor memory, sixteen warps run
+// one warp issues tcgen05 matrix instructions into tensor memory, sixteen warps run
 // the epilogue of the tile before meanwhile (two accumulators of 256 columns).
 // Shared memory: the ring, the epilogue warps' buffers, the barriers.
 //
 // Bound by the tensor cores where K is long: kStats on 12800 x 32000 x 1024 runs
-// alone in 417 us, 2.0 PFLOP/s, the tensor pipe active 88% of the time; back to
-// back the power limit lowers the clock (495 us).  A tile's end costs some 1500
-// cycles, which K = 512 feels (12000 x 5000 x 512: kStats 46 us, 1.33 PFLOP/s, the
-// pipe active 60%; kDlogits 54 us, its epilogue also sums the columns and writes
-// 120 MB; dx and dw 88 us, which read d back from HBM).  The ring of 160 KB covers
-// the copies' latency.
+// alone in 406 us, 2.06 PFLOP/s, the tensor pipe active 94% of the time; back to
+// back the power limit lowers the clock (465 us).  With K = 512 the epilogue's
+// warps run all the time and keep the warp that issues from its slots: a step of 64
+// takes 750 cycles then instead of 512 (12000 x 5000 x 512: kStats 42.7 us, 1.44
+// PFLOP/s, the pipe active 64%; kDlogits 53 us, whose epilogue also sums the columns
+// and writes 120 MB).  dx and dw, 89 us, are bound by the copies: an SM takes in 60
+// bytes a cycle, 544 cycles a step at best, and has nothing to make up a late one
+// with (bringing d into L2 ahead takes from the same rate: 109 us and more).
 template <int MODE, class T, int CG>
 __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Params<MODE> prm) {
   constexpr int P = Params<MODE>::kProblems;
