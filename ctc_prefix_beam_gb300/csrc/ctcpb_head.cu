@@ -1170,11 +1170,16 @@ __global__ void __launch_bounds__(256) k_rows(const RowArgs a, int per) {
     for (int k = 0; k < 8; ++k) count(t[k]);
   }
   before = block_sum(before, red);
-  // the largest |grad| (float16 only): d is scaled by it to stay in range
+  // the largest finite |grad| of the rows that are kept (float16 only): d is scaled
+  // by it to stay in range.  An ignored row's gradient is not asked for, and one that
+  // is not finite must not take the others' with it.
   float gmax = 1.f;
   if (a.grad && a.reduction == CTCPB_REDUCE_NONE && a.type == CTCPB_F16) {
     float g = 0.f;
-    for (int i = threadIdx.x; i < a.N; i += 256) g = fmaxf(g, fabsf(a.grad[i]));
+    for (int i = threadIdx.x; i < a.N; i += 256) {
+      const float v = fabsf(a.grad[i]);
+      if (kept(a.targets[i]) && v < INFINITY) g = fmaxf(g, v);
+    }
     for (int s = 16; s > 0; s >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, s));
     if (lane == 0) fred[warp] = g;
     __syncthreads();

@@ -516,7 +516,11 @@ int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, con
  *                 may be NULL (not computed).
  * The logits are made again, in pieces of the vocabulary whose d fits in 256 MB
  * of the workspace.  d is held in `type` (16 bits); every sum is float32 and in
- * a fixed order, so results are reproducible bit for bit.
+ * a fixed order, so results are reproducible bit for bit.  An ignored row's
+ * grad[r] is of no account, whatever it holds; one of a kept row that is not
+ * finite shows in that row of dx and in the sums over rows.  CTCPB_F16 with
+ * REDUCE_NONE holds d relative to the largest finite |grad[r]| of the kept rows:
+ * what is below 2^-39 of it (2^-29: with fewer bits) is lost.
  */
 int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, const void* x, int64_t ldx,
                                  const void* weight, int64_t ldw, const void* bias, const int32_t* targets,
