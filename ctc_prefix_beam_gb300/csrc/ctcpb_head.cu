@@ -6,7 +6,7 @@
 //
 //   z = x w^T + b                        [rows, V], never stored as such
 //   kStats    per row and column tile (max z, sum exp(z - max)), z[target]
-//   kLogp     z - lse, float32           the decoder's log_prob
+//   kLogp     z - lse, float32           the decoder's log_prob, as (z - max z) - log(sum)
 //   kBand     both at once: a band of rows stays in the tensor memory of the
 //             blocks that share it until its lse is known
 //   kDlogits  d = (exp(z - lse) - [c = target]) r   16 bits, a piece of V
@@ -59,7 +59,8 @@ struct GemmArgs {
   const float* rs;      // per-row factor of d
   int per_row;          // ... which differs from row to row
   float one_r, log2_r;  // ... or is this, and its log2
-  float factor;         // of the accumulator: log2(e) (kLogp: 1), times what truncation lost
+  float factor;         // of the accumulator: log2(e), times what truncation lost
+  const float2* norm;   // kLogp: a row's max z (to base 2) and -log of its sum
   float* zt;
   float2* part;
   long long part_ld;
@@ -363,7 +364,7 @@ __device__ void band_epilogue(const GemmArgs& a, Sched<1> sc, char* smem, u32 tm
       lim = a.N - n0;
       end = a.bn < lim ? a.bn : lim;
       const int c = (int)threadIdx.x - 128 - set * 256;
-      bias_s[c] = c < end ? (a.bias ? load_elem(a.bias, a.bias_type, n0 + c) : 0.f) : -INFINITY;
+      bias_s[c] = c < end ? (a.bias ? load_elem(a.bias, a.bias_type, n0 + c) * kLog2e : 0.f) : -INFINITY;
       set_sync(set);
       first = false;
     }
@@ -397,13 +398,13 @@ __device__ void band_epilogue(const GemmArgs& a, Sched<1> sc, char* smem, u32 tm
 #pragma unroll
         for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], fmaxf(v[i + k], v[i + k + 4]));
       }
-      const float mn = fmaxf(fmaxf(bm, kLog2e * fmaxf(m4[0], m4[1])), kLog2e * fmaxf(m4[2], m4[3]));
+      const float mn = fmaxf(fmaxf(bm, fmaxf(m4[0], m4[1])), fmaxf(m4[2], m4[3]));
       const float mm = mn == -INFINITY ? 0.f : mn;
       float s[4] = {bs * ex2(bm - mm), 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 32; i += 4) {
-        fma2(v[i], v[i + 1], kLog2e, -mm, -mm);
-        fma2(v[i + 2], v[i + 3], kLog2e, -mm, -mm);
+        add2(v[i], v[i + 1], -mm);
+        add2(v[i + 2], v[i + 3], -mm);
         add2(s[0], s[1], ex2(v[i]), ex2(v[i + 1]));
         add2(s[2], s[3], ex2(v[i + 2]), ex2(v[i + 3]));
       }
@@ -453,8 +454,8 @@ __device__ void band_epilogue(const GemmArgs& a, Sched<1> sc, char* smem, u32 tm
       const float2 both[2] = {all[r128], all[128 + r128]};
       sum = join_sums(both);
     }
-    const float lse = ((sum.x == -INFINITY ? 0.f : sum.x) + log2f(sum.y)) * kLn2;
-    // 3. z - lse
+    // 3. z - lse as (z - m) - log(sum), so that nothing grows with |z|
+    const float ls = -log2f(sum.y) * kLn2;
     const int row0 = (sg.m * CG + (int)rank) * 128 + q * 32, row = row0 + lane;
 #pragma unroll 1
     for (int c0 = u; c0 < end && c0 < u + 128; c0 += 32) {
@@ -469,8 +470,13 @@ __device__ void band_epilogue(const GemmArgs& a, Sched<1> sc, char* smem, u32 tm
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float4 b = b4[i];
-        fma2(v[4 * i], v[4 * i + 1], a.factor, b.x - lse, b.y - lse);
-        fma2(v[4 * i + 2], v[4 * i + 3], a.factor, b.z - lse, b.w - lse);
+        fma2(v[4 * i], v[4 * i + 1], a.factor, b.x, b.y);
+        fma2(v[4 * i + 2], v[4 * i + 3], a.factor, b.z, b.w);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        add2(v[i], v[i + 1], -sum.x);
+        fma2(v[i], v[i + 1], kLn2, ls, ls);
       }
       stage_f32(buf, lane, v);
       // a tiled copy writes 32 columns, and cuts a row off at 16 bytes only
@@ -691,8 +697,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
         }
         if (row < mrows) {
           if (MODE != kLogp && a.tgt) w.tgt = a.tgt[row];
-          if (MODE != kStats) w.lse = a.lse[row];
-          if (MODE == kDlogits) w.rs = a.rs[row];
+          if (MODE == kLogp) {
+            const float2 norm = a.norm[row];
+            w.rs = norm.x;
+            w.lse = norm.y;
+          }
+          if (MODE == kDlogits) {
+            w.lse = a.lse[row];
+            w.rs = a.rs[row];
+          }
         }
       }
       return w;
@@ -714,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
       const int orow = w.orow, tgt = w.tgt - a.col0 - n0;  // (no target: below every column)
       const float rs = w.rs;
       float lse = w.lse, bq[2] = {w.bias[0], w.bias[1]};
-      if (MODE == kStats || MODE == kDlogits) {
+      if (!is_product(MODE)) {
         bq[0] *= kLog2e;
         bq[1] *= kLog2e;
       }
@@ -746,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
         if constexpr (!is_product(MODE)) {
-          // to base 2 (but for kLogp), so that exp and log cost nothing more: z log2(e) + b log2(e)
+          // to base 2, so that exp and log cost nothing more: z log2(e) + b log2(e)
           if (c0 < a.bn) {
             const float4* b4 = reinterpret_cast<const float4*>(bias_s);
 #pragma unroll
@@ -786,7 +799,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
           bs = (s[0] + s[1]) + (s[2] + s[3]);
         } else if constexpr (MODE == kLogp) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) add2(v[i], v[i + 1], -lse);
+          for (int i = 0; i < 32; i += 2) {
+            add2(v[i], v[i + 1], -rs);
+            fma2(v[i], v[i + 1], kLn2, lse, lse);
+          }
           if (store_tiled && j) {
             if (lane == 0) tma_store_wait();
             __syncwarp();
@@ -1258,6 +1274,7 @@ struct CombineArgs {
   long long part_ld;
   int slots;
   float* lse;            // [row]
+  float2* norm;          // or, for log-probabilities: m and -log(sum)
   const int* rowmap;     // null: the rows themselves, no loss
   const float* zt;
   float* loss;
@@ -1267,7 +1284,7 @@ struct CombineArgs {
 };
 
 // lse = m + log(sum_j s_j exp(m_j - m)) over a row's tiles (m, s and z[target]
-// are to base 2, see kStats), and the losses: a block per 32 rows, 16 slices of
+// are to base 2, see kStats), and the losses, (m - z[target]) + log(sum): a block per 32 rows, 16 slices of
 // the tiles, eight of a slice's loads in flight.  12000 rows of 80 pairs: 12 us,
 // half of it the mean's chain of block sums.
 constexpr int kSlices = 16;
@@ -1310,11 +1327,13 @@ __global__ void __launch_bounds__(32 * kSlices) k_combine(const CombineArgs a) {
     const float mm = m == -INFINITY ? 0.f : m;
     s = 0.f;
     for (int w = 0; w < kSlices; ++w) s = __fmaf_rn(red[w][lane].y, ex2(red[w][lane].x - mm), s);
-    const float lse2 = mm + log2f(s);
-    a.lse[row] = lse2 * kLn2;
+    const float l = log2f(s);
     if (a.rowmap) {
-      loss = (lse2 - zt) * kLn2;
+      a.lse[row] = (mm + l) * kLn2;
+      loss = ((m - zt) + l) * kLn2;  // the target's distance to the largest first: it is exact where it is small
       if (a.reduction == CTCPB_REDUCE_NONE) a.loss[row] = loss;
+    } else {
+      a.norm[row] = make_float2(m, -l * kLn2);
     }
   }
   if (!a.rowmap || a.reduction == CTCPB_REDUCE_NONE) return;
@@ -1452,7 +1471,7 @@ int group_of(int K, int cg) {
 // 2^-24, for logits of either sign and the large ones of targets alike; the
 // factor that scales the accumulator anyway puts it back.
 constexpr double kLog2ed = 1.4426950408889634;
-float factor_of(int K, double f) { return (float)(f * (1.0 + 0.26 * ((K + 15) / 16) * (1.0 / 16777216.0))); }
+float factor_of(int K) { return (float)(kLog2ed * (1.0 + 0.26 * ((K + 15) / 16) * (1.0 / 16777216.0))); }
 
 bool rows_aligned(const void* p, long long ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
 // Rows that tiled copies may read: they fill what lies past H only from the next 16 bytes on.
@@ -1525,7 +1544,7 @@ struct LogpLayout {
   BandPlan band;
   int bn, nt, Hp;
   long long Np;
-  size_t o_part, o_lse, o_x, o_w, total;
+  size_t o_part, o_norm, o_x, o_w, total;
 };
 LogpLayout logp_layout(long long N, int V, int H) {
   LogpLayout l{};
@@ -1537,7 +1556,7 @@ LogpLayout logp_layout(long long N, int V, int H) {
   const size_t two = (size_t)l.nt * part_slots(l.bn), one = (size_t)l.band.members;
   Taker t;
   l.o_part = t.take((two > one ? two : one) * l.Np * 8);
-  l.o_lse = t.take((size_t)l.Np * 4);
+  l.o_norm = t.take((size_t)l.Np * 8);
   l.o_x = t.take((size_t)N * l.Hp * 2);  // rows that no tiled copy can read are laid out here
   l.o_w = t.take((size_t)V * l.Hp * 2);
   l.total = align_up(t.off, 256);
@@ -1632,6 +1651,7 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   a.K = H;
   a.bias = bias;
   a.bias_type = bias_type;
+  a.factor = factor_of(H);
   a.part = (float2*)(b + l.o_part);
   a.out = out;
   a.ldo = ldo;
@@ -1645,7 +1665,6 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
     if (!make_map(&mb, type, weight, l.Hp, V, ldw, p.bn / p.cg)) return CTCPB_ECUDA;
     a.bn = p.bn;
     a.stages = stages_of(p.bn, p.cg, kBandTile);
-    a.factor = factor_of(H, 1.0);
     a.members = p.members;
     a.bands = p.bands;
     a.reset_status = 1;
@@ -1662,8 +1681,7 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   a.stages = stages_of(l.bn, cg);
   a.group = group_of(H, cg);
   a.part_ld = l.Np;
-  a.factor = factor_of(H, kLog2ed);
-  a.lse = (float*)(b + l.o_lse);
+  a.norm = (const float2*)(b + l.o_norm);
   a.reset_status = 1;
   const long long tiles = (N + 128 * cg - 1) / (128 * cg) * l.nt;
   const int blocks = cg * (int)(tiles < sms / cg ? tiles : sms / cg);
@@ -1674,9 +1692,8 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   c.part = a.part;
   c.part_ld = l.Np;
   c.slots = part_slots(l.bn) * l.nt;
-  c.lse = (float*)(b + l.o_lse);
+  c.norm = (float2*)(b + l.o_norm);
   TRY(launch(k_combine, (unsigned)((N + 31) / 32), 32 * kSlices, 0, s, 1, c));
-  a.factor = factor_of(H, 1.0);
   a.group = 1;  // neighbours write neighbouring columns
   TRY((launch_gemm<kLogp>(type, cg, ma, mb, mo, a, blocks, s)));
   return CTCPB_OK;
@@ -1765,7 +1782,7 @@ int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, con
   a.bias = bias;
   a.bias_type = bias_type;
   a.tgt = r.tgt;
-  a.factor = factor_of(H, kLog2ed);
+  a.factor = factor_of(H);
   a.zt = (float*)(b + l.o_zt);
   a.part = (float2*)(b + l.o_part);
   a.part_ld = l.Np;
@@ -1844,7 +1861,7 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
     a.per_row = reduction == CTCPB_REDUCE_NONE;
     a.log2_r = type == CTCPB_F16 ? 15.f : 0.f;  // see k_rows
     a.one_r = type == CTCPB_F16 ? 32768.f : 1.f;
-    a.factor = factor_of(H, kLog2ed);
+    a.factor = factor_of(H);
     a.out = b + l.o_d;
     a.ldo = l.piece;
     a.tiled = 1;

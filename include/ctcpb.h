@@ -476,6 +476,8 @@ int ctcpb_layer_norm_backward(int type, int param_type, const void* dy, int64_t 
  *   out        row stride ldo (>= V) elements.  Rows that start on 16-byte
  *              boundaries (ldo % 4 == 0) are written, and decoded, fastest.
  *   ws         ctcpb_log_probs_workspace_size() bytes.
+ * A value is (z - max z) - log sum exp(z - max z), the difference exact where it
+ * is small: never above 0, and 0 for a certain label, however large its z.
  * Any strides >= H and any alignment of the element type are taken; x or
  * weight whose rows do not start on 16-byte boundaries are laid out again in
  * the workspace first.  N == 0 is a no-op.
@@ -488,6 +490,7 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
 /*
  * Softmax cross entropy of the head's logits z = x weight^T + bias, which are
  * never stored: loss_r = lse_r - z[r, target_r], lse_r = log sum_c exp z[r, c].
+ * (loss_r from the distances to the row's largest z: never below 0.)
  *   targets       [N] int32.  A row whose target is ignore_index takes no part:
  *                 its x is not read into any sum, its loss and lse are 0.  Any
  *                 other target outside [0, V) is ignored as well and sets
