@@ -18,8 +18,6 @@
 #include <atomic>
 #include <mutex>
 
-#include <cooperative_groups.h>
-
 #include "ctcpb_head.cuh"
 
 namespace ctcpb {
@@ -496,6 +494,18 @@ __device__ void band_epilogue(const GemmArgs& a, Sched<1> sc, char* smem, u32 tm
   __syncwarp();
 }
 
+// Mark n pairs of pairs as not there, in a launch before the one that exchanges
+// them: no member then reads what an earlier call left, and the members need not
+// meet first, a wait that would have no limit (128 x 5000 x 512, both launches:
+// 13.8 us a call, 14.4 with a meeting; 512 x 5000 x 512: 15.6 and 14.5).
+__global__ void __launch_bounds__(256) k_marks(uint4* pairs, long long n) {
+  pdl_wait();
+  pdl_next();
+  static_assert(kNoPair == ~0ull, "the mark is all ones");
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256)
+    pairs[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+}
+
 // ---------------------------------------------------------------- the matrix kernel
 
 // Persistent, one block (or pair of blocks, on a tile of 256 x 256) per SM.  One
@@ -578,16 +588,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
   sc.init(prm.g, CG, worker, workers);
   Seg sg;
   bool ok = true;
-
-  if constexpr (MODE == kBand) {
-    if (a.members > 1) {  // nobody reads a pair before its owner has marked it as not there
-      Sched<P> mine = sc;
-      while (mine.next(sg))
-        if (threadIdx.x < 128)
-          reinterpret_cast<u64*>(a.part)[(((long long)sg.m * CG + rank) * a.members + sg.n) * 128 + threadIdx.x] = kNoPair;
-      cooperative_groups::this_grid().sync();
-    }
-  }
 
   if (warp == 0) {
     if (lane == 0) {  // ---- operand tiles
@@ -1668,6 +1668,10 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
     a.members = p.members;
     a.bands = p.bands;
     a.reset_status = 1;
+    if (p.members > 1) {
+      const long long n = up_to(N, 128 * p.cg) * p.members / 2, blocks = (n + 255) / 256;
+      TRY(launch(k_marks, (unsigned)(blocks < 4 * kWorkers ? blocks : 4 * kWorkers), 256, 0, s, 1, (uint4*)a.part, n));
+    }
     const cudaError_t e = launch_gemm<kBand>(type, p.cg, ma, mb, mo, a, p.cg * p.members * p.bands, s);
     if (e == cudaSuccess) return CTCPB_OK;
     if (e != cudaErrorCooperativeLaunchTooLarge && e != cudaErrorNotSupported) return CTCPB_ECUDA;
