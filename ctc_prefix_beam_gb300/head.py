@@ -10,6 +10,11 @@ decoder's ``log_prob`` and what trains it.
 Argument marshalling only, as in ``decoder``: tensors live on one CUDA device,
 the calls run on its current stream and allocate their outputs and workspaces
 from PyTorch unless they are given.  Rows are frames: ``x`` is [..., H].
+
+What a call finds out on the device (a target out of range, a wait that gave up,
+which makes its results invalid) is in the status word of its workspace.  A caller
+that wants to know passes a workspace, and reads ``decoder.read_status(workspace)``
+when it next waits for the GPU, before the workspace is used again.
 """
 from __future__ import annotations
 
@@ -224,7 +229,8 @@ def log_probs(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor
               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The decoder's input, log_softmax(x weight^T + bias): float32 [..., V].
     x and weight are bfloat16 or float16.  ``out``: a tensor [..., V] to write,
-    its rows at one stride (the padded rows of a wider tensor, for instance)."""
+    its rows at one stride (the padded rows of a wider tensor, for instance).
+    ``workspace``'s status is 0 unless the results are invalid (CTCPB_DEV_TIMEOUT)."""
     xr, N, H, ldx, dev, dt, w, V, ldw, b, bt = _head_args(x, weight, bias)
     shape = (N, V) if x.dim() == 2 else (*x.shape[:-1], V)
     ldo = V
@@ -282,7 +288,7 @@ def cross_entropy_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Te
                            reduction: str = "mean", workspace: Optional[torch.Tensor] = None):
     """Gradients of ``cross_entropy`` for the loss's gradient ``grad`` (float32,
     a scalar, or [...] for reduction "none"): (dx like x, dweight, dbias; dbias
-    is None without a bias)."""
+    is None without a bias).  ``workspace``'s status is as ``cross_entropy``'s."""
     xr, N, H, ldx, dev, dt, w, V, ldw, b, bt = _head_args(x, weight, bias)
     t, red = _targets(targets, x, dev), _reduction(reduction)
     lead = x.shape[:-1]

@@ -66,6 +66,13 @@ def label_error_rate(tokens, lengths, seqs):
     return wrong / sum(len(s) for s in seqs)
 
 
+def checked(workspace, what):
+    """The status of the last call that used a workspace; it waits for the GPU."""
+    status = D.read_status(workspace)
+    if status:
+        raise RuntimeError(f"{what}: " + ("a target is out of range" if status & head.DEV_TARGET else f"status {status:#x}"))
+
+
 def main(steps=80, B=16, T=120, V=64, H=128, lr=2.0, seed=0, verbose=True):
     g = torch.Generator().manual_seed(seed)
     protos = torch.randn(V, H, generator=g).cuda() / H ** 0.5 * 2.0
@@ -74,13 +81,20 @@ def main(steps=80, B=16, T=120, V=64, H=128, lr=2.0, seed=0, verbose=True):
     p = {k: v.cuda() for k, v in p.items()}
     test = utterances(B, T, V, H, protos, g)
     one = torch.ones((), device="cuda")
+    # workspaces of the calls, kept so that their statuses can be read
+    n, dt = B * T, torch.bfloat16
+    sizes = dict(lp=head.log_probs_workspace_size(dt, n, V, H),
+                 ce=head.cross_entropy_workspace_size(dt, n, V, H, False),
+                 grad=head.cross_entropy_workspace_size(dt, n, V, H, True))
+    ws = {k: torch.empty(size, dtype=torch.uint8, device="cuda") for k, size in sizes.items()}
 
     def features(x):
         return head.layer_norm(x.to(torch.bfloat16), p["gamma"], p["beta"])
 
     def decode(x, lens):
         y, _, _ = features(x)
-        log_prob = head.log_probs(y, p["w"].to(torch.bfloat16), p["b"])
+        log_prob = head.log_probs(y, p["w"].to(torch.bfloat16), p["b"], workspace=ws["lp"])
+        checked(ws["lp"], "log-probabilities")
         return D.decode_offline(D.Config(beam=8, nbest=1), log_prob, lens)
 
     tokens, lengths, _ = decode(test[0], test[2])
@@ -89,12 +103,14 @@ def main(steps=80, B=16, T=120, V=64, H=128, lr=2.0, seed=0, verbose=True):
         x, targets, _, _ = utterances(B, T, V, H, protos, g)
         x16, w16 = x.to(torch.bfloat16), p["w"].to(torch.bfloat16)
         y, mean, rstd = head.layer_norm(x16, p["gamma"], p["beta"])
-        loss, lse = head.cross_entropy(y, w16, targets, p["b"])
-        dy, dw, db = head.cross_entropy_backward(one, y, w16, targets, lse, p["b"])
+        loss, lse = head.cross_entropy(y, w16, targets, p["b"], workspace=ws["ce"])
+        dy, dw, db = head.cross_entropy_backward(one, y, w16, targets, lse, p["b"], workspace=ws["grad"])
         _, dgamma, dbeta = head.layer_norm_backward(dy, x16, p["gamma"], mean, rstd)
         for name, grad in (("gamma", dgamma), ("beta", dbeta), ("w", dw.float()), ("b", db)):
             p[name].sub_(grad, alpha=lr)
         result["losses"].append(loss.item())
+        checked(ws["ce"], "loss")
+        checked(ws["grad"], "gradients")
         if verbose and (step % 20 == 0 or step == steps - 1):
             print(f"step {step:3d}  loss {result['losses'][-1]:.4f}")
 
