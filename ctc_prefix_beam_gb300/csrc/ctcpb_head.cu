@@ -1593,7 +1593,7 @@ CeLayout ce_layout(long long N, int V, int H, bool backward) {
     l.o_zt = t.take((size_t)l.Np * 4);
     l.o_sums = t.take((size_t)(l.Np / 32) * 4);
   } else {
-    // pieces of the vocabulary whose d takes at most 256 MB, of equal width
+    // pieces of the vocabulary whose d takes at most 256 MB (but 256 labels at least), of equal width
     const long long most = (256ll << 20) / (l.Np * 2) / 256 * 256;
     const long long Vp = up_to(V, 256);
     l.pieces = (int)((Vp + (most > 256 ? most : 256) - 1) / (most > 256 ? most : 256));

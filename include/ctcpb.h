@@ -485,8 +485,9 @@ int ctcpb_layer_norm_backward(int type, int param_type, const void* dy, int64_t 
  * integers) are 0.26 too large (5e-7 of z at H = 512, 8e-6 at 8192), and products
  * of one sign up to 1.5 too small.
  * Any strides >= H and any alignment of the element type are taken; x or
- * weight whose rows do not start on 16-byte boundaries are laid out again in
- * the workspace first.  N == 0 is a no-op.
+ * weight whose rows do not start on 16-byte boundaries, or whose H is no multiple
+ * of 8, are laid out again in the workspace first (every workspace of these calls
+ * has the room, 2 N H and 2 V H bytes, used or not).  N == 0 is a no-op.
  */
 int ctcpb_log_probs_workspace_size(int type, int64_t N, int V, int H, size_t* bytes);
 int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const void* weight, int64_t ldw,
@@ -523,8 +524,9 @@ int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, con
  *   lse           of the forward call, on the same x, weight, bias and targets.
  *   dx, dweight   of `type`, row strides lddx, lddw;  dbias of bias_type.  Each
  *                 may be NULL (not computed).
- * The logits are made again, in pieces of the vocabulary whose d fits in 256 MB
- * of the workspace.  d is held in `type` (16 bits); every sum is float32 and in
+ * The logits are made again, in pieces of the vocabulary whose d takes at most
+ * 256 MB of the workspace, or 512 bytes a row where that is more (a piece is at
+ * least 256 labels; above 524,288 rows).  d is held in `type` (16 bits); every sum is float32 and in
  * a fixed order, so results are reproducible bit for bit.  An ignored row's
  * grad[r] is of no account, whatever it holds; one of a kept row that is not
  * finite shows in that row of dx and in the sums over rows.  CTCPB_F16 with
