@@ -265,6 +265,12 @@ def _reduction(reduction: str) -> int:
     return _REDUCTIONS[reduction]
 
 
+def _ignored(index: int) -> int:
+    if not -2 ** 31 <= index < 2 ** 31:  # the C call would take its lowest 32 bits
+        raise ValueError("ignore_index must be an int32 value")
+    return index
+
+
 def cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
                   ignore_index: int = -1, reduction: str = "mean", workspace: Optional[torch.Tensor] = None):
     """Softmax cross entropy of the logits x weight^T + bias, which are never
@@ -279,7 +285,7 @@ def cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, 
     lse = torch.empty(lead, dtype=torch.float32, device=dev)
     ws, nbytes = _workspace(workspace, cross_entropy_workspace_size(dt, N, V, H, False), dev)
     _run(dev, "ctcpb_cross_entropy", _TYPES[dt], _TYPES[bt], _p(xr), ldx, _p(w), ldw, _p(b), _p(t), N, V, H,
-         ignore_index, red, _p(loss), _p(lse), _p(ws), nbytes)
+         _ignored(ignore_index), red, _p(loss), _p(lse), _p(ws), nbytes)
     return loss, lse
 
 
@@ -299,5 +305,5 @@ def cross_entropy_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Te
     db = torch.empty((V,), dtype=bt, device=dev) if bias is not None else None
     ws, nbytes = _workspace(workspace, cross_entropy_workspace_size(dt, N, V, H, True), dev)
     _run(dev, "ctcpb_cross_entropy_backward", _TYPES[dt], _TYPES[bt], _p(grad), _p(xr), ldx, _p(w), ldw, _p(b),
-         _p(t), _p(lse), N, V, H, ignore_index, red, _p(dx), H, _p(dw), H, _p(db), _p(ws), nbytes)
+         _p(t), _p(lse), N, V, H, _ignored(ignore_index), red, _p(dx), H, _p(dw), H, _p(db), _p(ws), nbytes)
     return dx, dw, db
