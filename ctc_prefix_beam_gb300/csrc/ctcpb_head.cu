@@ -520,9 +520,10 @@ __global__ void __launch_bounds__(256) k_marks(uint4* pairs, long long n) {
 // warps run all the time and keep the warp that issues from its slots: a step of 64
 // takes 750 cycles then instead of 512 (12000 x 5000 x 512: kStats 42.7 us, 1.44
 // PFLOP/s, the pipe active 64%; kDlogits 53 us, whose epilogue also sums the columns
-// and writes 120 MB).  dx and dw, 89 us, are bound by the copies: an SM takes in 60
-// bytes a cycle, 544 cycles a step at best, and has nothing to make up a late one
-// with (bringing d into L2 ahead takes from the same rate: 109 us and more).
+// and writes 120 MB).  dx and dw, 89 us, take some 757 cycles a step: its copies take
+// 544 (an SM takes in 60 bytes a cycle) and nothing makes up a late one, and the cut
+// tiles of dw read d from HBM again (381 MB, 262 would do); bringing d into L2 ahead
+// takes from the same rate (109 us and more), and with d in L2 a step is no shorter.
 template <int MODE, class T, int CG>
 __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Params<MODE> prm) {
   constexpr int P = Params<MODE>::kProblems;
