@@ -57,8 +57,8 @@ struct GemmArgs {
   const float* rs;      // per-row factor of d
   int per_row;          // ... which differs from row to row
   float one_r, log2_r;  // ... or is this, and its log2
-  float factor;         // of the accumulator: log2(e), times what truncation lost
-  const float2* norm;   // kLogp: a row's max z (to base 2) and -log of its sum
+  float factor;         // of the accumulator: what truncation lost (kBand: times log2(e))
+  const float2* norm;   // kLogp: a row's max z and -log of its sum
   float* zt;
   float2* part;
   long long part_ld;
@@ -369,7 +369,7 @@ __device__ void band_epilogue(const GemmArgs& a, Sched<1> sc, char* smem, u32 tm
     __all_sync(0xffffffffu, wait(tfull, ph));
     ph ^= 1;
     tc_fence_after();
-    // 1. the sums of the warp's columns, of the tile's
+    // 1. the sums of the warp's columns, of the tile's (z to base 2 here, so that exp takes no product)
     float bm = -INFINITY, bs = 0.f;
 #pragma unroll 1
     for (int c0 = u; c0 < end && c0 < u + 128; c0 += 32) {
@@ -727,13 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
       float bm = -INFINITY, bs = 0.f;  // running max and sum of the row
       const int orow = w.orow, tgt = w.tgt - a.col0 - n0;  // (no target: below every column)
       const float rs = w.rs;
-      float lse = w.lse, bq[2] = {w.bias[0], w.bias[1]};
-      if (!is_product(MODE)) {
-        bq[0] *= kLog2e;
-        bq[1] *= kLog2e;
-      }
-      // d = exp(z - lse) r: a factor r that all rows share is in the exponent
-      if (MODE == kDlogits) lse = __fmaf_rn(lse, kLog2e, a.per_row ? 0.f : -a.log2_r);
+      const float lse = w.lse, bq[2] = {w.bias[0], w.bias[1]};
       if (!(ok = __all_sync(0xffffffffu, wait(s_tfull + 8 * as, aph)))) break;
       tc_fence_after();
       more = sc.next(sg);
@@ -760,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
         if constexpr (!is_product(MODE)) {
-          // to base 2, so that exp and log cost nothing more: z log2(e) + b log2(e)
+          // z, the same bits in every use: z - max z and z - lse are exact where they are small
           if (c0 < a.bn) {
             const float4* b4 = reinterpret_cast<const float4*>(bias_s);
 #pragma unroll
@@ -788,11 +782,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
             for (int i = 0; i < 32; ++i)
               if (tr == i) a.zt[row] = v[i];
           }
-          float s[4] = {bs * ex2(bm - mm), 0.f, 0.f, 0.f};
+          float s[4] = {bs * ex2((bm - mm) * kLog2e), 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             add2(v[i], v[i + 1], -mm);
             add2(v[i + 2], v[i + 3], -mm);
+            mul2(v[i], v[i + 1], kLog2e);
+            mul2(v[i + 2], v[i + 3], kLog2e);
             add2(s[0], s[1], ex2(v[i]), ex2(v[i + 1]));
             add2(s[2], s[3], ex2(v[i + 2]), ex2(v[i + 3]));
           }
@@ -802,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             add2(v[i], v[i + 1], -rs);
-            fma2(v[i], v[i + 1], kLn2, lse, lse);
+            add2(v[i], v[i + 1], lse);
           }
           if (store_tiled && j) {
             if (lane == 0) tma_store_wait();
@@ -819,9 +815,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
           }
         } else if constexpr (MODE == kDlogits) {
           if (c0 < a.bn) {
+            const float lr = a.per_row ? 0.f : a.log2_r;  // d = exp(z - lse) r: a factor r that all rows share is in the exponent
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               add2(v[i], v[i + 1], -lse);
+              fma2(v[i], v[i + 1], kLog2e, lr, lr);
               v[i] = ex2(v[i]);
               v[i + 1] = ex2(v[i + 1]);
             }
@@ -1284,8 +1282,8 @@ struct CombineArgs {
   u32* ticket;
 };
 
-// lse = m + log(sum_j s_j exp(m_j - m)) over a row's tiles (m, s and z[target]
-// are to base 2, see kStats), and the losses, (m - z[target]) + log(sum): a block per 32 rows, 16 slices of
+// lse = m + log(sum_j s_j exp(m_j - m)) over a row's tiles, and the losses,
+// (m - z[target]) + log(sum): a block per 32 rows, 16 slices of
 // the tiles, eight of a slice's loads in flight.  12000 rows of 80 pairs: 12 us,
 // half of it the mean's chain of block sums.
 constexpr int kSlices = 16;
@@ -1314,9 +1312,9 @@ __global__ void __launch_bounds__(32 * kSlices) k_combine(const CombineArgs a) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) mn = fmaxf(mn, p[k].x);
       const float mm = mn == -INFINITY ? 0.f : mn;
-      s *= ex2(m - mm);
+      s *= ex2((m - mm) * kLog2e);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s = __fmaf_rn(p[k].y, ex2(p[k].x - mm), s);
+      for (int k = 0; k < 8; ++k) s = __fmaf_rn(p[k].y, ex2((p[k].x - mm) * kLog2e), s);
       m = mn;
     }
   }
@@ -1327,14 +1325,14 @@ __global__ void __launch_bounds__(32 * kSlices) k_combine(const CombineArgs a) {
     for (int w = 1; w < kSlices; ++w) m = fmaxf(m, red[w][lane].x);
     const float mm = m == -INFINITY ? 0.f : m;
     s = 0.f;
-    for (int w = 0; w < kSlices; ++w) s = __fmaf_rn(red[w][lane].y, ex2(red[w][lane].x - mm), s);
-    const float l = log2f(s);
+    for (int w = 0; w < kSlices; ++w) s = __fmaf_rn(red[w][lane].y, ex2((red[w][lane].x - mm) * kLog2e), s);
+    const float l = log2f(s) * kLn2;
     if (a.rowmap) {
-      a.lse[row] = (mm + l) * kLn2;
-      loss = ((m - zt) + l) * kLn2;  // the target's distance to the largest first: it is exact where it is small
+      a.lse[row] = mm + l;
+      loss = (m - zt) + l;  // the target's distance to the largest first: it is exact where it is small
       if (a.reduction == CTCPB_REDUCE_NONE) a.loss[row] = loss;
     } else {
-      a.norm[row] = make_float2(m, -l * kLn2);
+      a.norm[row] = make_float2(m, -l);
     }
   }
   if (!a.rowmap || a.reduction == CTCPB_REDUCE_NONE) return;
@@ -1478,7 +1476,7 @@ int group_of(int K, int cg) {
 // Its price: exact sums come out that much too large, 5e-7 of the value at K = 512
 // and 8e-6 at 8192, as the others would come out too small without it.
 constexpr double kLog2ed = 1.4426950408889634;
-float factor_of(int K) { return (float)(kLog2ed * (1.0 + 0.26 * ((K + 15) / 16) * (1.0 / 16777216.0))); }
+float factor_of(int K, double f) { return (float)(f * (1.0 + 0.26 * ((K + 15) / 16) * (1.0 / 16777216.0))); }
 
 bool rows_aligned(const void* p, long long ld) { return ((uintptr_t)p & 15) == 0 && ld % 8 == 0; }
 // Rows that tiled copies may read: they fill what lies past H only from the next 16 bytes on.
@@ -1658,7 +1656,6 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   a.K = H;
   a.bias = bias;
   a.bias_type = bias_type;
-  a.factor = factor_of(H);
   a.part = (float2*)(b + l.o_part);
   a.out = out;
   a.ldo = ldo;
@@ -1672,6 +1669,7 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
     if (!make_map(&mb, type, weight, l.Hp, V, ldw, p.bn / p.cg)) return CTCPB_ECUDA;
     a.bn = p.bn;
     a.stages = stages_of(p.bn, p.cg, kBandTile);
+    a.factor = factor_of(H, kLog2ed);
     a.members = p.members;
     a.bands = p.bands;
     a.reset_status = 1;
@@ -1692,6 +1690,7 @@ int ctcpb_log_probs(int type, int bias_type, const void* x, int64_t ldx, const v
   a.stages = stages_of(l.bn, cg);
   a.group = group_of(H, cg);
   a.part_ld = l.Np;
+  a.factor = factor_of(H, 1.0);
   a.norm = (const float2*)(b + l.o_norm);
   a.reset_status = 1;
   const long long tiles = (N + 128 * cg - 1) / (128 * cg) * l.nt;
@@ -1793,7 +1792,7 @@ int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, con
   a.bias = bias;
   a.bias_type = bias_type;
   a.tgt = r.tgt;
-  a.factor = factor_of(H);
+  a.factor = factor_of(H, 1.0);
   a.zt = (float*)(b + l.o_zt);
   a.part = (float2*)(b + l.o_part);
   a.part_ld = l.Np;
@@ -1872,7 +1871,7 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
     a.per_row = reduction == CTCPB_REDUCE_NONE;
     a.log2_r = type == CTCPB_F16 ? 15.f : 0.f;  // see k_rows
     a.one_r = type == CTCPB_F16 ? 32768.f : 1.f;
-    a.factor = factor_of(H);
+    a.factor = factor_of(H, 1.0);
     a.out = b + l.o_d;
     a.ldo = l.piece;
     a.tiled = 1;

@@ -48,6 +48,7 @@ __device__ __forceinline__ void add2(float& x, float& y, float bx, float by) {
   unpair(x, y, add2(pair(x, y), pair(bx, by)));
 }
 __device__ __forceinline__ void add2(float& x, float& y, float b) { add2(x, y, b, b); }
+__device__ __forceinline__ void mul2(float& x, float& y, float f) { unpair(x, y, mul2(pair(x, y), pair(f, f))); }
 
 // ---------------------------------------------------------------- element types
 

@@ -520,6 +520,8 @@ int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, con
  *   dx = d weight  [N, H],  dweight = d^T x  [V, H],  dbias = sum_r d[r]  [V],
  * where g_r is grad[r] (REDUCE_NONE), grad[0] (REDUCE_SUM) or grad[0] over the
  * number of rows that take part (REDUCE_MEAN); ignored rows get exact zeros.
+ * z is made again with the forward call's roundings: the target of a row that is
+ * certain of it (lse_r is z[r, target_r] in float32) has d = 0.
  *   grad          device float32: [N] or one value.
  *   lse           of the forward call, on the same x, weight, bias and targets.
  *   dx, dweight   of `type`, row strides lddx, lddw;  dbias of bias_type.  Each
