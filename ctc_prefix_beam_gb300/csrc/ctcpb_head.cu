@@ -14,7 +14,8 @@
 //
 // Sums, maxima and exponentials are float32; d is rounded to the operands' 16
 // bits because the products that read it take no other: each of its entries
-// moves by half a unit at most, as the rounded gradients themselves do.
+// moves by half a unit at most, as the rounded gradients themselves do.  In small
+// calls (terms_of) what the rounding took off is a second term of the products.
 #include <atomic>
 #include <mutex>
 
@@ -49,6 +50,7 @@ struct GemmArgs {
   int stages;
   int group;            // row tiles that share a sweep over the columns
   int col0;             // first vocabulary entry of the piece
+  int lo_at;            // columns from d to its second term (0: it has one)
   // logits
   const void* bias;
   int bias_type;
@@ -134,6 +136,7 @@ struct Sched {
         rem[i] = tiles % G;
         if (5 * rem[i] > 4 * G) rem[i] = 0;  // a nearly full wave: joining would cost more than it gives
       }
+      if (P > 1 && a.lo_at) ks[i] *= 2;  // both terms of d, one after the other
       dp[i] = tiles - rem[i];
       slices += rem[i] * ks[i];
     }
@@ -238,6 +241,25 @@ __device__ __forceinline__ void stage_f32(char* buf, int lane, const float (&v)[
 #pragma unroll
   for (int c = 0; c < 8; ++c)
     *reinterpret_cast<float4*>(buf + stage_at(lane, c)) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+// 32 columns of a thread's own row as two 16-bit terms, the rounded value and what
+// that took off, written by the thread itself (small calls only).
+template <class T>
+__device__ __forceinline__ void store_terms(T* hi, T* lo, const float (&v)[32]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    u32 h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = v[8 * c + 2 * i], y = v[8 * c + 2 * i + 1];
+      float hx, hy;
+      h[i] = Elem<T>::pack(x, y);
+      unpair(hx, hy, Elem<T>::unpack(h[i]));
+      l[i] = Elem<T>::pack(x - hx, y - hy);
+    }
+    reinterpret_cast<uint4*>(hi)[c] = make_uint4(h[0], h[1], h[2], h[3]);
+    reinterpret_cast<uint4*>(lo)[c] = make_uint4(l[0], l[1], l[2], l[3]);
+  }
 }
 template <class T>
 __device__ __forceinline__ void stage_16(char* buf, int lane, const float (&v)[32], int half) {
@@ -524,7 +546,9 @@ __global__ void __launch_bounds__(256) k_marks(uint4* pairs, long long n) {
 // 544 (an SM takes in 60 bytes a cycle) and nothing makes up a late one, and the cut
 // tiles of dw read d from HBM again (381 MB, 262 would do); bringing d into L2 ahead
 // takes from the same rate (109 us and more), and with d in L2 a step is no shorter.
-template <int MODE, class T, int CG>
+//
+// TWO (kDlogits, kProduct): d has two terms.
+template <int MODE, class T, int CG, bool TWO>
 __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Params<MODE> prm) {
   constexpr int P = Params<MODE>::kProblems;
   constexpr bool BMN = is_product(MODE);  // the second operand has its rows along K
@@ -599,20 +623,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
         const int m0 = (sg.m * CG + (int)rank) * 128, n0 = sg.n * a.bn + (int)rank * bnb, col0 = prm.g[problem(sg)].col0;
         const CUtensorMap *map_a = &prm.a[problem(sg)], *map_b = &prm.b[problem(sg)];
         const bool amn = problem(sg) == 1;  // d^T: its columns are the rows, and contiguous
-        for (int k = sg.k0; k < sg.k1; ++k) {
+        const int each = (problem(sg) ? sc.ks[P - 1] : sc.ks[0]) / 2;  // TWO: slices of a term
+        for (int j = sg.k0; j < sg.k1; ++j) {
+          const bool lo = is_product(MODE) && TWO && j >= each;
+          const int k = lo ? j - each : j, term = lo ? a.lo_at : 0;
           if (!(ok = wait(s_empty + 8 * st, ph))) break;
           const u32 at = s_tiles + (u32)st * stage_bytes, bt = at + 16384u, bar = full0 + 8 * st;
           if (rank == 0) mbar_expect(s_full + 8 * st, stage_bytes * CG);
           if (!amn) {
-            tma_load<CG>(at, map_a, k * 64, m0, bar);
+            tma_load<CG>(at, map_a, term + k * 64, m0, bar);
           } else {
-            tma_load<CG>(at, map_a, m0, k * 64, bar);
-            tma_load<CG>(at + 8192u, map_a, m0 + 64, k * 64, bar);
+            tma_load<CG>(at, map_a, term + m0, k * 64, bar);
+            tma_load<CG>(at + 8192u, map_a, term + m0 + 64, k * 64, bar);
           }
           if constexpr (!BMN) {
             tma_load<CG>(bt, map_b, k * 64, col0 + n0, bar);
           } else {
-            for (int j = 0; j < bnb; j += 64) tma_load<CG>(bt + (u32)j * 128u, map_b, n0 + j, col0 + k * 64, bar);
+            for (int c = 0; c < bnb; c += 64) tma_load<CG>(bt + (u32)c * 128u, map_b, n0 + c, col0 + k * 64, bar);
           }
           if (++st == a.stages) {
             st = 0;
@@ -838,7 +865,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
               for (int i = 0; i < 32; ++i) v[i] = row < mrows ? v[i] : 0.f;
             }
           }
-          stage_16<T>(buf, lane, v, j);
+          if constexpr (TWO) {
+            T* const o = (T*)a.out + (long long)row * (2 * a.ldo) + n0 + c0;
+            store_terms<T>(o, o + a.lo_at, v);
+          } else {
+            stage_16<T>(buf, lane, v, j);
+          }
           if (a.dbp) {
             const float cs = column_sums(v, lane);
             if (c0 + lane < lim) a.dbp[((long long)mtile * 4 + q) * a.ldo + n0 + c0 + lane] = cs;
@@ -882,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_gemm(const __grid_constant__ Pa
       }
       // 64 columns of 16 bits are a buffer's worth
       if constexpr (MODE == kDlogits) {
-        if (busy) {
+        if (busy && !TWO) {
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) tma_store(&map_o, n0 + u, row0, saddr(buf));
@@ -1399,21 +1431,22 @@ template <int MODE>
 Params<MODE> as_mode(const Params<kProduct>& p) {
   return {{p.a[0], p.a[1]}, {p.b[0], p.b[1]}, p.o, {p.g[0], p.g[1]}};
 }
-template <int MODE, class T, int CG>
+template <int MODE, class T, int CG, bool TWO>
 cudaError_t launch_gemm_t(const Params<MODE>& prm, int blocks, cudaStream_t s) {
-  constexpr auto kern = k_gemm<MODE, T, CG>;
+  constexpr auto kern = k_gemm<MODE, T, CG, TWO>;
   cudaError_t e = smem_optin<kern>(kSmem);
   if (e != cudaSuccess) return e;
   return launch_as(MODE == kBand, kern, dim3(blocks), kThreads, kSmem, s, CG, prm);
 }
-template <int MODE>
+template <int MODE, bool TWO = false>
 cudaError_t launch_gemm(int type, int cg, const Params<MODE>& prm, int blocks, cudaStream_t s) {
   if (cg == 2)
-    return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, 2>(prm, blocks, s)
-                              : launch_gemm_t<MODE, __half, 2>(prm, blocks, s);
-  return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, 1>(prm, blocks, s) : launch_gemm_t<MODE, __half, 1>(prm, blocks, s);
+    return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, 2, TWO>(prm, blocks, s)
+                              : launch_gemm_t<MODE, __half, 2, TWO>(prm, blocks, s);
+  return type == CTCPB_BF16 ? launch_gemm_t<MODE, __nv_bfloat16, 1, TWO>(prm, blocks, s)
+                            : launch_gemm_t<MODE, __half, 1, TWO>(prm, blocks, s);
 }
-template <int MODE>
+template <int MODE, bool TWO = false>
 cudaError_t launch_gemm(int type, int cg, const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& mo,
                         const GemmArgs& a, int blocks, cudaStream_t s) {
   Params<MODE> prm;
@@ -1421,7 +1454,7 @@ cudaError_t launch_gemm(int type, int cg, const CUtensorMap& ma, const CUtensorM
   prm.b[0] = mb;
   prm.o = mo;
   prm.g[0] = a;
-  return launch_gemm<MODE>(type, cg, prm, blocks, s);
+  return launch_gemm<MODE, TWO>(type, cg, prm, blocks, s);
 }
 
 constexpr int kWorkers = 152;  // SMs; the split wave's slots are sized by it
@@ -1568,8 +1601,17 @@ LogpLayout logp_layout(long long N, int V, int H) {
   return l;
 }
 
+// Terms of d.  One 16-bit term puts the error of dx at 1.43 times the one that its
+// rounding has anyway where few labels carry a row's sum (1.25 for V >= 5000), and at
+// up to 1.7 in small calls, where no number of rows averages it out.  Two terms, the
+// rounded value and what that took off, have no part in it and double the products'
+// depth.  Two in calls whose products are no longer than their launch (backward, of
+// a graph: 50 x 32 x 64 15.7 -> 16.7 us, 50 x 2000 x 64 23.8 -> 25.3, 1000 x 60 x 60
+// 22.8 -> 26.1); beyond, 4000 rows of 8 labels and 512 features would go from 38 to 49.
+int terms_of(long long Np, int V, int H) { return Np <= 1024 && Np * V * up_to(H, 64) <= 1ll << 25 ? 2 : 1; }
+
 struct CeLayout {
-  int bn, nt, Hp, pieces, piece, pbn;
+  int bn, nt, Hp, pieces, piece, pbn, terms;
   long long Np;
   size_t o_ctl, o_map, o_tgt, o_xg, o_w;
   size_t o_part, o_zt, o_sums;
@@ -1599,11 +1641,12 @@ CeLayout ce_layout(long long N, int V, int H, bool backward) {
     l.piece = (int)up_to((V + l.pieces - 1) / l.pieces, 256);
     if (l.pieces == 1) l.piece = (int)up_to(V, 64);
     l.pieces = (V + l.piece - 1) / l.piece;
+    l.terms = l.pieces == 1 ? terms_of(l.Np, V, H) : 1;
     l.pbn = product_bn(H);
     const long long mt = l.Np / 128, nt = (H + l.pbn - 1) / l.pbn;
     l.o_lse = t.take((size_t)l.Np * 4);
     l.o_rs = t.take((size_t)l.Np * 4);
-    l.o_d = t.take((size_t)l.Np * l.piece * 2);
+    l.o_d = t.take((size_t)l.Np * l.piece * 2 * l.terms);
     l.o_dbp = t.take((size_t)mt * 4 * l.piece * 4);
     for (auto& o : l.o_slots) o = t.take((size_t)2 * kWorkers * 128 * l.pbn * 4);
     l.o_acc = t.take(l.pieces > 1 ? (size_t)mt * nt * 128 * l.pbn * 4 : 0);
@@ -1847,12 +1890,13 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
     ldw = l.Hp;
   }
   const int cg = pair_of(N, l.bn), sms = sm_count();
+  const int ldd = l.piece * l.terms, lo_at = l.terms > 1 ? l.piece : 0;  // d's rows: a term behind the other
   for (int p = 0; p < l.pieces; ++p) {
     const int v0 = p * l.piece, cols = V - v0 < l.piece ? V - v0 : l.piece;
     CUtensorMap ma, mb, mo;
     // d
     if (!make_map(&ma, type, r.xg, l.Hp, l.Np, l.Hp, 128) || !make_map(&mb, type, weight, l.Hp, V, ldw, l.bn / cg) ||
-        !make_map(&mo, type, b + l.o_d, l.piece, l.Np, l.piece, 32))
+        !make_map(&mo, type, b + l.o_d, ldd, l.Np, ldd, 32))
       return CTCPB_ECUDA;
     GemmArgs a{};
     a.rows_dev = r.nv;
@@ -1874,11 +1918,14 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
     a.factor = factor_of(H, 1.0);
     a.out = b + l.o_d;
     a.ldo = l.piece;
+    a.lo_at = lo_at;
     a.tiled = 1;
     a.dbp = dbias ? (float*)(b + l.o_dbp) : nullptr;
     a.status = r.status;
     long long tiles = l.Np / (128 * cg) * ((cols + l.bn - 1) / l.bn);
-    TRY((launch_gemm<kDlogits>(type, cg, ma, mb, mo, a, cg * (int)(tiles < sms / cg ? tiles : sms / cg), s)));
+    const int blocks_d = cg * (int)(tiles < sms / cg ? tiles : sms / cg);
+    TRY(lo_at ? (launch_gemm<kDlogits, true>(type, cg, ma, mb, mo, a, blocks_d, s))
+              : (launch_gemm<kDlogits>(type, cg, ma, mb, mo, a, blocks_d, s)));
     FinishArgs f{};
     long long left = 0;
     if (dbias) {
@@ -1906,6 +1953,7 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
       g.slots = (float*)(b + l.o_slots[0]);
       g.status = r.status;
       g.bn = l.pbn;
+      g.lo_at = lo_at;
       prm.g[0] = prm.g[1] = g;
       {  // dx (+)= d w[piece]
         GemmArgs& q = prm.g[0];
@@ -1920,7 +1968,7 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
         q.acc = l.pieces > 1 ? (float*)(b + l.o_acc) : nullptr;
         q.first = p == 0;
         q.last = p == l.pieces - 1;
-        if (!make_map(&prm.a[0], type, b + l.o_d, l.piece, l.Np, l.piece, 128) ||
+        if (!make_map(&prm.a[0], type, b + l.o_d, ldd, l.Np, ldd, 128) ||
             !make_map(&prm.b[0], type, weight, l.Hp, V, ldw, 64))
           return CTCPB_ECUDA;
       }
@@ -1933,7 +1981,7 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
         q.ldo = lddw;
         q.vec = rows_aligned(q.out, lddw);
         q.first = q.last = 1;
-        if (!make_map(&prm.a[1], type, b + l.o_d, l.piece, l.Np, l.piece, 64) ||
+        if (!make_map(&prm.a[1], type, b + l.o_d, ldd, l.Np, ldd, 64) ||
             !make_map(&prm.b[1], type, r.xg, l.Hp, l.Np, l.Hp, 64))
           return CTCPB_ECUDA;
       }
@@ -1943,7 +1991,7 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
       // the waves of either share what they read (8192 x 65536 x 2048 with all
       // its gradients: 5.27 ms apart, 5.50 together).
       const long long mt = (N > 0 ? N : 1), nt = (H + l.pbn - 1) / l.pbn, rows = 128 * cgp;
-      const bool apart = ((mt + rows - 1) / rows + (cols + rows - 1) / rows) * nt > 4ll * workers;
+      const bool apart = !lo_at && ((mt + rows - 1) / rows + (cols + rows - 1) / rows) * nt > 4ll * workers;
       f.runs = 0;
       for (int run = 0; run < (apart ? 2 : 1); ++run) {
         Params<kProduct> q = prm;
@@ -1952,7 +2000,8 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
           q.g[1 - run].none = 2;
           q.g[run].slots = (float*)(b + l.o_slots[run]);
         }
-        TRY(!apart     ? launch_gemm<kProduct>(type, cgp, q, workers * cgp, s)
+        TRY(lo_at      ? (launch_gemm<kProduct, true>(type, cgp, q, workers * cgp, s))
+            : !apart   ? launch_gemm<kProduct>(type, cgp, q, workers * cgp, s)
             : run == 0 ? launch_gemm<kDx>(type, cgp, as_mode<kDx>(q), workers * cgp, s)
                        : launch_gemm<kDw>(type, cgp, as_mode<kDw>(q), workers * cgp, s));
         f.g[f.runs][0] = q.g[0];

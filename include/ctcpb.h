@@ -528,7 +528,8 @@ int ctcpb_cross_entropy(int type, int bias_type, const void* x, int64_t ldx, con
  *                 may be NULL (not computed).
  * The logits are made again, in pieces of the vocabulary whose d takes at most
  * 256 MB of the workspace, or 512 bytes a row where that is more (a piece is at
- * least 256 labels; above 524,288 rows).  d is held in `type` (16 bits); every sum is float32 and in
+ * least 256 labels; above 524,288 rows).  d is held in `type` (16 bits), in small
+ * calls as two such terms, the rounded value and what that took off; every sum is float32 and in
  * a fixed order, so results are reproducible bit for bit.  An ignored row's
  * grad[r] is of no account, whatever it holds; one of a kept row that is not
  * finite shows in that row of dx and in the sums over rows.  CTCPB_F16 with
