@@ -68,7 +68,8 @@ int ctcpb_lse_table(float* out, int n);
 #define CTCPB_DEV_TIMEOUT 0x4u  /* a bounded inter-block wait gave up: results of the call are invalid */
 #define CTCPB_DEV_OVERFLOW 0x8u /* an internal candidate buffer overflowed: results are invalid */
 #define CTCPB_DEV_BOOST 0x10u   /* a label-boost entry was rejected and ignored (see ctcpb_boost) */
-#define CTCPB_DEV_TARGET 0x20u  /* a target outside [0, V) was ignored (ctcpb_cross_entropy) */
+#define CTCPB_DEV_TARGET 0x20u  /* a target outside [0, V) was ignored (ctcpb_cross_entropy), or a pair's index of N
+                                   or more (ctcpb_preference_loss) */
 
 /*
  * Decoder configuration (section 11).
@@ -541,6 +542,146 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
                                  const float* lse, int64_t N, int V, int H, int32_t ignore_index, int reduction,
                                  void* dx, int64_t lddx, void* dweight, int64_t lddw, void* dbias, void* ws,
                                  size_t ws_bytes, ctcpb_stream_t stream);
+
+/* ---- Around the label head: a norm for convolutional blocks, dropout, and the
+ * losses that train the model from the decoder's own N-best lists. */
+
+/*
+ * Group norm with an activation, over frames with their channels last:
+ *   y[b, t, c] = act((x[b, t, c] - mean[b, g]) * rstd[b, g] * weight[c] + bias[c]),
+ * g = c / (C / G), the mean and rstd = 1 / sqrt(variance + eps) taken over the
+ * frames t < lengths[b] and the C / G channels of the group.
+ *   type          of x and y: CTCPB_F32, CTCPB_BF16 or CTCPB_F16.
+ *   param_type    of weight and bias: `type` or CTCPB_F32.
+ *   x, y          [B, T, C]: utterance b, frame t at b * stride_b + t * stride_t
+ *                 elements, C contiguous; stride_t >= C, stride_b any but negative.
+ *   weight, bias  [C], each may be NULL (1 and 0).
+ *   lengths       [B] int32 frames of each utterance (clamped to [0, T]); NULL: T.
+ *                 Frames from there on are not read, and y is 0 there.
+ *   activation    CTCPB_ACT_NONE, CTCPB_ACT_RELU max(h, 0) or CTCPB_ACT_SILU
+ *                 h / (1 + exp(-h)).
+ *   mean, rstd    [B, G] float32, for the backward pass; both NULL: not written.
+ *                 An utterance without frames has mean 0 and rstd 0.
+ * Limits: B * T <= 2^24 frames, C <= 8192 channels, G divides C.  The variance is
+ * the mean squared distance from the mean (no difference of large sums); sums
+ * and statistics are float32 in a fixed order, y is rounded once.  y may not
+ * overlap x.  B * T == 0 is a no-op, but for mean and rstd.
+ */
+#define CTCPB_ACT_NONE 0
+#define CTCPB_ACT_RELU 1
+#define CTCPB_ACT_SILU 2
+int ctcpb_group_norm(int type, int param_type, const void* x, int64_t x_stride_b, int64_t x_stride_t,
+                     const void* weight, const void* bias, const int32_t* lengths, float eps, int activation, int B,
+                     int T, int C, int G, void* y, int64_t y_stride_b, int64_t y_stride_t, float* mean, float* rstd,
+                     ctcpb_stream_t stream);
+
+/*
+ * Its backward pass: with xh = (x - mean) * rstd, h = xh * weight + bias,
+ * dh = dy * act'(h) (relu'(0) = 0) and t = dh * weight,
+ *   dx = rstd * (t - mean_g(t) - xh * mean_g(t * xh)),  0 from lengths[b] on,
+ *   dweight = sum over b, t of dh * xh,  dbias = sum over b, t of dh.
+ * x, weight, bias, lengths, mean, rstd and activation as in the forward call.
+ * dx, dweight and dbias may each be NULL (not computed); no frames: sums of 0.
+ * Results are reproducible bit for bit.  dx may not overlap x or dy.
+ */
+int ctcpb_group_norm_workspace_size(int B, int T, int C, int G, size_t* bytes);
+int ctcpb_group_norm_backward(int type, int param_type, const void* dy, int64_t dy_stride_b, int64_t dy_stride_t,
+                              const void* x, int64_t x_stride_b, int64_t x_stride_t, const void* weight,
+                              const void* bias, const int32_t* lengths, const float* mean, const float* rstd,
+                              int activation, int B, int T, int C, int G, void* dx, int64_t dx_stride_b,
+                              int64_t dx_stride_t, void* dweight, void* dbias, void* ws, size_t ws_bytes,
+                              ctcpb_stream_t stream);
+
+/*
+ * Dropout from a counter-based generator; its mask is never stored.
+ *   y[r, c] = residual[r, c] + (kept ? x[r, c] * 65536 / (65536 - k) : 0)
+ * Element i = r * H + c, whatever the strides, is kept iff its 16-bit number is at
+ * least k = 65536 p, rounded to the nearest integer (half to even): p is held to
+ * 2^-16, the factor is exact for the p that is.  The number is half i % 8 (low
+ * half of a word first) of the four words of Philox4x32 with 10 rounds (Salmon,
+ * Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011), key =
+ * the seed's low and high word, counter = (i / 8 low, high, offset low, high).
+ *   rng        [2] int64, on the device: seed and offset.  Another offset gives
+ *              other numbers; the caller changes it between steps (a replayed
+ *              graph reads what it holds then).
+ *   p          in [0, 1]; k = 65536 drops all.  A dropped element is 0 whatever x
+ *              holds.
+ *   residual   of x's type, or NULL.
+ *   x, y       [N, H] of `type`, rows ldx, ldr, ldy elements apart; y may be x or
+ *              residual itself, with its stride.
+ * Limits: N <= 2^24 rows, H <= 8192.  The sum is float32, rounded once.
+ * The backward pass is the same call on dy without a residual (the residual's
+ * gradient is dy itself).
+ */
+int ctcpb_dropout(int type, const void* x, int64_t ldx, const void* residual, int64_t ldr, double p,
+                  const int64_t* rng, int64_t N, int H, void* y, int64_t ldy, ctcpb_stream_t stream);
+
+/*
+ * The clipped policy loss of sequences (hypotheses of N-best lists) with a KL term.
+ * A sequence's tokens have negative log-probabilities, as ctcpb_cross_entropy gives
+ * them without a reduction (CTCPB_REDUCE_NONE), and an advantage A.  With
+ *   ratio = exp(old_nll - nll),  u = nll - ref_nll,
+ *   token loss = -min(ratio * A, clamp(ratio, 1 - clip_low, 1 + clip_high) * A)
+ *                + kl_weight * (exp(u) - 1 - u).
+ *   nll, old_nll, ref_nll   [S, L] float32, rows ld_* elements apart; ref_nll NULL:
+ *                 no KL term (kl_weight is of no account).
+ *   advantages    [S] float32 (ld_advantages == 0), or [S, L] with rows that far apart.
+ *                 Where A is 0 the first term is 0, whatever the ratio.
+ *   lengths       [S] int32 tokens of each sequence (clamped to [0, L]); NULL: L.
+ *                 What a row holds behind them is of no account.
+ *   clip_low      in [0, inf), clip_high in [0, inf]; whether a ratio is past the
+ *                 border is decided without rounding it.
+ *   reduction     CTCPB_REDUCE_NONE: loss is [S, L], 0 behind the lengths; _MEAN: one
+ *                 value, the mean over all tokens; _SUM; or CTCPB_REDUCE_SEQUENCE_MEAN:
+ *                 the mean, over the sequences that have tokens, of each one's mean.
+ *                 Means over nothing are NaN, their gradients 0.
+ *   grad          the loss's gradient, device float32: one value, or [S, L] (NONE),
+ *                 dense; NULL with dnll NULL.
+ *   loss          NULL: not written.
+ *   stats         [2] float32 or NULL: the mean over all tokens of exp(u) - 1 - u
+ *                 (0 without ref_nll), and the share of tokens held at the border.
+ *   dnll          [S, L] float32, dense, or NULL: the gradient with respect to nll,
+ *                 0 behind the lengths; in the same pass, as ctcpb_cross_entropy_backward
+ *                 takes it.
+ * Sums over tokens are pairs of float32 (value and error), made in a fixed order.
+ * Limits: S, L <= 2^24.
+ */
+#define CTCPB_REDUCE_SEQUENCE_MEAN 3
+int ctcpb_policy_loss_workspace_size(int64_t S, int64_t L, size_t* bytes);
+int ctcpb_policy_loss(const float* nll, int64_t ld_nll, const float* old_nll, int64_t ld_old, const float* ref_nll,
+                      int64_t ld_ref, const float* advantages, int64_t ld_advantages, const int32_t* lengths,
+                      int64_t S, int64_t L, double clip_low, double clip_high, float kl_weight, int reduction,
+                      const float* grad, float* loss, float* stats, float* dnll, void* ws, size_t ws_bytes,
+                      ctcpb_stream_t stream);
+
+/*
+ * The preference loss of a pair of hypotheses of each N-best list.  With
+ *   R[b, n] = sum over the hypothesis' tokens of (ref_nll - nll)   (its log-probability,
+ *             over the reference model's; `average`: over its length too),
+ *   z[b] = beta * (R[b, chosen[b]] - R[b, rejected[b]]) - margin,
+ *   loss[b] = (1 - s) * log(1 + exp(-z)) + s * log(1 + exp(z)),  s = label_smoothing.
+ *   nll, ref_nll       [B, N, L] float32: hypothesis n of list b is row b * N + n, rows
+ *                      ld_* apart; ref_nll NULL: 0.
+ *   chosen, rejected   [B] int32 in [0, N).  A list with a negative index takes no part:
+ *                      its loss, margin and gradients are 0.  One with an index of N or
+ *                      more is ignored as well and sets CTCPB_DEV_TARGET in the
+ *                      workspace's status.  Both the same: z = -margin, no gradient.
+ *   lengths            [B, N] int32 (clamped to [0, L]); NULL: L.  R of none is 0.
+ *   reduction          CTCPB_REDUCE_NONE: loss is [B]; _MEAN: over the lists that take
+ *                      part (NaN if none does; gradients 0); _SUM.
+ *   grad               device float32: one value, or [B] (NONE); NULL with dnll NULL.
+ *   loss, margins      margins [B]: z.  Each may be NULL.
+ *   dnll               [B, N, L] float32, dense, or NULL: the gradient with respect to
+ *                      nll, 0 for the other hypotheses and behind the lengths.
+ * R is summed in pairs of float32 (value and error), in a fixed order.
+ * Limits: B * N, L <= 2^24; 0 <= s <= 1; beta and margin finite.
+ */
+int ctcpb_preference_loss_workspace_size(int64_t B, int N, int64_t L, size_t* bytes);
+int ctcpb_preference_loss(const float* nll, int64_t ld_nll, const float* ref_nll, int64_t ld_ref,
+                          const int32_t* chosen, const int32_t* rejected, const int32_t* lengths, int64_t B, int N,
+                          int64_t L, float beta, float margin, float label_smoothing, int average, int reduction,
+                          const float* grad, float* loss, float* margins, float* dnll, void* ws, size_t ws_bytes,
+                          ctcpb_stream_t stream);
 
 #ifdef __cplusplus
 }
