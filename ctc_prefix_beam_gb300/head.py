@@ -7,6 +7,16 @@ decoder's ``log_prob`` and what trains it.
     dy, dw, db = cross_entropy_backward(grad, y, w, targets, lse, b)
     dx, dweight, dbias = layer_norm_backward(dy, x, weight, mean, rstd)
 
+Around it: a norm for convolutional blocks, dropout, and the losses that train the
+model from the decoder's own N-best lists (tokens [B, N, L] and their lengths):
+
+    y, mean, rstd = group_norm(x, groups, weight, bias, lengths=lengths, activation="silu")
+    y = dropout(x, p, rng, residual=r)                  # rng: int64 [2] on the device, (seed, offset)
+    nll, lse = cross_entropy(y, w, tokens, b, reduction="none")
+    loss, stats, dnll = policy_loss(nll, old_nll, advantages, lengths=lengths, ref_nll=ref_nll, kl_weight=k, grad=one)
+    loss, margins, dnll = preference_loss(nll, chosen, rejected, lengths=lengths, ref_nll=ref_nll, grad=one)
+    dy, dw, db = cross_entropy_backward(dnll, y, w, tokens, lse, b, reduction="none")
+
 Argument marshalling only, as in ``decoder``: tensors live on one CUDA device,
 the calls run on its current stream and allocate their outputs and workspaces
 from PyTorch unless they are given.  Rows are frames: ``x`` is [..., H].
@@ -26,9 +36,11 @@ import torch
 
 from . import decoder as D
 
-NONE, MEAN, SUM = 0, 1, 2
+NONE, MEAN, SUM, SEQUENCE_MEAN = 0, 1, 2, 3
 DEV_TARGET = 0x20
 _REDUCTIONS = {"none": NONE, "mean": MEAN, "sum": SUM}
+_SEQ_REDUCTIONS = {**_REDUCTIONS, "sequence_mean": SEQUENCE_MEAN}
+_ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2}
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _fns = None
 
@@ -37,7 +49,7 @@ def _lib():
     global _fns
     if _fns is None:
         L = D.lib()
-        P, I, I64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
+        P, I, I64, F, DBL = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double
         SZ, SZP = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
         sig = {
             "ctcpb_layer_norm": [I, I, P, I64, P, P, F, I64, I, P, I64, P, P, P],
@@ -49,6 +61,15 @@ def _lib():
             "ctcpb_cross_entropy": [I, I, P, I64, P, I64, P, P, I64, I, I, I, I, P, P, P, SZ, P],
             "ctcpb_cross_entropy_backward": [I, I, P, P, I64, P, I64, P, P, P, I64, I, I, I, I, P, I64, P, I64, P, P, SZ,
                                              P],
+            "ctcpb_group_norm": [I, I, P, I64, I64, P, P, P, F, I, I, I, I, I, P, I64, I64, P, P, P],
+            "ctcpb_group_norm_workspace_size": [I, I, I, I, SZP],
+            "ctcpb_group_norm_backward": [I, I, P, I64, I64, P, I64, I64, P, P, P, P, P, I, I, I, I, I, P, I64, I64, P, P, P,
+                                          SZ, P],
+            "ctcpb_dropout": [I, P, I64, P, I64, DBL, P, I64, I, P, I64, P],
+            "ctcpb_policy_loss_workspace_size": [I64, I64, SZP],
+            "ctcpb_policy_loss": [P, I64, P, I64, P, I64, P, I64, P, I64, I64, DBL, DBL, F, I, P, P, P, P, P, SZ, P],
+            "ctcpb_preference_loss_workspace_size": [I64, I, I64, SZP],
+            "ctcpb_preference_loss": [P, I64, P, I64, P, P, P, I64, I, I64, F, F, F, I, I, P, P, P, P, P, SZ, P],
         }
         fns = {}
         for name, args in sig.items():
@@ -307,3 +328,226 @@ def cross_entropy_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Te
     _run(dev, "ctcpb_cross_entropy_backward", _TYPES[dt], _TYPES[bt], _p(grad), _p(xr), ldx, _p(w), ldw, _p(b),
          _p(t), _p(lse), N, V, H, _ignored(ignore_index), red, _p(dx), H, _p(dw), H, _p(db), _p(ws), nbytes)
     return dx, dw, db
+
+
+def _frames(t: torch.Tensor, what: str, dtype=None):
+    """``t`` [B, T, C], channels contiguous and the rows of an utterance at one
+    stride of at least C (else it is copied): (tensor, its strides)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3 or t.dtype not in _TYPES:
+        raise ValueError(f"{what} must be a CUDA float32, bfloat16 or float16 tensor [B, T, C]")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}")
+    B, T, C = t.shape
+    if not t.is_contiguous() and (C > 1 and t.stride(2) != 1 or T > 1 and t.stride(1) < C):
+        t = t.contiguous()
+    return t, t.stride(0) if B > 1 else T * C, t.stride(1) if T > 1 else C
+
+
+def _ints(t, shape, device, what: str):
+    """An optional int32 tensor (contiguous)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.shape != shape:
+        raise ValueError(f"{what} must be an int32 tensor {list(shape)} on {device}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _activation(name: str) -> int:
+    if name not in _ACTIVATIONS:
+        raise ValueError("activation must be none, relu or silu")
+    return _ACTIVATIONS[name]
+
+
+def _groups(groups: int, C: int) -> int:
+    if not isinstance(groups, int) or groups < 1 or C < 1 or C % groups:
+        raise ValueError(f"groups must divide the {C} channels")
+    return groups
+
+
+def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               *, lengths: Optional[torch.Tensor] = None, eps: float = 1e-5, activation: str = "none", outputs=None):
+    """Group norm and an activation (none, relu, silu) over channels-last frames
+    [B, T, C]: a group's statistics are over its channels and an utterance's first
+    ``lengths[b]`` (int32 [B]) frames; later frames are not read, and y is 0 there.
+    Returns (y like x, mean, rstd [B, groups] float32); ``outputs``: the three to
+    write (y may not be x)."""
+    act = _activation(activation)
+    xr, sb, st = _frames(x, "x")
+    B, T, C = x.shape
+    G, dev, dt = _groups(groups, C), xr.device, xr.dtype
+    w, b, pt = _params(dt, C, dev, "weight", weight, "bias", bias)
+    n = _ints(lengths, (B,), dev, "lengths")
+    if outputs is None:
+        y = torch.empty((B, T, C), dtype=dt, device=dev)
+        mean = torch.empty((B, G), dtype=torch.float32, device=dev)
+        rstd = torch.empty((B, G), dtype=torch.float32, device=dev)
+    else:
+        y, mean, rstd = outputs
+        _given(y, x.shape, dt, dev, "y")
+        _given(mean, (B, G), torch.float32, dev, "mean")
+        _given(rstd, (B, G), torch.float32, dev, "rstd")
+    _run(dev, "ctcpb_group_norm", _TYPES[dt], _TYPES[pt], _p(xr), sb, st, _p(w), _p(b), _p(n), eps, act, B, T, C, G, _p(y),
+         T * C, C, _p(mean), _p(rstd))
+    return y, mean, rstd
+
+
+def group_norm_workspace_size(B: int, T: int, C: int, groups: int) -> int:
+    return _size("ctcpb_group_norm_workspace_size", B, T, C, groups)
+
+
+def group_norm_backward(dy: torch.Tensor, x: torch.Tensor, groups: int, weight: Optional[torch.Tensor],
+                        bias: Optional[torch.Tensor], mean: torch.Tensor, rstd: torch.Tensor, *,
+                        lengths: Optional[torch.Tensor] = None, activation: str = "none", param_dtype=None,
+                        workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``group_norm`` (the same weight, bias, lengths and activation):
+    (dx like x, dweight, dbias [C]).  The last two are of the parameters' type, or
+    ``param_dtype`` (x's) without any."""
+    act = _activation(activation)
+    xr, sb, st = _frames(x, "x")
+    B, T, C = x.shape
+    G, dev, dt = _groups(groups, C), xr.device, xr.dtype
+    dyr, db_, dt_ = _frames(dy, "dy", dt)
+    if dy.shape != x.shape or dyr.device != dev:
+        raise ValueError("dy must have x's shape and device")
+    _given(mean, (B, G), torch.float32, dev, "mean")
+    _given(rstd, (B, G), torch.float32, dev, "rstd")
+    w, b, pt = _params(dt, C, dev, "weight", weight, "bias", bias)
+    if weight is None and bias is None and param_dtype is not None:
+        if param_dtype not in (dt, torch.float32):
+            raise ValueError(f"param_dtype must be {dt} or float32")
+        pt = param_dtype
+    n = _ints(lengths, (B,), dev, "lengths")
+    dx = torch.empty((B, T, C), dtype=dt, device=dev)
+    dw = torch.empty((C,), dtype=pt, device=dev)
+    db = torch.empty((C,), dtype=pt, device=dev)
+    ws, nbytes = _workspace(workspace, group_norm_workspace_size(B, T, C, G), dev)
+    _run(dev, "ctcpb_group_norm_backward", _TYPES[dt], _TYPES[pt], _p(dyr), db_, dt_, _p(xr), sb, st, _p(w), _p(b), _p(n),
+         _p(mean), _p(rstd), act, B, T, C, G, _p(dx), T * C, C, _p(dw), _p(db), _p(ws), nbytes)
+    return dx, dw, db
+
+
+def dropout(x: torch.Tensor, p: float, rng: torch.Tensor, *, residual: Optional[torch.Tensor] = None,
+            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Dropout of x [..., H] with probability ``p`` (held to 2^-16), what is kept
+    scaled up, added to ``residual`` if there is one.  Whether an element is kept
+    is a function of its index in x's shape and of ``rng``, an int64 tensor [2] on
+    x's device that holds a seed and an offset; the call does not change it.
+    ``out``: the tensor to write, which may be x or residual."""
+    xr, N, H, ldx = _rows(x, "x")
+    dev, dt = xr.device, xr.dtype
+    if not isinstance(rng, torch.Tensor) or rng.dtype != torch.int64 or rng.shape != (2,) or rng.device != dev or \
+            not rng.is_contiguous():
+        raise ValueError(f"rng must be a contiguous int64 tensor [2] on {dev}")
+    r, ldr = None, 0
+    if residual is not None:
+        r, _, _, ldr = _rows(residual, "residual", dt)
+        if residual.shape != x.shape or r.device != dev:
+            raise ValueError("residual must have x's shape and device")
+    y = torch.empty(x.shape, dtype=dt, device=dev) if out is None else _given(out, x.shape, dt, dev, "out")
+    _run(dev, "ctcpb_dropout", _TYPES[dt], _p(xr), ldx, _p(r), ldr, p, _p(rng), N, H, _p(y), H)
+    return y
+
+
+def dropout_backward(dy: torch.Tensor, p: float, rng: torch.Tensor, *, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of ``dropout`` with respect to x (the residual's is dy): the
+    same elements, for the same ``rng``, kept and scaled."""
+    return dropout(dy, p, rng, out=out)
+
+
+def _scores(t, shape, device, what: str):
+    """float32 rows [..., L] at one stride: (tensor, stride)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device or t.shape != shape:
+        raise ValueError(f"{what} must be a float32 tensor {list(shape)} on {device}")
+    if t.is_contiguous():
+        return t, shape[-1]
+    t, _, _, ld = _rows(t, what)
+    return t, ld
+
+
+def _loss_grad(grad, reduction: int, shape, device):
+    if grad is not None:
+        _given(grad, shape if reduction == NONE else (), torch.float32, device, "grad")
+    return grad
+
+
+def policy_loss_workspace_size(S: int, L: int) -> int:
+    return _size("ctcpb_policy_loss_workspace_size", S, L)
+
+
+def policy_loss(nll: torch.Tensor, old_nll: torch.Tensor, advantages: torch.Tensor, *,
+                lengths: Optional[torch.Tensor] = None, ref_nll: Optional[torch.Tensor] = None, clip_low: float = 0.2,
+                clip_high: float = 0.2, kl_weight: float = 0.0, reduction: str = "mean",
+                grad: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """The clipped policy loss of sequences of tokens, whose negative
+    log-probabilities ``nll`` [..., L] are ``cross_entropy``'s losses (reduction
+    "none"), with the KL term of ``ref_nll``.  ``old_nll`` is of the model that made
+    the sequences; ``advantages`` float32 [...], or [..., L] for each token;
+    ``lengths`` int32 [...].  ``reduction``: none ([..., L]), mean (over all tokens),
+    sum, or sequence_mean (the mean over sequences of each one's mean).  Returns
+    (loss, stats), stats float32 [2] the mean KL and the share of clipped tokens;
+    with the loss's gradient ``grad`` (float32, a scalar or [..., L]), known when
+    the loss is made, (loss, stats, dnll): ``cross_entropy_backward``'s grad."""
+    if reduction not in _SEQ_REDUCTIONS:
+        raise ValueError("reduction must be none, mean, sum or sequence_mean")
+    red = _SEQ_REDUCTIONS[reduction]
+    if not isinstance(nll, torch.Tensor) or not nll.is_cuda or nll.dim() < 1:
+        raise ValueError("nll must be a CUDA float32 tensor [..., L]")
+    dev, shape = nll.device, nll.shape
+    lead, L = shape[:-1], shape[-1]
+    a, lda = _scores(nll, shape, dev, "nll")
+    o, ldo = _scores(old_nll, shape, dev, "old_nll")
+    r, ldr = (None, 0) if ref_nll is None else _scores(ref_nll, shape, dev, "ref_nll")
+    if isinstance(advantages, torch.Tensor) and advantages.dim() == nll.dim():
+        v, ldv = _scores(advantages, shape, dev, "advantages")
+    else:
+        if not isinstance(advantages, torch.Tensor) or advantages.dtype != torch.float32 or advantages.device != dev or \
+                advantages.shape != lead:
+            raise ValueError(f"advantages must be a float32 tensor {list(lead)} or {list(shape)} on {dev}")
+        v, ldv = advantages.contiguous(), 0
+    n = _ints(lengths, lead, dev, "lengths")
+    S = lead.numel()
+    g = _loss_grad(grad, red, shape, dev)
+    loss = torch.empty(shape if red == NONE else (), dtype=torch.float32, device=dev)
+    stats = torch.empty(2, dtype=torch.float32, device=dev)
+    dnll = None if g is None else torch.empty(shape, dtype=torch.float32, device=dev)
+    ws, nbytes = _workspace(workspace, policy_loss_workspace_size(S, L), dev)
+    _run(dev, "ctcpb_policy_loss", _p(a), lda, _p(o), ldo, _p(r), ldr, _p(v), ldv, _p(n), S, L, clip_low, clip_high,
+         kl_weight, red, _p(g), _p(loss), _p(stats), _p(dnll), _p(ws), nbytes)
+    return (loss, stats) if g is None else (loss, stats, dnll)
+
+
+def preference_loss_workspace_size(B: int, N: int, L: int) -> int:
+    return _size("ctcpb_preference_loss_workspace_size", B, N, L)
+
+
+def preference_loss(nll: torch.Tensor, chosen: torch.Tensor, rejected: torch.Tensor, *,
+                    lengths: Optional[torch.Tensor] = None, ref_nll: Optional[torch.Tensor] = None, beta: float = 0.1,
+                    margin: float = 0.0, label_smoothing: float = 0.0, average: bool = False, reduction: str = "mean",
+                    grad: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """The preference loss of a pair of hypotheses of each N-best list: ``nll``
+    [B, N, L] as in ``policy_loss``, ``chosen`` and ``rejected`` int32 [B] index the
+    list (negative: the list takes no part), ``lengths`` int32 [B, N].  The
+    log-ratios to ``ref_nll`` (0 without) are sums over tokens, or means with
+    ``average``.  Returns (loss, margins [B]), the loss a scalar or [B] (reduction
+    "none"); with ``grad`` (float32, a scalar or [B]) also dnll [B, N, L].
+    ``D.read_status(workspace)`` holds ``DEV_TARGET`` if an index was N or more
+    (such a list is ignored)."""
+    red = _reduction(reduction)
+    if not isinstance(nll, torch.Tensor) or not nll.is_cuda or nll.dim() != 3:
+        raise ValueError("nll must be a CUDA float32 tensor [B, N, L]")
+    dev, shape = nll.device, nll.shape
+    B, N, L = shape
+    a, lda = _scores(nll, shape, dev, "nll")
+    r, ldr = (None, 0) if ref_nll is None else _scores(ref_nll, shape, dev, "ref_nll")
+    if chosen is None or rejected is None:
+        raise ValueError("chosen and rejected must be int32 tensors [B]")
+    c, j = _ints(chosen, (B,), dev, "chosen"), _ints(rejected, (B,), dev, "rejected")
+    n = _ints(lengths, (B, N), dev, "lengths")
+    g = _loss_grad(grad, red, (B,), dev)
+    loss = torch.empty((B,) if red == NONE else (), dtype=torch.float32, device=dev)
+    margins = torch.empty((B,), dtype=torch.float32, device=dev)
+    dnll = None if g is None else torch.empty(shape, dtype=torch.float32, device=dev)
+    ws, nbytes = _workspace(workspace, preference_loss_workspace_size(B, N, L), dev)
+    _run(dev, "ctcpb_preference_loss", _p(a), lda, _p(r), ldr, _p(c), _p(j), _p(n), B, N, L, beta, margin, label_smoothing,
+         int(bool(average)), red, _p(g), _p(loss), _p(margins), _p(dnll), _p(ws), nbytes)
+    return (loss, margins) if g is None else (loss, margins, dnll)
