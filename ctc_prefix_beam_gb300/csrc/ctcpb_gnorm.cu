@@ -11,172 +11,30 @@
 // and keeps it in shared memory between the two passes; where a slab is too long
 // for a block, or there are too few of them, a cluster of blocks shares its frames
 // and exchanges the statistics.  A thread copies into shared memory just what it
-// will read itself.  What no cluster holds is read twice.
-#include "ctcpb_head.cuh"
+// will read itself.  What no cluster holds, or too few blocks would work on, takes
+// two launches (ctcpb_gnorm_split.cu).
+#include <type_traits>
+
+#include "ctcpb_gnorm.cuh"
 
 namespace ctcpb {
 namespace {
 
-constexpr int kGnThreads = 512;          // of a block at most
 constexpr int kGnRanks = 8;              // blocks that share a slab at most
 constexpr int kGnSmem = 200 * 1024;      // what a block keeps of a slab at most
 constexpr int kGnSmemShare = 72 * 1024;  // ... and where more blocks can share it: three on an SM
 constexpr int kGnPart = 4096;            // blocks of a backward launch that hold column sums
 constexpr long long kGnPartSize = 1 << 22;  // ... and their columns
 
-struct GnArgs {
-  const void *x, *dy;
-  void* y;  // or dx
-  long long x_b, x_t, dy_b, dy_t, y_b, y_t;
-  const void *weight, *bias;
-  int ptype;
-  const int* lengths;
-  int B, T, C, G, D;
-  float eps;
-  int act;
-  float *mean, *rstd;
-  float* part;  // [slots][2][C]
-  // geometry
-  int gs;      // groups of a slab
-  int tw;      // vectors of a row that the block takes at once
-  int tiles;   // ... and how often (more than once only where a slab is one group)
-  int rs;      // rows that the block takes at once
-  int slots;   // rows of a thread that shared memory holds
-  int ranks;
-};
-
-// V elements as one access.
-template <int BYTES>
-struct Raw;
-template <>
-struct Raw<16> {
-  typedef uint4 type;
-};
-template <>
-struct Raw<8> {
-  typedef uint2 type;
-};
-template <>
-struct Raw<4> {
-  typedef u32 type;
-};
-template <>
-struct Raw<2> {
-  typedef u16 type;
-};
-template <class T, int V>
-struct Vec {
-  static constexpr int bytes = V * (int)sizeof(T);
-  typename Raw<bytes>::type q;
-  __device__ __forceinline__ void get(float (&v)[V]) const {
-    const T* e = reinterpret_cast<const T*>(&q);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = Elem<T>::to(e[i]);
-  }
-  __device__ __forceinline__ void put(const float (&v)[V]) {
-    T* e = reinterpret_cast<T*>(&q);
-#pragma unroll
-    for (int i = 0; i < V; ++i) e[i] = Elem<T>::from(v[i]);
-  }
-  __device__ __forceinline__ void load(const T* p) { q = *reinterpret_cast<const decltype(q)*>(p); }
-  __device__ __forceinline__ void load_shared(u32 at) {
-    if constexpr (bytes == 16)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n"
-                   : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                   : "r"(at)
-                   : "memory");
-    else if constexpr (bytes == 8)
-      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];\n" : "=r"(q.x), "=r"(q.y) : "r"(at) : "memory");
-    else if constexpr (bytes == 4)
-      asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(q) : "r"(at) : "memory");
-  }
-  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<decltype(q)*>(p) = q; }
-};
-template <int BYTES>
-__device__ __forceinline__ void copy_async(u32 dst, const void* src) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
-
-// Count, mean and sum of squared distances from it; joined without a difference of
-// large sums (Chan, Golub, LeVeque).
-struct Moments {
-  float n, mean, m2;
-  __device__ __forceinline__ void join(const Moments& o) {
-    const float tot = n + o.n, share = tot > 0.f ? o.n / tot : 0.f, d = o.mean - mean;
-    mean = fmaf(d, share, mean);
-    m2 += fmaf(d * d, n * share, o.m2);
-    n = tot;
-  }
-};
-struct Two {
-  float a, b;
-  __device__ __forceinline__ void join(const Two& o) {
-    a += o.a;
-    b += o.b;
-  }
-};
+// The slab's sums over the blocks of the cluster, in order: `own` -> `all`.
 template <class S>
-__device__ __forceinline__ S shuffled(const S& s, int mask) {
-  constexpr int n = sizeof(S) / 4;
-  S r;
-#pragma unroll
-  for (int i = 0; i < n; ++i)
-    reinterpret_cast<float*>(&r)[i] = __shfl_xor_sync(0xffffffffu, reinterpret_cast<const float*>(&s)[i], mask);
-  return r;
-}
-
-__device__ __forceinline__ int frames_of(const GnArgs& a, int b) {
-  if (!a.lengths) return a.T;
-  const int n = a.lengths[b];
-  return n < 0 ? 0 : n > a.T ? a.T : n;
-}
-
-// What a block works on.
-struct Place {
-  int slab, rank, groups, c0, wv;  // groups and vectors of this slab, its first channel
-  int cv, ty;
-  bool on;  // the thread has a vector
-};
-template <int V>
-__device__ __forceinline__ Place place_of(const GnArgs& a) {
-  Place p;
-  p.slab = blockIdx.x / a.ranks;
-  p.rank = blockIdx.x - p.slab * a.ranks;
-  p.groups = a.G - p.slab * a.gs < a.gs ? a.G - p.slab * a.gs : a.gs;
-  p.c0 = p.slab * a.gs * a.D;
-  p.wv = p.groups * (a.D / V);
-  p.ty = threadIdx.x / a.tw;
-  p.cv = threadIdx.x - p.ty * a.tw;
-  p.on = p.ty < a.rs;
-  return p;
-}
-
-// The sums `s` of all threads by group (in `own`, [groups]), then over the blocks
-// of the slab (in `all`).  A warp per group; blocks in order.
-template <class S, int V>
-__device__ __forceinline__ void group_sums(const GnArgs& a, const Place& p, const S& s, S* each, S* own, S* all) {
-  each[threadIdx.x] = s;
-  __syncthreads();
-  const int dv = a.tiles > 1 ? a.tw : a.D / V, lane = threadIdx.x & 31;
-  for (int g = threadIdx.x >> 5; g < p.groups; g += blockDim.x >> 5) {
-    S t{};
-    for (int e = lane; e < dv * a.rs; e += 32) {
-      const int ty = e / dv;
-      t.join(each[ty * a.tw + g * dv + e - ty * dv]);
-    }
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) t.join(shuffled(t, m));
-    if (lane == 0) (a.ranks > 1 ? own : all)[g] = t;
-  }
-  if (a.ranks > 1) {
+__device__ __forceinline__ void over_cluster(const GnArgs& a, const Place& p, S* own, S* all) {
+  if (a.parts > 1) {
     cluster_sync();
     constexpr int n = sizeof(S) / 4;
     for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
       S t{};
-      for (int r = 0; r < a.ranks; ++r) {
+      for (int r = 0; r < a.parts; ++r) {
         S o;
         const u32 at = cluster_addr(saddr(own + g), r);
 #pragma unroll
@@ -189,317 +47,183 @@ __device__ __forceinline__ void group_sums(const GnArgs& a, const Place& p, cons
       }
       all[g] = t;
     }
-    // every block has read before any writes `own` again or leaves
+    // every block has read before any writes `own` again or leaves (over_cluster_done)
     asm volatile("barrier.cluster.arrive.release;\n" ::: "memory");
   }
   __syncthreads();
 }
-__device__ __forceinline__ void group_sums_done(const GnArgs& a) {
-  if (a.ranks > 1) asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory");
+__device__ __forceinline__ void over_cluster_done(const GnArgs& a) {
+  if (a.parts > 1) asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory");
 }
-
-// Rows of a rank: [first, end).
-__device__ __forceinline__ void rows_of(const GnArgs& a, const Place& p, int len, long long& first, long long& end) {
-  first = (u32)len * (u32)p.rank / (u32)a.ranks;  // len <= 2^24
-  end = (u32)len * (u32)(p.rank + 1) / (u32)a.ranks;
-}
-
-__device__ __forceinline__ float sigmoid(float h) { return __fdividef(1.f, 1.f + ex2(-kLog2e * h)); }
 
 template <class T, int V>
-__device__ __forceinline__ void zero_rows(const GnArgs& a, const Place& p, T* yb, int len) {
-  Vec<T, V> z;
-  float v[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = 0.f;
-  z.put(v);
-  if (!p.on) return;
-  for (int tile = 0; tile < a.tiles; ++tile) {
-    const int at = tile * a.tw + p.cv;
-    if (at >= p.wv) break;
-    for (long long r = len + p.rank * a.rs + p.ty; r < a.T; r += a.ranks * a.rs) z.store(yb + r * a.y_t + at * V);
-  }
-}
-
-template <int V>
-__device__ __forceinline__ void params_of(const GnArgs& a, int c, float (&w)[V], float (&b)[V]) {
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    w[i] = a.weight ? load_elem(a.weight, a.ptype, c + i) : 1.f;
-    b[i] = a.bias ? load_elem(a.bias, a.ptype, c + i) : 0.f;
-  }
-}
-
-// RES: the slab stays in shared memory.
-template <class T, int V, bool RES>
-__global__ void __launch_bounds__(kGnThreads) k_gn(const GnArgs a) {
+__global__ void __launch_bounds__(kGnThreads, 2) k_gn(const GnArgs a) {
   extern __shared__ __align__(16) char smem[];
   typedef Vec<T, V> W;
-  constexpr int kRows = 4;
+  constexpr int P = W::P;
   Moments* const each = reinterpret_cast<Moments*>(smem);
   Moments* const own = each + blockDim.x;
   Moments* const all = own + a.gs;
   const u32 keep = (saddr(all + a.gs) + 15u & ~15u) + threadIdx.x * W::bytes;
   const u32 pitch = blockDim.x * W::bytes;
+  Place p;
+  p.set<V>(a, blockIdx.x / a.parts, blockIdx.x % a.parts);
   pdl_wait();
   pdl_next();
-  const Place p = place_of<V>(a);
-  const int dv = a.D / V;
+  u64 w[P], bias[P];
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
     const int len = frames_of(a, b);
-    long long first, end;
-    rows_of(a, p, len, first, end);
-    const T* const xb = (const T*)a.x + (long long)b * a.x_b + p.c0;
-    T* const yb = (T*)a.y + (long long)b * a.y_b + p.c0;
-    first += p.ty;
-    const int n = first < end ? ((int)(end - first) + a.rs - 1) / a.rs : 0;  // rows of this thread
-    const long long x_step = a.rs * a.x_t, y_step = a.rs * a.y_t;
-    // row k of the thread's vector `at` of a tile
-    auto fetch = [&](W& v, int tile, int at, int k) {
-      if constexpr (RES)
-        v.load_shared(keep + (tile * a.slots + k) * pitch);
-      else
-        v.load(xb + first * a.x_t + at * V + k * x_step);
-    };
-    if constexpr (RES) {
-      if (p.on)
-        for (int tile = 0; tile < a.tiles; ++tile) {
-          const int at = tile * a.tw + p.cv;
-          u32 to = keep + tile * a.slots * pitch;
-          const T* from = xb + first * a.x_t + at * V;
-          if (at < p.wv)
-            for (int k = 0; k < n; ++k, to += pitch, from += x_step) copy_async<W::bytes>(to, from);
-        }
-      cp_wait_all();
-    }
-    Moments m{0.f, 0.f, 0.f};
-    if (p.on)
-      for (int tile = 0; tile < a.tiles; ++tile) {
-        const int at = tile * a.tw + p.cv;
-        if (at >= p.wv) break;
-        for (int k0 = 0; k0 < n; k0 += kRows) {
-          W raw[kRows];
-          float v[kRows][V];
-          const int here = n - k0 < kRows ? n - k0 : kRows;
+    const Rows rows(a, p, len);
+    const T* const x = (const T*)a.x + (long long)b * a.x_b + p.c0;
+    T* const y = (T*)a.y + (long long)b * a.y_b + p.c0;
+    fetch_rows<T, V>(keep, pitch, x + rows.first * a.x_t + p.cv * V, a.rs * a.x_t, rows.n);
+    params_of<V>(a, p.c0 + p.cv * V, p.on, w, bias);
+    cp_wait_all();
+    u64 s[P];
 #pragma unroll
-          for (int k = 0; k < kRows; ++k)
-            if (k < here) fetch(raw[k], tile, at, k0 + k);
-          float s = 0.f, q = 0.f;
-#pragma unroll
-          for (int k = 0; k < kRows; ++k)
-            if (k < here) {
-              raw[k].get(v[k]);
-#pragma unroll
-              for (int i = 0; i < V; ++i) s += v[k][i];
-            }
-          const float cnt = (float)(here * V), mean = s / cnt;
-#pragma unroll
-          for (int k = 0; k < kRows; ++k)
-            if (k < here) {
-#pragma unroll
-              for (int i = 0; i < V; ++i) q = fmaf(v[k][i] - mean, v[k][i] - mean, q);
-            }
-          m.join(Moments{cnt, mean, q});
-        }
-      }
-    group_sums<Moments, V>(a, p, m, each, own, all);
-    if (a.mean && p.rank == 0)
-      for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
-        const long long o = (long long)b * a.G + p.slab * a.gs + g;
-        a.mean[o] = all[g].mean;
-        a.rstd[o] = len > 0 ? rsqrtf(all[g].m2 / all[g].n + a.eps) : 0.f;
-      }
-    if (p.on)
-      for (int tile = 0; tile < a.tiles; ++tile) {
-        const int at = tile * a.tw + p.cv;
-        if (at >= p.wv) break;
-        const Moments t = all[at / dv];
-        const float rstd = rsqrtf(t.m2 / t.n + a.eps), mean = t.mean;
-        float w[V], bias[V];
-        params_of<V>(a, p.c0 + at * V, w, bias);
-#pragma unroll
-        for (int i = 0; i < V; ++i) w[i] *= rstd;
-        T* to = yb + first * a.y_t + at * V;
+    for (int i = 0; i < P; ++i) s[i] = 0;
 #pragma unroll 4
-        for (int k = 0; k < n; ++k, to += y_step) {
-          W raw;
-          float v[V];
-          fetch(raw, tile, at, k);
-          raw.get(v);
+    for (int k = 0; k < rows.n; ++k) {
+      W raw;
+      u64 v[P];
+      raw.load_shared(keep + k * pitch);
+      raw.get(v);
 #pragma unroll
-          for (int i = 0; i < V; ++i) v[i] = fmaf(v[i] - mean, w[i], bias[i]);
-          if (a.act == CTCPB_ACT_SILU) {
+      for (int i = 0; i < P; ++i) s[i] = add2(s[i], v[i]);
+    }
+    Moments m{(float)(rows.n * V), 0.f, 0.f};
+    if (rows.n > 0) m.mean = lanes<V>(s) / m.n;
+    u64 nm = pair(-m.mean, -m.mean);
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] *= sigmoid(v[i]);
-          } else if (a.act == CTCPB_ACT_RELU) {
+    for (int i = 0; i < P; ++i) s[i] = 0;
+#pragma unroll 4
+    for (int k = 0; k < rows.n; ++k) {
+      W raw;
+      u64 v[P];
+      raw.load_shared(keep + k * pitch);
+      raw.get(v);
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = v[i] > 0.f ? v[i] : v[i] != v[i] ? v[i] : 0.f;
-          }
-          raw.put(v);
-          raw.store(to);
-        }
+      for (int i = 0; i < P; ++i) {
+        v[i] = add2(v[i], nm);
+        s[i] = fma2(v[i], v[i], s[i]);
       }
-    zero_rows<T, V>(a, p, yb, len);
-    group_sums_done(a);
+    }
+    m.m2 = lanes<V>(s);
+    by_group<Moments, V>(a, p, m, each, [&](int g, const Moments& t) { (a.parts > 1 ? own : all)[g] = t; });
+    over_cluster(a, p, own, all);
+    if (a.mean && p.part == 0)
+      for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
+        const long long o = (long long)b * a.G + p.g0 + g;
+        a.mean[o] = all[g].mean;
+        a.rstd[o] = len > 0 ? all[g].rstd(a.eps) : 0.f;
+      }
+    const Moments t = all[p.group<V>(a)];
+    const float rstd = t.rstd(a.eps);
+    nm = pair(-t.mean, -t.mean);
+#pragma unroll
+    for (int i = 0; i < P; ++i) w[i] = mul2(w[i], pair(rstd, rstd));
+    const long long step = a.rs * a.y_t;
+    T* to = y + rows.first * a.y_t + p.cv * V;
+#pragma unroll 2
+    for (int k = 0; k < rows.n; ++k, to += step) {
+      W raw;
+      u64 v[P];
+      raw.load_shared(keep + k * pitch);
+      raw.get(v);
+      activate(v, nm, w, bias, a.act);
+      raw.put(v);
+      raw.store(to);
+    }
+    zero_rows<T, V>(a, p, y, len);
+    over_cluster_done(a);
     __syncthreads();
   }
 }
 
-template <class T, int V, bool RES>
-__global__ void __launch_bounds__(kGnThreads) k_gn_bwd(const GnArgs a) {
+template <class T, int V>
+__global__ void __launch_bounds__(kGnThreads, 2) k_gn_bwd(const GnArgs a) {
   extern __shared__ __align__(16) char smem[];
   typedef Vec<T, V> W;
+  constexpr int P = W::P;
   Two* const each = reinterpret_cast<Two*>(smem);
   Two* const own = each + blockDim.x;
   Two* const all = own + a.gs;
-  const u32 keep = (saddr(all + a.gs) + 15u & ~15u) + threadIdx.x * W::bytes;
-  const u32 pitch = blockDim.x * W::bytes, second = a.tiles * a.slots * pitch;  // dy lies behind x
+  float* const red = reinterpret_cast<float*>(all + a.gs);
+  const u32 keep = (saddr(red + (a.cols ? 2 * a.cr * a.tw * V : 0)) + 15u & ~15u) + threadIdx.x * W::bytes;
+  const u32 pitch = blockDim.x * W::bytes, second = a.slots * pitch;  // dy lies behind x
+  Place p;
+  p.set<V>(a, blockIdx.x / a.parts, blockIdx.x % a.parts);
   pdl_wait();
   pdl_next();
-  const Place p = place_of<V>(a);
-  const int dv = a.D / V;
-  float* const part = a.part ? a.part + (long long)(blockIdx.y * a.ranks + p.rank) * 2 * a.C + p.c0 : nullptr;
-  float tw[V], tb[V];  // column sums (one tile)
-#pragma unroll
-  for (int i = 0; i < V; ++i) tw[i] = tb[i] = 0.f;
+  u64 w[P], bias[P];
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
     const int len = frames_of(a, b);
-    long long first, end;
-    rows_of(a, p, len, first, end);
-    const T* const xb = (const T*)a.x + (long long)b * a.x_b + p.c0;
-    const T* const db = (const T*)a.dy + (long long)b * a.dy_b + p.c0;
-    T* const yb = (T*)a.y + (long long)b * a.y_b + p.c0;
-    first += p.ty;
-    const int n = first < end ? ((int)(end - first) + a.rs - 1) / a.rs : 0;
-    const long long x_step = a.rs * a.x_t, d_step = a.rs * a.dy_t, y_step = a.rs * a.y_t;
-    auto fetch = [&](float (&x)[V], float (&d)[V], int tile, int at, int k) {
-      W v, u;
-      if constexpr (RES) {
-        const u32 from = keep + (tile * a.slots + k) * pitch;
-        v.load_shared(from);
-        u.load_shared(from + second);
-      } else {
-        v.load(xb + first * a.x_t + at * V + k * x_step);
-        u.load(db + first * a.dy_t + at * V + k * d_step);
-      }
-      v.get(x);
-      u.get(d);
-    };
-    if constexpr (RES) {
-      if (p.on)
-        for (int tile = 0; tile < a.tiles; ++tile) {
-          const int at = tile * a.tw + p.cv;
-          u32 to = keep + tile * a.slots * pitch;
-          const T *px = xb + first * a.x_t + at * V, *pd = db + first * a.dy_t + at * V;
-          if (at < p.wv)
-            for (int k = 0; k < n; ++k, to += pitch, px += x_step, pd += d_step) {
-              copy_async<W::bytes>(to, px);
-              copy_async<W::bytes>(to + second, pd);
-            }
-        }
-      cp_wait_all();
-    }
-    // xh into x, the gradient before the activation into d
-    auto before = [&](float (&x)[V], float (&d)[V], const float (&w)[V], const float (&bias)[V], float mean, float rstd) {
+    const Rows rows(a, p, len);
+    const T* const x = (const T*)a.x + (long long)b * a.x_b + p.c0;
+    const T* const dy = (const T*)a.dy + (long long)b * a.dy_b + p.c0;
+    fetch_rows<T, V>(keep, pitch, x + rows.first * a.x_t + p.cv * V, a.rs * a.x_t, rows.n);
+    fetch_rows<T, V>(keep + second, pitch, dy + rows.first * a.dy_t + p.cv * V, a.rs * a.dy_t, rows.n);
+    params_of<V>(a, p.c0 + p.cv * V, p.on, w, bias);
+    const long long o = (long long)b * a.G + p.g0 + p.group<V>(a);
+    const float mean = a.mean[o], rstd = a.rstd[o];
+    const u64 nm = pair(-mean, -mean), rr = pair(rstd, rstd);
+    cp_wait_all();
+    u64 sw[P], sb[P];
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = (x[i] - mean) * rstd;
-      if (a.act == CTCPB_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float h = fmaf(x[i], w[i], bias[i]), s = sigmoid(h);
-          d[i] *= s * fmaf(h, 1.f - s, 1.f);
-        }
-      } else if (a.act == CTCPB_ACT_RELU) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = fmaf(x[i], w[i], bias[i]) > 0.f ? d[i] : 0.f;
-      }
-    };
-    Two m{0.f, 0.f};
-    if (p.on)
-      for (int tile = 0; tile < a.tiles; ++tile) {
-        const int at = tile * a.tw + p.cv;
-        if (at >= p.wv) break;
-        const long long o = (long long)b * a.G + p.slab * a.gs + at / dv;
-        const float mean = a.mean[o], rstd = a.rstd[o];
-        float w[V], bias[V], sw[V], sb[V];
-        params_of<V>(a, p.c0 + at * V, w, bias);
-#pragma unroll
-        for (int i = 0; i < V; ++i) sw[i] = sb[i] = 0.f;
+    for (int i = 0; i < P; ++i) sw[i] = sb[i] = 0;
 #pragma unroll 2
-        for (int k = 0; k < n; ++k) {
-          float x[V], d[V];
-          fetch(x, d, tile, at, k);
-          before(x, d, w, bias, mean, rstd);
+    for (int k = 0; k < rows.n; ++k) {
+      W raw;
+      u64 v[P], d[P];
+      raw.load_shared(keep + k * pitch);
+      raw.get(v);
+      raw.load_shared(keep + second + k * pitch);
+      raw.get(d);
+      before(v, d, nm, rr, w, bias, a.act);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            sw[i] = fmaf(d[i], x[i], sw[i]);
-            sb[i] += d[i];
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          m.a = fmaf(sb[i], w[i], m.a);
-          m.b = fmaf(sw[i], w[i], m.b);
-          if (a.tiles == 1) {
-            tw[i] += sw[i];
-            tb[i] += sb[i];
-          } else if (part) {  // the thread alone has these columns
-            float* const q = part + at * V + i;
-            const bool begun = b != (int)blockIdx.y;
-            q[0] = begun ? q[0] + sw[i] : sw[i];
-            q[a.C] = begun ? q[a.C] + sb[i] : sb[i];
-          }
-        }
+      for (int i = 0; i < P; ++i) {
+        sw[i] = fma2(d[i], v[i], sw[i]);
+        sb[i] = add2(sb[i], d[i]);
       }
+    }
+    Two m;
+    {
+      u64 t[P];
+#pragma unroll
+      for (int i = 0; i < P; ++i) t[i] = mul2(sb[i], w[i]);
+      m.a = lanes<V>(t);
+#pragma unroll
+      for (int i = 0; i < P; ++i) t[i] = mul2(sw[i], w[i]);
+      m.b = lanes<V>(t);
+    }
+    if (a.cols) column_sums<V>(a, p, sw, sb, red, (long long)blockIdx.y * a.parts + p.part, b != (int)blockIdx.y);
     if (a.y) {
-      group_sums<Two, V>(a, p, m, each, own, all);
-      const float inv = len > 0 ? 1.f / ((float)len * (float)a.D) : 0.f;
-      if (p.on)
-        for (int tile = 0; tile < a.tiles; ++tile) {
-          const int at = tile * a.tw + p.cv;
-          if (at >= p.wv) break;
-          const long long o = (long long)b * a.G + p.slab * a.gs + at / dv;
-          const float mean = a.mean[o], rstd = a.rstd[o];
-          const Two t = all[at / dv];
-          const float m0 = t.a * inv, m1 = t.b * inv;
-          float w[V], bias[V];
-          params_of<V>(a, p.c0 + at * V, w, bias);
-          T* to = yb + first * a.y_t + at * V;
+      T* const y = (T*)a.y + (long long)b * a.y_b + p.c0;
+      by_group<Two, V>(a, p, m, each, [&](int g, const Two& t) { (a.parts > 1 ? own : all)[g] = t; });
+      over_cluster(a, p, own, all);
+      const Two t = all[p.group<V>(a)];
+      const float inv = len > 0 ? 1.f / ((float)len * (float)a.D) : 0.f, c0 = -rstd * t.a * inv, c1 = -rstd * t.b * inv;
+      const u64 m0 = pair(c0, c0), m1 = pair(c1, c1);
+      const long long step = a.rs * a.y_t;
+      T* to = y + rows.first * a.y_t + p.cv * V;
 #pragma unroll 2
-          for (int k = 0; k < n; ++k, to += y_step) {
-            float x[V], d[V];
-            fetch(x, d, tile, at, k);
-            before(x, d, w, bias, mean, rstd);
+      for (int k = 0; k < rows.n; ++k, to += step) {
+        W raw;
+        u64 v[P], d[P];
+        raw.load_shared(keep + k * pitch);
+        raw.get(v);
+        raw.load_shared(keep + second + k * pitch);
+        raw.get(d);
+        before(v, d, nm, rr, w, bias, a.act);
 #pragma unroll
-            for (int i = 0; i < V; ++i) d[i] = rstd * fmaf(-x[i], m1, fmaf(d[i], w[i], -m0));
-            W out;
-            out.put(d);
-            out.store(to);
-          }
-        }
-      zero_rows<T, V>(a, p, yb, len);
-      group_sums_done(a);
-      __syncthreads();
+        for (int i = 0; i < P; ++i) d[i] = fma2(mul2(d[i], w[i]), rr, fma2(v[i], m1, m0));
+        raw.put(d);
+        raw.store(to);
+      }
+      zero_rows<T, V>(a, p, y, len);
+      over_cluster_done(a);
     }
-  }
-  if (!part || a.tiles > 1) return;
-  // column sums over the threads that share them, in order (the slab's memory is free now)
-  float* const cols = reinterpret_cast<float*>(smem);  // [rs][2][tw * V]
-  const int width = a.tw * V;
-  __syncthreads();
-  if (p.on)
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      cols[(2 * p.ty) * width + p.cv * V + i] = tw[i];
-      cols[(2 * p.ty + 1) * width + p.cv * V + i] = tb[i];
-    }
-  __syncthreads();
-  for (int e = threadIdx.x; e < 2 * width; e += blockDim.x) {
-    const int c = e < width ? e : e - width;
-    if (c >= p.wv * V) continue;
-    float s = 0.f;
-    for (int k = 0; k < a.rs; ++k) s += cols[2 * k * width + e];
-    part[(e < width ? 0 : a.C) + c] = s;
+    __syncthreads();
   }
 }
 
@@ -531,12 +255,6 @@ __global__ void __launch_bounds__(1024) k_gn_cols(const float* __restrict__ part
   }
 }
 
-struct GnShape {
-  int v;  // elements of an access
-  int threads, gs, tw, tiles, rs, slots, ranks, slabs, by;
-  bool res;
-  size_t smem;
-};
 // Elements of one access: a group's channels and every row start at its multiples.
 int gn_vec(int type, int D, uintptr_t at, long long strides) {
   const int e = type == CTCPB_F32 ? 4 : 2;
@@ -554,74 +272,74 @@ GnShape gn_shape(int type, int v, int B, int T, int C, int G, bool bwd) {
   s.gs = 128 / (D * e) > 1 ? 128 / (D * e) : 1;
   while (s.gs < G && (long long)s.gs * dv * T < 32) s.gs *= 2;
   if (s.gs > G) s.gs = G;
-  s.slabs = (G + s.gs - 1) / s.gs;
-  const int wv = s.gs * dv;
-  s.threads = wv > 256 ? up32(wv) : up32((long long)wv * T < 256 ? (long long)wv * T : 256);
-  if (s.threads > kGnThreads) s.threads = kGnThreads;
+  s.pieces = s.gs * dv > kGnThreads ? (dv + kGnThreads - 1) / kGnThreads : 1;
+  s.tw = s.pieces > 1 ? (dv + s.pieces - 1) / s.pieces : s.gs * dv;
+  s.slabs = s.pieces > 1 ? G * s.pieces : (G + s.gs - 1) / s.gs;
+  s.threads = s.tw > 256 ? up32(s.tw) : up32((long long)s.tw * T < 256 ? (long long)s.tw * T : 256);
   if (s.threads < 32) s.threads = 32;
-  s.tw = wv < s.threads ? wv : s.threads;
-  s.tiles = (wv + s.tw - 1) / s.tw;
   s.rs = s.threads / s.tw;
-  const size_t stat = align_up((size_t)(s.threads + 2 * s.gs) * (bwd ? sizeof(Two) : sizeof(Moments)), 16);
+  s.cr = 32 % s.tw == 0 && s.rs * s.tw == s.threads ? s.threads / 32 : s.rs;
+  const size_t stat = align_up((size_t)(s.threads + 2 * s.gs) * (bwd ? sizeof(Two) : sizeof(Moments)) +
+                                   (bwd ? (size_t)s.cr * 2 * s.tw * v * 4 : 0), 16);
   auto slab = [&](int ranks) {
     s.slots = ((T + ranks - 1) / ranks + s.rs - 1) / s.rs;
-    return (size_t)s.slots * s.tiles * s.threads * v * e * (bwd ? 2 : 1);
+    return (size_t)s.slots * s.threads * v * e * (bwd ? 2 : 1);
   };
-  s.ranks = 1;
-  while (s.ranks < kGnRanks && T > 2 * s.ranks * s.rs &&
-         (slab(s.ranks) > (size_t)kGnSmemShare || (long long)B * s.slabs * s.ranks < 304))
-    s.ranks *= 2;
-  s.smem = slab(s.ranks);
-  s.res = v * e >= 4 && s.smem <= (size_t)kGnSmem;
-  s.smem = stat + (s.res ? s.smem : 0);
-  if (bwd && s.tiles == 1) {
-    const size_t cols = (size_t)s.rs * 2 * s.tw * v * 4;
-    if (s.smem < cols) s.smem = cols;
+  s.parts = 1;
+  while (s.parts < kGnRanks && T > 2 * s.parts * s.rs &&
+         (slab(s.parts) > (size_t)kGnSmemShare || (long long)B * s.slabs * s.parts < 304))
+    s.parts *= 2;
+  s.smem = stat + slab(s.parts);
+  s.split = s.pieces > 1 || s.smem > (size_t)kGnSmem;
+  if (s.split) {  // so many chunks of frames that the blocks fill the SMs, eight of a thread's rows in each at least
+    const long long most = ((long long)T + 8 * s.rs - 1) / (8 * s.rs);
+    long long parts = (152 * 6 + (long long)B * s.slabs - 1) / ((long long)B * s.slabs);
+    if (parts > most) parts = most;
+    s.parts = (int)(parts > 1 ? parts : 1);
+    s.smem = stat;
   }
   long long by = B;
   if (bwd) {  // column sums of so many blocks at most
-    long long cap = kGnPart / ((long long)s.slabs * s.ranks), room = kGnPartSize / C / s.ranks;
+    long long cap = kGnPart / ((long long)s.slabs * s.parts), room = kGnPartSize / C / s.parts;
     if (cap > room) cap = room;
     if (by > cap) by = cap > 1 ? cap : 1;
   }
   s.by = (int)(by < 65535 ? by : 65535);
   return s;
 }
+// Workspace: the column sums, then the groups' sums of a split call.
+struct GnLayout {
+  size_t o_group, total;
+};
+GnLayout gn_layout(const GnShape& s, int B, int C, int G, bool bwd) {
+  GnLayout l{};
+  l.o_group = bwd ? align_up((size_t)s.by * s.parts * 2 * C * 4, 256) : 0;
+  l.total = l.o_group + (s.split ? align_up((size_t)B * s.parts * G * s.pieces * (bwd ? sizeof(Two) : sizeof(Moments)), 256) : 0);
+  return l;
+}
 
-template <class T, int V>
-cudaError_t gn_run(bool bwd, GnArgs& a, const GnShape& s, cudaStream_t st) {
+template <class T>
+cudaError_t gn_whole(bool bwd, const GnArgs& a, const GnShape& s, cudaStream_t st) {
+  return gn_each_vec<T>(s.v, [&](auto, auto vc) {
+    constexpr int V = decltype(vc)::value;
+    constexpr auto f = k_gn<T, V>, g = k_gn_bwd<T, V>;
+    const cudaError_t e = bwd ? smem_optin<g>(s.smem) : smem_optin<f>(s.smem);
+    return e != cudaSuccess ? e : launch(bwd ? g : f, dim3(s.slabs * s.parts, s.by), s.threads, s.smem, st, s.parts, a);
+  });
+}
+cudaError_t gn_run(int type, bool bwd, GnArgs& a, const GnShape& s, cudaStream_t st) {
   a.gs = s.gs;
+  a.pieces = s.pieces;
   a.tw = s.tw;
-  a.tiles = s.tiles;
   a.rs = s.rs;
   a.slots = s.slots;
-  a.ranks = s.ranks;
-  const dim3 grid(s.slabs * s.ranks, s.by);
-  auto go = [&](auto kern, cudaError_t e) {
-    return e != cudaSuccess ? e : launch(kern, grid, s.threads, s.smem, st, s.ranks, a);
-  };
-  if constexpr (V * sizeof(T) >= 4) {
-    if (s.res) {
-      constexpr auto f = k_gn<T, V, true>, g = k_gn_bwd<T, V, true>;
-      return bwd ? go(g, smem_optin<g>(s.smem)) : go(f, smem_optin<f>(s.smem));
-    }
-  }
-  constexpr auto f = k_gn<T, V, false>, g = k_gn_bwd<T, V, false>;
-  return bwd ? go(g, smem_optin<g>(s.smem)) : go(f, smem_optin<f>(s.smem));
-}
-template <class T>
-cudaError_t gn_run_v(bool bwd, GnArgs& a, const GnShape& s, cudaStream_t st) {
-  if constexpr (sizeof(T) == 2) {
-    if (s.v == 8) return gn_run<T, 8>(bwd, a, s, st);
-  }
-  if (s.v == 4) return gn_run<T, 4>(bwd, a, s, st);
-  if (s.v == 2) return gn_run<T, 2>(bwd, a, s, st);
-  return gn_run<T, 1>(bwd, a, s, st);
-}
-cudaError_t gn_run_t(int type, bool bwd, GnArgs& a, const GnShape& s, cudaStream_t st) {
-  if (type == CTCPB_F32) return gn_run_v<float>(bwd, a, s, st);
-  if (type == CTCPB_BF16) return gn_run_v<__nv_bfloat16>(bwd, a, s, st);
-  return gn_run_v<__half>(bwd, a, s, st);
+  a.parts = s.parts;
+  a.cr = s.cr;
+  a.by = s.by;
+  if (s.split) return gn_split(type, bwd, a, s, st);
+  if (type == CTCPB_F32) return gn_whole<float>(bwd, a, s, st);
+  if (type == CTCPB_BF16) return gn_whole<__nv_bfloat16>(bwd, a, s, st);
+  return gn_whole<__half>(bwd, a, s, st);
 }
 
 int gn_check(int type, int ptype, int act, int B, int T, int C, int G) {
@@ -631,6 +349,27 @@ int gn_check(int type, int ptype, int act, int B, int T, int C, int G) {
   if (B < 0 || T < 0 || (long long)B * T > kHeadMaxRows || B > kHeadMaxRows || T > kHeadMaxRows || C < 1 ||
       C > kHeadMaxWidth || G < 1 || C % G)
     return CTCPB_EINVAL;
+  return CTCPB_OK;
+}
+
+// The most that any alignment of a call's tensors needs.
+size_t gn_need(int type, int B, int T, int C, int G, bool bwd) {
+  size_t most = 0;
+  if (B > 0)
+    for (int v = gn_vec(type, C / G, 0, 0); v >= 1; v /= 2) {
+      const size_t n = gn_layout(gn_shape(type, v, B, T, C, G, bwd), B, C, G, bwd).total;
+      if (n > most) most = n;
+    }
+  return most;
+}
+int gn_workspace(GnArgs& a, int type, const GnShape& s, int B, int T, int C, int G, bool bwd, void* ws, size_t ws_bytes) {
+  const size_t need = gn_need(type, B, T, C, G, bwd);
+  if (need == 0) return CTCPB_OK;
+  if (!ws) return CTCPB_ENULL;
+  if (((uintptr_t)ws & 255u) != 0) return CTCPB_EALIGN;
+  if (ws_bytes < need) return CTCPB_ESIZE;
+  a.cols = bwd ? (float*)ws : nullptr;
+  a.group = (float*)((char*)ws + gn_layout(s, B, C, G, bwd).o_group);
   return CTCPB_OK;
 }
 
@@ -644,7 +383,7 @@ extern "C" {
 int ctcpb_group_norm(int type, int param_type, const void* x, int64_t x_stride_b, int64_t x_stride_t,
                      const void* weight, const void* bias, const int32_t* lengths, float eps, int activation, int B,
                      int T, int C, int G, void* y, int64_t y_stride_b, int64_t y_stride_t, float* mean, float* rstd,
-                     ctcpb_stream_t stream) {
+                     void* ws, size_t ws_bytes, ctcpb_stream_t stream) {
   int rc = gn_check(type, weight || bias ? param_type : type, activation, B, T, C, G);
   if (rc) return rc;
   if (!(eps >= 0.f)) return CTCPB_EINVAL;
@@ -674,17 +413,16 @@ int ctcpb_group_norm(int type, int param_type, const void* x, int64_t x_stride_b
   a.rstd = rstd;
   const int v = gn_vec(type, a.D, (uintptr_t)x | (uintptr_t)y, x_stride_b | x_stride_t | y_stride_b | y_stride_t);
   const GnShape s = gn_shape(type, v, B, T, C, G, false);
-  return gn_run_t(type, false, a, s, (cudaStream_t)stream) == cudaSuccess ? CTCPB_OK : CTCPB_ECUDA;
+  if ((rc = gn_workspace(a, type, s, B, T, C, G, false, ws, ws_bytes))) return rc;
+  return gn_run(type, false, a, s, (cudaStream_t)stream) == cudaSuccess ? CTCPB_OK : CTCPB_ECUDA;
 }
 
-int ctcpb_group_norm_workspace_size(int B, int T, int C, int G, size_t* bytes) {
-  int rc = gn_check(CTCPB_F32, CTCPB_F32, CTCPB_ACT_NONE, B, T, C, G);
+int ctcpb_group_norm_workspace_size(int type, int B, int T, int C, int G, int backward, size_t* bytes) {
+  int rc = gn_check(type, type, CTCPB_ACT_NONE, B, T, C, G);
   if (rc) return rc;
+  if (backward != 0 && backward != 1) return CTCPB_EINVAL;
   if (!bytes) return CTCPB_ENULL;
-  long long rows = kGnPartSize / C < kGnPart ? kGnPartSize / C : kGnPart;
-  if (rows < kGnRanks) rows = kGnRanks;
-  if (rows > (long long)B * kGnRanks) rows = (long long)B * kGnRanks;
-  *bytes = align_up((size_t)(rows > 0 ? rows : 1) * 2 * C * 4, 256);
+  *bytes = gn_need(type, B, T, C, G, backward);
   return CTCPB_OK;
 }
 
@@ -703,13 +441,6 @@ int ctcpb_group_norm_backward(int type, int param_type, const void* dy, int64_t 
               (dx && (dx_stride_t < C || dx_stride_b < 0))))
     return CTCPB_EINVAL;
   if (any && (!dy || !x || !mean || !rstd)) return CTCPB_ENULL;
-  if (cols) {
-    size_t need = 0;
-    if ((rc = ctcpb_group_norm_workspace_size(B, T, C, G, &need))) return rc;
-    if (!ws) return CTCPB_ENULL;
-    if (((uintptr_t)ws & 255u) != 0) return CTCPB_EALIGN;
-    if (ws_bytes < need) return CTCPB_ESIZE;
-  }
   cudaStream_t st = (cudaStream_t)stream;
   int rows = 0;
   if (any) {
@@ -735,12 +466,13 @@ int ctcpb_group_norm_backward(int type, int param_type, const void* dy, int64_t 
     a.act = activation;
     a.mean = const_cast<float*>(mean);
     a.rstd = const_cast<float*>(rstd);
-    a.part = cols ? (float*)ws : nullptr;
     const int v = gn_vec(type, a.D, (uintptr_t)x | (uintptr_t)dy | (uintptr_t)dx,
                          x_stride_b | x_stride_t | dy_stride_b | dy_stride_t | a.y_b | a.y_t);
     const GnShape s = gn_shape(type, v, B, T, C, G, true);
-    rows = s.by * s.ranks;
-    if (gn_run_t(type, true, a, s, st) != cudaSuccess) return CTCPB_ECUDA;
+    if ((rc = gn_workspace(a, type, s, B, T, C, G, true, ws, ws_bytes))) return rc;
+    if (!cols) a.cols = nullptr;
+    rows = s.by * s.parts;
+    if (gn_run(type, true, a, s, st) != cudaSuccess) return CTCPB_ECUDA;
   }
   if (cols && launch(k_gn_cols, (2 * C + 31) / 32, 1024, 0, st, 1, (const float*)ws, rows, C, param_type, dweight, dbias) !=
                   cudaSuccess)

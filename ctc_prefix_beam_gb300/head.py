@@ -61,8 +61,8 @@ def _lib():
             "ctcpb_cross_entropy": [I, I, P, I64, P, I64, P, P, I64, I, I, I, I, P, P, P, SZ, P],
             "ctcpb_cross_entropy_backward": [I, I, P, P, I64, P, I64, P, P, P, I64, I, I, I, I, P, I64, P, I64, P, P, SZ,
                                              P],
-            "ctcpb_group_norm": [I, I, P, I64, I64, P, P, P, F, I, I, I, I, I, P, I64, I64, P, P, P],
-            "ctcpb_group_norm_workspace_size": [I, I, I, I, SZP],
+            "ctcpb_group_norm": [I, I, P, I64, I64, P, P, P, F, I, I, I, I, I, P, I64, I64, P, P, P, SZ, P],
+            "ctcpb_group_norm_workspace_size": [I, I, I, I, I, I, SZP],
             "ctcpb_group_norm_backward": [I, I, P, I64, I64, P, I64, I64, P, P, P, P, P, I, I, I, I, I, P, I64, I64, P, P, P,
                                           SZ, P],
             "ctcpb_dropout": [I, P, I64, P, I64, DBL, P, I64, I, P, I64, P],
@@ -150,6 +150,8 @@ def _size(name: str, *args) -> int:
 
 
 def _workspace(ws, need: int, device):
+    if need == 0:
+        return None, 0
     if ws is None:  # PyTorch's allocations start on 512-byte boundaries
         return torch.empty(need, dtype=torch.uint8, device=device), need
     return ws, D._check_buf(ws, need, device, "workspace")
@@ -365,7 +367,8 @@ def _groups(groups: int, C: int) -> int:
 
 
 def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
-               *, lengths: Optional[torch.Tensor] = None, eps: float = 1e-5, activation: str = "none", outputs=None):
+               *, lengths: Optional[torch.Tensor] = None, eps: float = 1e-5, activation: str = "none", outputs=None,
+               workspace: Optional[torch.Tensor] = None):
     """Group norm and an activation (none, relu, silu) over channels-last frames
     [B, T, C]: a group's statistics are over its channels and an utterance's first
     ``lengths[b]`` (int32 [B]) frames; later frames are not read, and y is 0 there.
@@ -386,13 +389,14 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
         _given(y, x.shape, dt, dev, "y")
         _given(mean, (B, G), torch.float32, dev, "mean")
         _given(rstd, (B, G), torch.float32, dev, "rstd")
+    ws, nbytes = _workspace(workspace, group_norm_workspace_size(dt, B, T, C, G, False), dev)
     _run(dev, "ctcpb_group_norm", _TYPES[dt], _TYPES[pt], _p(xr), sb, st, _p(w), _p(b), _p(n), eps, act, B, T, C, G, _p(y),
-         T * C, C, _p(mean), _p(rstd))
+         T * C, C, _p(mean), _p(rstd), _p(ws), nbytes)
     return y, mean, rstd
 
 
-def group_norm_workspace_size(B: int, T: int, C: int, groups: int) -> int:
-    return _size("ctcpb_group_norm_workspace_size", B, T, C, groups)
+def group_norm_workspace_size(dtype, B: int, T: int, C: int, groups: int, backward: bool) -> int:
+    return _size("ctcpb_group_norm_workspace_size", _TYPES[dtype], B, T, C, groups, int(bool(backward)))
 
 
 def group_norm_backward(dy: torch.Tensor, x: torch.Tensor, groups: int, weight: Optional[torch.Tensor],
@@ -420,7 +424,7 @@ def group_norm_backward(dy: torch.Tensor, x: torch.Tensor, groups: int, weight: 
     dx = torch.empty((B, T, C), dtype=dt, device=dev)
     dw = torch.empty((C,), dtype=pt, device=dev)
     db = torch.empty((C,), dtype=pt, device=dev)
-    ws, nbytes = _workspace(workspace, group_norm_workspace_size(B, T, C, G), dev)
+    ws, nbytes = _workspace(workspace, group_norm_workspace_size(dt, B, T, C, G, True), dev)
     _run(dev, "ctcpb_group_norm_backward", _TYPES[dt], _TYPES[pt], _p(dyr), db_, dt_, _p(xr), sb, st, _p(w), _p(b), _p(n),
          _p(mean), _p(rstd), act, B, T, C, G, _p(dx), T * C, C, _p(dw), _p(db), _p(ws), nbytes)
     return dx, dw, db

@@ -566,14 +566,17 @@ int ctcpb_cross_entropy_backward(int type, int bias_type, const float* grad, con
  * the mean squared distance from the mean (no difference of large sums); sums
  * and statistics are float32 in a fixed order, y is rounded once.  y may not
  * overlap x.  B * T == 0 is a no-op, but for mean and rstd.
+ *   ws            ctcpb_group_norm_workspace_size() bytes; NULL where that is 0 (a
+ *                 forward call whose utterances' groups fit in shared memory).
  */
 #define CTCPB_ACT_NONE 0
 #define CTCPB_ACT_RELU 1
 #define CTCPB_ACT_SILU 2
+int ctcpb_group_norm_workspace_size(int type, int B, int T, int C, int G, int backward, size_t* bytes);
 int ctcpb_group_norm(int type, int param_type, const void* x, int64_t x_stride_b, int64_t x_stride_t,
                      const void* weight, const void* bias, const int32_t* lengths, float eps, int activation, int B,
                      int T, int C, int G, void* y, int64_t y_stride_b, int64_t y_stride_t, float* mean, float* rstd,
-                     ctcpb_stream_t stream);
+                     void* ws, size_t ws_bytes, ctcpb_stream_t stream);
 
 /*
  * Its backward pass: with xh = (x - mean) * rstd, h = xh * weight + bias,
@@ -584,7 +587,6 @@ int ctcpb_group_norm(int type, int param_type, const void* x, int64_t x_stride_b
  * dx, dweight and dbias may each be NULL (not computed); no frames: sums of 0.
  * Results are reproducible bit for bit.  dx may not overlap x or dy.
  */
-int ctcpb_group_norm_workspace_size(int B, int T, int C, int G, size_t* bytes);
 int ctcpb_group_norm_backward(int type, int param_type, const void* dy, int64_t dy_stride_b, int64_t dy_stride_t,
                               const void* x, int64_t x_stride_b, int64_t x_stride_t, const void* weight,
                               const void* bias, const int32_t* lengths, const float* mean, const float* rstd,

@@ -61,7 +61,8 @@ def check(x, w, b, dy, n, G, act, ws=None, ref_x=None):
 # wider than a block takes at once; lengths of one, of no whole block's rows, of a cluster, of more than it holds
 SHAPES = [(1, 1, 8, 1), (3, 1, 512, 32), (2, 2, 6, 3), (1, 50, 64, 8), (5, 37, 96, 4), (4, 33, 40, 10), (3, 65, 36, 6),
           (2, 129, 771, 3), (7, 20, 33, 33), (2, 300, 512, 32), (3, 500, 1024, 32), (2, 77, 2048, 1), (2, 19, 4098, 1),
-          (2, 9, 8192, 1), (1, 5, 8191, 1), (2, 4000, 64, 2), (1, 20000, 24, 3), (300, 8, 16, 2), (2, 3000, 7, 1)]
+          (2, 9, 8192, 1), (1, 5, 8191, 1), (2, 4000, 64, 2), (1, 20000, 24, 3), (300, 8, 16, 2), (2, 3000, 7, 1),
+          (1, 40000, 64, 1), (3, 5000, 771, 1), (2, 9000, 260, 2)]
 
 
 @pytest.mark.parametrize("B,T,C,G", SHAPES)

@@ -35,16 +35,23 @@ def test_generator_vectors(ctr, key, want):
 
 
 def test_size_queries(lib):
-    assert 0 < head.group_norm_workspace_size(2, 10, 64, 4) < head.group_norm_workspace_size(64, 500, 512, 32)
-    assert head.group_norm_workspace_size(0, 10, 64, 4) > 0
-    assert head.group_norm_workspace_size(1 << 20, 16, 8192, 1) <= 64 << 20
+    BF = torch.bfloat16
+    assert 0 < head.group_norm_workspace_size(BF, 2, 10, 64, 4, True) < head.group_norm_workspace_size(BF, 64, 500, 512, 32, True)
+    assert head.group_norm_workspace_size(BF, 32, 500, 512, 32, False) == 0
+    assert 0 < head.group_norm_workspace_size(BF, 1, 100000, 512, 1, False) < 1 << 20
+    assert head.group_norm_workspace_size(BF, 0, 10, 64, 4, True) == 0
+    # a small share of the tensors, whatever the shape
+    for shape in ((1 << 20, 16, 8192, 1), (1 << 24, 1, 64, 1), (1, 1 << 24, 8, 8), (1 << 12, 1 << 12, 513, 27)):
+        for dtype, e in ((BF, 2), (torch.float32, 4)):
+            assert head.group_norm_workspace_size(dtype, *shape, True) <= (64 << 20) + shape[0] * shape[1] * shape[2] * e // 50
     assert head.policy_loss_workspace_size(320, 40) % 256 == 0 and head.preference_loss_workspace_size(32, 10, 40) > 0
     n = ctypes.c_size_t()
     g, p, q = (lib["ctcpb_%s_workspace_size" % x] for x in ("group_norm", "policy_loss", "preference_loss"))
     for bad in ((-1, 4, 64, 4), (4, -1, 64, 4), (4, 4, 0, 1), (4, 4, 64, 0), (4, 4, 64, 5), (4, 4, 8193, 1),
                 (1 << 13, 1 << 12, 64, 4), (0, (1 << 24) + 1, 64, 4), ((1 << 24) + 1, 0, 64, 4)):
-        assert g(*bad, ctypes.byref(n)) == D.EINVAL, bad
-    assert g(4, 4, 64, 4, None) == D.ENULL
+        assert g(BF16, *bad, 1, ctypes.byref(n)) == D.EINVAL, bad
+    assert g(7, 4, 4, 64, 4, 1, ctypes.byref(n)) == D.EINVAL and g(BF16, 4, 4, 64, 4, 2, ctypes.byref(n)) == D.EINVAL
+    assert g(BF16, 4, 4, 64, 4, 1, None) == D.ENULL
     for bad in ((-1, 4), (4, -1), ((1 << 24) + 1, 4), (4, (1 << 24) + 1)):
         assert p(*bad, ctypes.byref(n)) == D.EINVAL, bad
     for bad in ((-1, 4, 4), (4, 0, 4), (4, 4, -1), (1 << 22, 8, 4), (1, 4, (1 << 24) + 1)):
@@ -56,8 +63,8 @@ def test_group_norm_refusals(lib):
     f, g = lib["ctcpb_group_norm"], lib["ctcpb_group_norm_backward"]
 
     def fwd(type=BF16, ptype=F32, x=P, xb=640, xt=64, w=P, b=P, n=P, eps=1e-5, act=2, B=4, T=10, C=64, G=8, y=P, yb=640,
-            yt=64, mean=P, rstd=P):
-        return f(type, ptype, x, xb, xt, w, b, n, eps, act, B, T, C, G, y, yb, yt, mean, rstd, None)
+            yt=64, mean=P, rstd=P, ws=P, nb=BIG):
+        return f(type, ptype, x, xb, xt, w, b, n, eps, act, B, T, C, G, y, yb, yt, mean, rstd, ws, nb, None)
 
     assert fwd(B=0, x=None, y=None) == D.OK
     assert fwd(T=0, x=None, y=None, mean=None, rstd=None) == D.OK
@@ -67,6 +74,8 @@ def test_group_norm_refusals(lib):
         assert fwd(**kw) == D.EINVAL, kw
     for kw in (dict(x=None), dict(y=None), dict(mean=None), dict(rstd=None)):
         assert fwd(**kw) == D.ENULL, kw
+    far = dict(B=1, T=100000, G=1, xb=0, yb=0)  # in two launches
+    assert fwd(ws=None, **far) == D.ENULL and fwd(ws=P + 16, **far) == D.EALIGN and fwd(nb=16, **far) == D.ESIZE
 
     def bwd(type=BF16, ptype=F32, dy=P, db=640, dt=64, x=P, xb=640, xt=64, w=P, b=P, n=P, mean=P, rstd=P, act=2, B=4, T=10,
             C=64, G=8, dx=P, ob=640, ot=64, dw=P, dbias=P, ws=P, nb=BIG):
