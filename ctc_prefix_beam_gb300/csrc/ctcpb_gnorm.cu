@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kGnThreads, 2) k_gn(const GnArgs a) {
   const u32 keep = (saddr(all + a.gs) + 15u & ~15u) + threadIdx.x * W::bytes;
   const u32 pitch = blockDim.x * W::bytes;
   Place p;
-  p.set<V>(a, blockIdx.x / a.parts, blockIdx.x % a.parts);
+  p.set<V>(a, blockIdx.x / (u32)a.parts, blockIdx.x % (u32)a.parts);
   pdl_wait();
   pdl_next();
   u64 w[P], bias[P];
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kGnThreads, 2) k_gn_bwd(const GnArgs a) {
   const u32 keep = (saddr(red + (a.cols ? 2 * a.cr * a.tw * V : 0)) + 15u & ~15u) + threadIdx.x * W::bytes;
   const u32 pitch = blockDim.x * W::bytes, second = a.slots * pitch;  // dy lies behind x
   Place p;
-  p.set<V>(a, blockIdx.x / a.parts, blockIdx.x % a.parts);
+  p.set<V>(a, blockIdx.x / (u32)a.parts, blockIdx.x % (u32)a.parts);
   pdl_wait();
   pdl_next();
   u64 w[P], bias[P];
@@ -336,6 +336,11 @@ cudaError_t gn_run(int type, bool bwd, GnArgs& a, const GnShape& s, cudaStream_t
   a.parts = s.parts;
   a.cr = s.cr;
   a.by = s.by;
+  a.by_tw = reciprocal(s.tw);
+  a.by_rs = reciprocal(s.rs);
+  a.by_dv = reciprocal(a.D / s.v);
+  const int e = a.ptype == CTCPB_F32 ? 4 : 2;
+  a.pvec = (((uintptr_t)a.weight | (uintptr_t)a.bias) & (s.v * e < 8 ? s.v * e - 1 : 7)) == 0;
   if (s.split) return gn_split(type, bwd, a, s, st);
   if (type == CTCPB_F32) return gn_whole<float>(bwd, a, s, st);
   if (type == CTCPB_BF16) return gn_whole<__nv_bfloat16>(bwd, a, s, st);

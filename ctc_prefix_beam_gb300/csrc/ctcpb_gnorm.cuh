@@ -31,7 +31,12 @@ struct GnArgs {
   int parts;   // blocks that share an utterance's frames (ranks of a cluster, or chunks)
   int cr;      // partial column sums of a block
   int by;
+  int pvec;    // the parameters' vectors of V start at multiples of their size
+  u32 by_tw, by_rs, by_dv;  // divisors' reciprocals (quot)
 };
+// x / d by the reciprocal ceil(2^32 / d) (0: d is 1): exact for x d < 2^32
+__host__ __device__ __forceinline__ u32 reciprocal(u32 d) { return d > 1 ? (u32)(((1ull << 32) + d - 1) / d) : 0u; }
+__device__ __forceinline__ int quot(int x, u32 rec) { return rec ? (int)__umulhi((u32)x, rec) : x; }
 
 // ---------------------------------------------------------------- vectors
 
@@ -231,8 +236,8 @@ struct Place {
   template <int V>
   __device__ __forceinline__ void set(const GnArgs& a, int slab, int part_) {
     part = part_;
-    const int dv = a.D / V;
     if (a.pieces > 1) {
+      const int dv = a.D / V;
       g0 = slab / a.pieces;
       piece = slab - g0 * a.pieces;
       groups = 1;
@@ -243,45 +248,57 @@ struct Place {
       piece = 0;
       groups = a.G - g0 < a.gs ? a.G - g0 : a.gs;
       c0 = g0 * a.D;
-      wv = groups * dv;
+      wv = groups == a.gs ? a.tw : groups * (a.D / V);
     }
-    ty = threadIdx.x / a.tw;
+    ty = quot(threadIdx.x, a.by_tw);
     cv = threadIdx.x - ty * a.tw;
     on = ty < a.rs && cv < wv;
   }
   // group of the thread's vector in the slab
   template <int V>
   __device__ __forceinline__ int group(const GnArgs& a) const {
-    return a.pieces > 1 || !on ? 0 : cv / (a.D / V);
+    return a.pieces > 1 || !on ? 0 : quot(cv, a.by_dv);
   }
 };
 // The frames of a part: the thread's first, and how many it has.
 struct Rows {
-  long long first;
-  int n;
+  int first, n;
   __device__ __forceinline__ Rows(const GnArgs& a, const Place& p, int len) {
-    const u32 from = (u32)((u64)len * (u32)p.part / (u32)a.parts), end = (u32)((u64)len * (u32)(p.part + 1) / (u32)a.parts);
-    const int left = (int)(end - from) - p.ty;
-    first = (long long)from + p.ty;
-    n = p.on && left > 0 ? (left + a.rs - 1) / a.rs : 0;
+    const int each = a.parts > 1 ? (len + a.parts - 1) / a.parts : len, from = p.part * each;
+    const int left = (from + each < len ? each : len - from) - p.ty;
+    first = from + p.ty;
+    n = p.on && left > 0 ? quot(left + a.rs - 1, a.by_rs) : 0;
   }
 };
 
-// A thread's elements of the parameters.
+// A thread's elements of a parameter (`none` without it).
+template <int V>
+__device__ __forceinline__ void param_of(u64 (&w)[(V + 1) / 2], const void* p, int type, bool vec, int c, bool on, float none) {
+  constexpr int P = (V + 1) / 2;
+#pragma unroll
+  for (int i = 0; i < P; ++i) w[i] = pair(none, none);
+  if (!p || !on) return;
+  if (vec && V > 1) {
+    if (type == CTCPB_F32) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) w[i] = reinterpret_cast<const u64*>((const float*)p + c)[i];
+    } else {
+      u32 q[P];
+#pragma unroll
+      for (int i = 0; i < P; ++i) q[i] = reinterpret_cast<const u32*>((const u16*)p + c)[i];
+#pragma unroll
+      for (int i = 0; i < P; ++i) w[i] = type == CTCPB_BF16 ? Elem<__nv_bfloat16>::unpack(q[i]) : Elem<__half>::unpack(q[i]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    w[i] = pair(load_elem(p, type, c + 2 * i), 2 * i + 1 < V ? load_elem(p, type, c + 2 * i + 1) : none);
+}
 template <int V>
 __device__ __forceinline__ void params_of(const GnArgs& a, int c, bool on, u64 (&w)[(V + 1) / 2], u64 (&b)[(V + 1) / 2]) {
-#pragma unroll
-  for (int i = 0; i < (V + 1) / 2; ++i) {
-    float x[2] = {1.f, 1.f}, y[2] = {0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (on && 2 * i + k < V) {
-        if (a.weight) x[k] = load_elem(a.weight, a.ptype, c + 2 * i + k);
-        if (a.bias) y[k] = load_elem(a.bias, a.ptype, c + 2 * i + k);
-      }
-    w[i] = pair(x[0], x[1]);
-    b[i] = pair(y[0], y[1]);
-  }
+  param_of<V>(w, a.weight, a.ptype, a.pvec, c, on, 1.f);
+  param_of<V>(b, a.bias, a.ptype, a.pvec, c, on, 0.f);
 }
 
 // y is 0 in the frames behind the last (the parts take them in turn).
@@ -290,8 +307,11 @@ __device__ __forceinline__ void zero_rows(const GnArgs& a, const Place& p, T* y,
   if (!p.on) return;
   Vec<T, V> z;
   z.zero();
-  const long long step = (long long)a.parts * a.rs;
-  for (long long r = len + (long long)p.part * a.rs + p.ty; r < a.T; r += step) z.store(y + r * a.y_t + p.cv * V);
+  const int step = a.parts * a.rs;
+  int r = len + p.part * a.rs + p.ty;
+  T* to = y + r * a.y_t + p.cv * V;
+  const long long y_step = step * a.y_t;
+  for (; r < a.T; r += step, to += y_step) z.store(to);
 }
 
 // ---------------------------------------------------------------- the activation
@@ -374,7 +394,7 @@ __device__ __forceinline__ void by_group(const GnArgs& a, const Place& p, const 
   for (int g = threadIdx.x >> 5; g < p.groups; g += blockDim.x >> 5) {
     S t{};
     for (int e = lane; e < dv * a.rs; e += 32) {
-      const int ty = e / dv;
+      const int ty = a.pieces > 1 ? e / dv : quot(e, a.by_dv);
       t.join(each[ty * a.tw + g * dv + e - ty * dv]);
     }
     warp_join(t);
