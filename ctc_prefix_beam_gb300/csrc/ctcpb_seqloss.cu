@@ -6,9 +6,11 @@
 //   token loss = -(A + A q) + kl (e^u - 1 - u),  q = e^d - 1, held at the border's
 //   R = sum (ref - nll),  z = beta (R_c - R_r) - margin,  log(1 + e^-z)
 //
-// Bound by HBM where lists are long, by the launches where they are short: each
-// input is read once, the gradient written in the same pass.  What the gradient's
-// factor needs first (the number of tokens, sequences or pairs) is a launch before.
+// Each input is read once, the gradient written in the same pass.  The gradient's
+// factor needs the number of tokens, sequences or pairs first: every block counts
+// the lengths (or pairs) itself, up to kCountHere of them, else a launch before does.
+// Small calls are one launch of one cluster, whose blocks add up their sums through
+// shared memory; larger ones leave them to a launch after, which starts meanwhile.
 //
 // A list's advantages sum to about nothing, so the policy loss is a small rest of
 // large terms: A and A q are added apart, as pairs of float32 (value and error), and
@@ -22,16 +24,19 @@
 namespace ctcpb {
 namespace {
 
-constexpr int kLossThreads = 256;
+constexpr int kLossThreads = 256;  // of a block of the policy loss
+constexpr int kPairThreads = 128;  // ... of the preference loss
 constexpr int kLossBlocks = 152 * 8;
-constexpr long long kMaxSeqs = 1 << 24, kMaxTokens = 1 << 24;
+constexpr int kOneBlocks = 8;      // of a call that is one cluster
+constexpr int kCountHere = 8192;   // lengths or pairs that every block counts itself
+constexpr long long kMaxSeqs = 1 << 24, kMaxTokens = 1 << 24, kMaxCall = 1ll << 32;
 
-// What a launch before the main one finds.
+// What a call's lengths or pairs come to.
 struct Ctl {
   long long items;  // tokens, or pairs
   double factor;    // of the sum of the losses (means: 1 over how many)
   float grad;       // of the gradients: the loss's, times the factor (REDUCE_NONE: 1)
-  u32 ticket;
+  u32 bad;          // an index past the end
 };
 struct LossLayout {
   size_t o_ctl, o_part, total;
@@ -43,6 +48,23 @@ LossLayout loss_layout() {
   l.total = align_up(l.o_part + (size_t)kLossBlocks * 3 * sizeof(float2), 256);
   return l;
 }
+
+// x / d for any x < 2^32 (Granlund and Montgomery: a multiplication by the
+// divisor's reciprocal to 33 bits).
+struct Divisor {
+  u32 d, m, s1, s2;
+  explicit Divisor(u32 d_ = 1) : d(d_) {
+    int l = 0;
+    while ((1ull << l) < d) ++l;
+    m = (u32)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+    s1 = l < 1 ? l : 1;
+    s2 = l > 1 ? l - 1 : 0;
+  }
+  __device__ __forceinline__ u32 operator()(u32 x) const {
+    const u32 t = __umulhi(m, x);
+    return (t + ((x - t) >> s1)) >> s2;
+  }
+};
 
 // A sum as value and error: what each addition rounds off is kept.
 struct Sum2 {
@@ -103,28 +125,43 @@ __device__ __forceinline__ void exp_less(float x, float& e1, float& e2) {
   }
 }
 
-// Sums over a block, in a fixed order; thread 0 has them.
-template <int N>
-__device__ __forceinline__ void block_sums(Sum2 (&v)[N], float2 (*red)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i].warp_sum();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0)
-    for (int i = 0; i < N; ++i) red[warp][i] = make_float2(v[i].hi, v[i].lo);
-  __syncthreads();
-  if (warp == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      v[i] = Sum2();
-      if (lane < (int)(blockDim.x >> 5)) {
-        v[i].hi = red[lane][i].x;
-        v[i].lo = red[lane][i].y;
-      }
-      v[i].warp_sum();
+__device__ __forceinline__ long long length_of(const int* lengths, long long s, long long L) {
+  if (!lengths) return L;
+  const long long n = lengths[s];
+  return n < 0 ? 0 : n > L ? L : n;
+}
+
+// A list's pair: (chosen, rejected), or false where it takes no part.
+__device__ __forceinline__ bool pair_of(const int* chosen, const int* rejected, long long b, int N, int& c, int& r) {
+  c = chosen[b];
+  r = rejected[b];
+  return c >= 0 && r >= 0 && c < N && r < N;
+}
+
+// ---------------------------------------------------------------- counts
+
+// What a call counts: tokens and sequences that have some, or pairs.
+struct Counted {
+  const int *lengths, *chosen, *rejected;
+  long long n, L;  // lengths, or lists
+  int N, reduction;
+  const float* grad;
+};
+// A block's count of all of them; thread 0 has it.
+__device__ __forceinline__ Ctl count(const Counted& a, long long (*red)[2]) {
+  long long v[2] = {0, 0};
+#pragma unroll 8
+  for (long long i = threadIdx.x; i < a.n; i += blockDim.x) {
+    if (a.chosen) {
+      int c, r;
+      v[0] += pair_of(a.chosen, a.rejected, i, a.N, c, r);
+      v[1] += c >= a.N || r >= a.N;
+    } else {
+      const long long l = length_of(a.lengths, i, a.L);
+      v[0] += l;
+      v[1] += l > 0;
     }
   }
-}
-__device__ __forceinline__ void block_counts(long long (&v)[2], long long (*red)[2]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -134,99 +171,141 @@ __device__ __forceinline__ void block_counts(long long (&v)[2], long long (*red)
     red[threadIdx.x >> 5][1] = v[1];
   }
   __syncthreads();
-  v[0] = v[1] = 0;
-  if (threadIdx.x == 0)
+  Ctl c{};
+  if (threadIdx.x == 0) {
+    v[0] = v[1] = 0;
     for (u32 w = 0; w < blockDim.x >> 5; ++w) {
       v[0] += red[w][0];
       v[1] += red[w][1];
     }
+    const bool mean = a.reduction == CTCPB_REDUCE_MEAN || a.reduction == CTCPB_REDUCE_SEQUENCE_MEAN;
+    const double of = (double)(a.reduction == CTCPB_REDUCE_SEQUENCE_MEAN ? v[1] : v[0]);
+    c.items = v[0];
+    c.factor = mean ? 1. / of : 1.;
+    c.grad = a.reduction == CTCPB_REDUCE_NONE || !a.grad ? 1.f : mean ? (float)((double)*a.grad / of) : *a.grad;
+    c.bad = a.chosen && v[1] ? 1u : 0u;
+  }
+  return c;
 }
-__device__ __forceinline__ void set_ctl(Ctl* ctl, long long items, long long of, int reduction, const float* grad) {
-  const bool mean = reduction == CTCPB_REDUCE_MEAN || reduction == CTCPB_REDUCE_SEQUENCE_MEAN;
-  ctl->items = items;
-  ctl->factor = mean ? 1. / (double)of : 1.;
-  ctl->grad = reduction == CTCPB_REDUCE_NONE || !grad ? 1.f : mean ? (float)((double)*grad / (double)of) : *grad;
-  ctl->ticket = 0;
-}
-
-__device__ __forceinline__ long long length_of(const int* lengths, long long s, long long L) {
-  if (!lengths) return L;
-  const long long n = lengths[s];
-  return n < 0 ? 0 : n > L ? L : n;
-}
-
-// ---------------------------------------------------------------- counts
-
-// Tokens and sequences that have some.
-__global__ void __launch_bounds__(1024) k_count_tokens(const int* lengths, long long S, long long L, int reduction,
-                                                       const float* grad, Ctl* ctl, u32* status) {
+__global__ void __launch_bounds__(1024) k_count(const Counted a, Ctl* ctl) {
   __shared__ long long red[32][2];
   pdl_wait();
   pdl_next();
-  long long v[2] = {0, 0};
-  for (long long s = threadIdx.x; s < S; s += blockDim.x) {
-    const long long l = length_of(lengths, s, L);
-    v[0] += l;
-    v[1] += l > 0;
-  }
-  block_counts(v, red);
-  if (threadIdx.x == 0) {
-    set_ctl(ctl, v[0], reduction == CTCPB_REDUCE_SEQUENCE_MEAN ? v[1] : v[0], reduction, grad);
-    *status = 0;
-  }
-}
-
-// A list's pair: (chosen, rejected), or false where it takes no part.
-__device__ __forceinline__ bool pair_of(const int* chosen, const int* rejected, long long b, int N, int& c, int& r) {
-  c = chosen[b];
-  r = rejected[b];
-  return c >= 0 && r >= 0 && c < N && r < N;
-}
-__global__ void __launch_bounds__(1024) k_count_pairs(const int* chosen, const int* rejected, long long B, int N,
-                                                      int reduction, const float* grad, Ctl* ctl, u32* status) {
-  __shared__ long long red[32][2];
-  pdl_wait();
-  pdl_next();
-  long long v[2] = {0, 0};  // pairs, and lists with an index past the end
-  for (long long b = threadIdx.x; b < B; b += blockDim.x) {
-    int c, r;
-    v[0] += pair_of(chosen, rejected, b, N, c, r);
-    v[1] += c >= N || r >= N;
-  }
-  block_counts(v, red);
-  if (threadIdx.x == 0) {
-    set_ctl(ctl, v[0], v[0], reduction, grad);
-    *status = v[1] ? CTCPB_DEV_TARGET : 0u;
-  }
+  const Ctl c = count(a, red);
+  if (threadIdx.x == 0) *ctl = c;
 }
 
 // ---------------------------------------------------------------- the end of a call
 
-// A block's sums go to its place; the block that comes last adds all of them in
-// order.  Returns whether this is that block (its thread 0 has the totals).
-template <int N>
-__device__ __forceinline__ bool last_block(Sum2 (&v)[N], float2* part, u32* ticket, float2 (*red)[N]) {
-  __shared__ u32 last;
-  block_sums<N>(v, red);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < N; ++i) part[(size_t)blockIdx.x * N + i] = make_float2(v[i].hi, v[i].lo);
-    __threadfence();
-    last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+// How a launch's blocks come by the counts and leave their sums.
+struct Ends {
+  Counted counted;
+  int here;       // every block counts (else ctl was written by a launch before)
+  int one;        // the launch is one cluster (else sums go to part, for k_loss_end)
+  Ctl* ctl;
+  float2* part;   // [blocks][3]
+  u32* status;    // (may be null in a call of one cluster)
+  float *loss, *stats;
+};
+struct Shared {
+  long long count[32][2];
+  float2 warp[32][3];
+  float2 block[3];
+  Ctl ctl;
+};
+__device__ __forceinline__ void begin(const Ends& a, Shared& sh) {
+  if (a.here) {
+    const Ctl c = count(a.counted, sh.count);
+    if (threadIdx.x == 0) {
+      sh.ctl = c;
+      if (blockIdx.x == 0 && !a.one) *a.ctl = c;  // for the launch after
+    }
+  } else if (threadIdx.x == 0) {
+    sh.ctl = *a.ctl;
   }
+  if (threadIdx.x == 0 && blockIdx.x == 0 && a.status) *a.status = sh.ctl.bad ? CTCPB_DEV_TARGET : 0u;
   __syncthreads();
-  if (!last) return false;
-  __threadfence();
-  for (int i = 0; i < N; ++i) v[i] = Sum2();
-  for (u32 b = threadIdx.x; b < gridDim.x; b += blockDim.x)
+}
+// A block's sums, in a fixed order (in sh.block once a barrier has passed).
+template <int N>
+__device__ __forceinline__ void block_sums(Sum2 (&v)[N], Shared& sh) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i].warp_sum();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) sh.warp[warp][i] = make_float2(v[i].hi, v[i].lo);
+  __syncthreads();
+  if (warp == 0) {
+#pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float2 p = __ldcg(part + (size_t)b * N + i);
+      Sum2 s;
+      if (lane < (int)(blockDim.x >> 5)) {
+        s.hi = sh.warp[lane][i].x;
+        s.lo = sh.warp[lane][i].y;
+      }
+      s.warp_sum();
+      if (lane == 0) sh.block[i] = make_float2(s.hi, s.lo);
+    }
+  }
+}
+// The results.  Over no tokens or pairs a mean's factor is infinite: not a number.
+__device__ __forceinline__ void results(const Ends& a, const Ctl& ctl, const Sum2 (&s)[3]) {
+  if (a.loss) *a.loss = (float)(s[0].value() * ctl.factor);
+  if (a.stats) {
+    a.stats[0] = (float)(s[1].value() / (double)ctl.items);
+    a.stats[1] = (float)(s[2].value() / (double)ctl.items);
+  }
+}
+template <int N>
+__device__ __forceinline__ void end(const Ends& a, Sum2 (&v)[N], Shared& sh) {
+  block_sums<N>(v, sh);
+  if (!a.one) {
+    if (threadIdx.x == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) a.part[(size_t)blockIdx.x * 3 + i] = sh.block[i];
+    return;
+  }
+  cluster_sync();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    Sum2 s[3];
+    for (u32 r = 0; r < gridDim.x; ++r)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        Sum2 q;
+        const u32 at = cluster_addr(saddr(&sh.block[i]), r);
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];\n" : "=f"(q.hi), "=f"(q.lo) : "r"(at) : "memory");
+        s[i].add(q);
+      }
+    results(a, sh.ctl, s);
+  }
+  cluster_sync();  // no block leaves before its sums are read
+}
+// The blocks' sums, in order.
+template <int N>
+__global__ void __launch_bounds__(256) k_loss_end(const Ends a, int blocks) {
+  __shared__ Shared sh;
+  pdl_wait();
+  pdl_next();
+  Sum2 v[3];
+  for (int b = threadIdx.x; b < blocks; b += blockDim.x)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 p = a.part[(size_t)b * 3 + i];
       Sum2 q;
       q.hi = p.x;
       q.lo = p.y;
       v[i].add(q);
     }
-  block_sums<N>(v, red);
-  return true;
+  block_sums<3>(v, sh);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i].hi = sh.block[i].x;
+    v[i].lo = sh.block[i].y;
+  }
+  results(a, *a.ctl, v);
 }
 
 // ---------------------------------------------------------------- the policy loss
@@ -241,11 +320,10 @@ struct PolicyArgs {
   float kl;
   int reduction;
   const float* grad;
-  float *loss, *stats, *dnll;
-  Ctl* ctl;
-  float2* part;
-  int tx;            // threads of a row (a power of two)
-  long long chunks;  // pieces of a row
+  float *loss, *dnll;  // the loss of each token (REDUCE_NONE)
+  Divisor pieces;      // vectors of a row
+  u32 work;            // vectors of all rows
+  Ends ends;
 };
 
 // One token.  `hold`: the ratio is past the border and counts no more.
@@ -279,81 +357,98 @@ __device__ __forceinline__ void token(const PolicyArgs& a, float nll, float old,
   each = more - A;
 }
 
+// A thread's tokens: four of a row, or one.
+template <int V>
+struct Tokens {
+  float nll[V], old[V], ref[V], adv[V], up[V];
+  static __device__ __forceinline__ void get(float (&v)[V], const float* p) {
+    if constexpr (V == 4) {
+      const float4 f = __ldcs(reinterpret_cast<const float4*>(p));
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else {
+      v[0] = __ldcs(p);
+    }
+  }
+  // (a vector may reach behind the length, not behind the row)
+  __device__ __forceinline__ void load(const PolicyArgs& a, bool none, u32 s, long long t) {
+    get(nll, a.nll + s * a.ld_nll + t);
+    get(old, a.old + s * a.ld_old + t);
+    if (a.ref) get(ref, a.ref + s * a.ld_ref + t);
+    if (a.ld_adv)
+      get(adv, a.adv + s * a.ld_adv + t);
+    else
+      adv[0] = a.adv[s];
+    if (none && a.grad) get(up, a.grad + s * a.L + t);
+  }
+};
+// Where a thread's tokens are: the row, the first, how many of its length.
+struct At {
+  u32 s, t, len;
+  __device__ __forceinline__ void set(const PolicyArgs& a, u64 x, int V) {
+    len = t = s = 0;
+    if (x < a.work) {
+      s = a.pieces((u32)x);
+      t = ((u32)x - s * a.pieces.d) * V;
+      len = (u32)length_of(a.lengths, s, a.L);
+    }
+  }
+  __device__ __forceinline__ int live(int V) const { return len <= t ? 0 : len - t >= (u32)V ? V : (int)(len - t); }
+};
+
 template <bool VEC>
 __global__ void __launch_bounds__(kLossThreads) k_policy(const PolicyArgs a) {
-  __shared__ float2 red[32][3];
+  __shared__ Shared sh;
   constexpr int V = VEC ? 4 : 1;
   pdl_wait();
   pdl_next();
-  const int tx = threadIdx.x & (a.tx - 1), ty = threadIdx.x / a.tx, rows = kLossThreads / a.tx;
   const bool none = a.reduction == CTCPB_REDUCE_NONE, by_len = a.reduction == CTCPB_REDUCE_SEQUENCE_MEAN;
-  const float g = a.ctl->grad;
+  // the next tokens are on their way while these are worked on, the lengths after them too
+  const u64 step = (u64)gridDim.x * kLossThreads;
+  u64 x = (u64)blockIdx.x * kLossThreads + threadIdx.x;
+  At at, next;
+  Tokens<V> ahead;
+  at.set(a, x, V);
+  if (at.live(V)) ahead.load(a, none, at.s, at.t);
+  next.set(a, x + step, V);
+  begin(a.ends, sh);
+  const float g = sh.ctl.grad;
   Sum2 sums[3];
-  const long long groups = (a.S + rows - 1) / rows, work = groups * a.chunks;
-  for (long long w = blockIdx.x; w < work; w += gridDim.x) {
-    const long long group = a.chunks == 1 ? w : w / a.chunks, s = group * rows + ty;
-    const long long t = ((w - group * a.chunks) * a.tx + tx) * V;
-    if (s >= a.S || t >= a.L) continue;
-    const long long len = length_of(a.lengths, s, a.L);
+  for (; x < a.work; x += step) {
+    const Tokens<V> k = ahead;
+    const At now = at;
+    at = next;
+    if (at.live(V)) ahead.load(a, none, at.s, at.t);
+    next.set(a, x + 2 * step, V);
+    const int live = now.live(V);
     // 1 / len, and what its rounding took off (len <= 2^24 is exact)
-    const float wt = by_len && len > 0 ? 1.f / (float)len : 1.f;
-    const float wt_lo = by_len && len > 0 ? fmaf(-wt, (float)len, 1.f) * wt : 0.f;
+    const float len = (float)now.len, wt = by_len && live ? 1.f / len : 1.f;
     const float gw = g * wt;
-    float nll[V], old[V], ref[V], adv[V], up[V], slope[V], each[V];
-    const long long at = s * a.L + t;
-    const int live = len - t >= V ? V : len > t ? (int)(len - t) : 0;
-    if (live) {
-      // (a vector may reach behind the length, not behind the row)
-      if constexpr (VEC) {
-        auto get = [](float (&v)[4], const float* p) {
-          const float4 f = __ldcs(reinterpret_cast<const float4*>(p));
-          v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-        };
-        get(nll, a.nll + s * a.ld_nll + t);
-        get(old, a.old + s * a.ld_old + t);
-        if (a.ref) get(ref, a.ref + s * a.ld_ref + t);
-        if (a.ld_adv) get(adv, a.adv + s * a.ld_adv + t);
-        if (none && a.grad) get(up, a.grad + at);
-      } else {
-        nll[0] = a.nll[s * a.ld_nll + t];
-        old[0] = a.old[s * a.ld_old + t];
-        if (a.ref) ref[0] = a.ref[s * a.ld_ref + t];
-        if (a.ld_adv) adv[0] = a.adv[s * a.ld_adv + t];
-        if (none && a.grad) up[0] = a.grad[at];
-      }
-    }
-    const float row_adv = a.ld_adv == 0 && live ? a.adv[s] : 0.f;
+    float slope[V], each[V];
     Sum2 loss;
     float kl = 0.f, held = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       slope[i] = each[i] = 0.f;
       if (i < live) {
-        token(a, nll[i], old[i], a.ref ? ref[i] : 0.f, a.ld_adv ? adv[i] : row_adv, loss, kl, held, slope[i], each[i]);
-        slope[i] *= none ? (a.grad ? up[i] : 1.f) : gw;
+        token(a, k.nll[i], k.old[i], a.ref ? k.ref[i] : 0.f, k.adv[a.ld_adv ? i : 0], loss, kl, held, slope[i], each[i]);
+        slope[i] *= none ? (a.grad ? k.up[i] : 1.f) : gw;
       }
     }
     if (live) {
-      sums[0].add(by_len ? loss.times(wt, wt_lo) : loss);
+      sums[0].add(by_len ? loss.times(wt, fmaf(-wt, len, 1.f) * wt) : loss);
       sums[1].add(kl);
       sums[2].add(held);
     }
+    const long long o = now.s * a.L + now.t;
     if constexpr (VEC) {
-      if (a.dnll) __stcs(reinterpret_cast<float4*>(a.dnll + at), make_float4(slope[0], slope[1], slope[2], slope[3]));
-      if (none && a.loss) __stcs(reinterpret_cast<float4*>(a.loss + at), make_float4(each[0], each[1], each[2], each[3]));
+      if (a.dnll) __stcs(reinterpret_cast<float4*>(a.dnll + o), make_float4(slope[0], slope[1], slope[2], slope[3]));
+      if (a.loss) __stcs(reinterpret_cast<float4*>(a.loss + o), make_float4(each[0], each[1], each[2], each[3]));
     } else {
-      if (a.dnll) a.dnll[at] = slope[0];
-      if (none && a.loss) a.loss[at] = each[0];
+      if (a.dnll) a.dnll[o] = slope[0];
+      if (a.loss) a.loss[o] = each[0];
     }
   }
-  if (!last_block<3>(sums, a.part, &a.ctl->ticket, red) || threadIdx.x != 0) return;
-  // over no tokens the factor is infinite and the means are not numbers
-  const double tokens = (double)a.ctl->items;
-  if (!none && a.loss) *a.loss = (float)(sums[0].value() * a.ctl->factor);
-  if (a.stats) {
-    a.stats[0] = (float)(sums[1].value() / tokens);
-    a.stats[1] = (float)(sums[2].value() / tokens);
-  }
+  end<3>(a.ends, sums, sh);
 }
 
 // ---------------------------------------------------------------- the preference loss
@@ -367,50 +462,75 @@ struct PairArgs {
   float beta, margin, smooth;
   int average, reduction;
   const float* grad;
-  float *loss, *margins, *dnll;
-  Ctl* ctl;
-  float2* part;
+  float *loss, *margins, *dnll;  // the loss of each list (REDUCE_NONE)
+  Ends ends;
 };
 
-// A list is worked on by GT threads (a warp, or the block): both rows' sums, the
-// pair's loss, then the gradients of all its hypotheses.
+// A row's values from `from` on: v in the first `len`, 0 behind.
 template <bool VEC, int GT>
-__global__ void __launch_bounds__(kLossThreads) k_preference(const PairArgs a) {
-  __shared__ float2 red[32][1];
+__device__ __forceinline__ void write_row(float* row, long long L, long long len, float v, int t0) {
+  constexpr int V = VEC ? 4 : 1;
+  for (long long t = (long long)t0 * V; t < L; t += GT * V) {
+    if constexpr (VEC)
+      __stcs(reinterpret_cast<float4*>(row + t),
+             make_float4(t < len ? v : 0.f, t + 1 < len ? v : 0.f, t + 2 < len ? v : 0.f, t + 3 < len ? v : 0.f));
+    else
+      row[t] = t < len ? v : 0.f;
+  }
+}
+
+// A list is worked on by GT threads (a warp, or the block): both rows' sums, the
+// pair's loss, then the two rows' gradients; the other rows' zeros while the sums'
+// values are on their way.
+template <bool VEC, int GT>
+__global__ void __launch_bounds__(kPairThreads) k_preference(const PairArgs a) {
+  __shared__ Shared sh;
   __shared__ float2 rowsum[2][GT / 32];
-  __shared__ float slopes[kLossThreads / GT];
-  constexpr int V = VEC ? 4 : 1, per = kLossThreads / GT;
+  __shared__ float slopes[kPairThreads / GT];
+  constexpr int V = VEC ? 4 : 1, per = kPairThreads / GT, U = 4;
   pdl_wait();
   pdl_next();
+  begin(a.ends, sh);
   const int t0 = threadIdx.x % GT, g = threadIdx.x / GT;
   const bool none = a.reduction == CTCPB_REDUCE_NONE;
-  const float scale = a.ctl->grad * a.beta;
+  const float scale = sh.ctl.grad * a.beta;
   Sum2 sums[1];
   const long long groups = (a.B + per - 1) / per;
   for (long long w = blockIdx.x; w < groups; w += gridDim.x) {
     const long long b = w * per + g;
     if (b >= a.B) continue;  // (a whole warp; never a part of the block where it meets)
     int c, r;
-    const bool pair = pair_of(a.chosen, a.rejected, b, a.N, c, r);
+    const bool pair = pair_of(a.chosen, a.rejected, b, a.N, c, r), both = pair && c != r;
     const long long lc = pair ? length_of(a.lengths, b * a.N + c, a.L) : 0;
     const long long lr = pair ? length_of(a.lengths, b * a.N + r, a.L) : 0;
+    float* const out = a.dnll ? a.dnll + b * a.N * a.L : nullptr;
+    if (out) {
+#pragma unroll 1
+      for (int n = 0; n < a.N; ++n)
+        if (!both || (n != c && n != r)) write_row<VEC, GT>(out + n * a.L, a.L, 0, 0.f, t0);
+    }
     Sum2 R[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const long long row = b * a.N + (k ? r : c), len = k ? lr : lc;
+      const long long row = b * a.N + (k ? r : c), len = both ? (k ? lr : lc) : 0;
       const float *const pn = a.nll + row * a.ld_nll, *const pf = a.ref + row * a.ld_ref;
-      for (long long t = (long long)t0 * V; t < len; t += GT * V) {
-        if constexpr (VEC) {
-          const float4 n = *reinterpret_cast<const float4*>(pn + t);
-          float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (a.ref) f = *reinterpret_cast<const float4*>(pf + t);
-          add_difference(R[k], f.x, n.x);
-          if (t + 1 < len) add_difference(R[k], f.y, n.y);
-          if (t + 2 < len) add_difference(R[k], f.z, n.z);
-          if (t + 3 < len) add_difference(R[k], f.w, n.w);
-        } else {
-          add_difference(R[k], a.ref ? pf[t] : 0.f, pn[t]);
+      for (long long t = (long long)t0 * V; t < len; t += U * GT * V) {
+        float n[U][V], f[U][V];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const long long at = t + i * GT * V;
+#pragma unroll
+          for (int j = 0; j < V; ++j) f[i][j] = 0.f;
+          if (at < len) {
+            Tokens<V>::get(n[i], pn + at);
+            if (a.ref) Tokens<V>::get(f[i], pf + at);
+          }
         }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (t + i * GT * V + j < len) add_difference(R[k], f[i][j], n[i][j]);
       }
       R[k].warp_sum();
     }
@@ -423,7 +543,7 @@ __global__ void __launch_bounds__(kLossThreads) k_preference(const PairArgs a) {
     }
     if (t0 == 0) {
       double z = 0.;
-      if (c != r) {
+      if (both) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           if constexpr (GT > 32) {
@@ -447,7 +567,7 @@ __global__ void __launch_bounds__(kLossThreads) k_preference(const PairArgs a) {
       const float e = expf(-fabsf(m)), tail = log1pf(e);
       const float up = (m >= 0.f ? 1.f : e) / (1.f + e), dn = (m >= 0.f ? e : 1.f) / (1.f + e);  // of m and -m
       const float loss = pair ? (1.f - a.smooth) * (fmaxf(-m, 0.f) + tail) + a.smooth * (fmaxf(m, 0.f) + tail) : 0.f;
-      if (none && a.loss) a.loss[b] = loss;
+      if (a.loss) a.loss[b] = loss;
       if (a.margins) a.margins[b] = m;
       sums[0].add(loss);
       slopes[g] = a.smooth * up - (1.f - a.smooth) * dn;
@@ -456,37 +576,53 @@ __global__ void __launch_bounds__(kLossThreads) k_preference(const PairArgs a) {
       __syncthreads();
     else
       __syncwarp();
-    if (a.dnll) {
-      const float dz = pair && c != r ? slopes[g] * (none ? a.beta * a.grad[b] : scale) : 0.f;
-      const float gc = -dz / (a.average && lc > 0 ? (float)lc : 1.f), gr = dz / (a.average && lr > 0 ? (float)lr : 1.f);
-      float* const out = a.dnll + b * a.N * a.L;
-      for (int n = 0; n < a.N; ++n) {
-        const bool is = pair && c != r && (n == c || n == r);
-        const float v = n == c ? gc : gr;
-        const long long len = is ? (n == c ? lc : lr) : 0;
-        for (long long t = (long long)t0 * V; t < a.L; t += GT * V) {
-          float* const p = out + n * a.L + t;
-          if constexpr (VEC)
-            *reinterpret_cast<float4*>(p) =
-                make_float4(t < len ? v : 0.f, t + 1 < len ? v : 0.f, t + 2 < len ? v : 0.f, t + 3 < len ? v : 0.f);
-          else
-            *p = t < len ? v : 0.f;
-        }
-      }
+    if (out && both) {
+      const float dz = slopes[g] * (none ? a.beta * a.grad[b] : scale);
+      write_row<VEC, GT>(out + c * a.L, a.L, lc, -dz / (a.average && lc > 0 ? (float)lc : 1.f), t0);
+      write_row<VEC, GT>(out + r * a.L, a.L, lr, dz / (a.average && lr > 0 ? (float)lr : 1.f), t0);
     }
     // (the next list's first meeting comes after its sums, so slopes may be written again then)
     if constexpr (GT == 32) __syncwarp();
   }
-  if (!last_block<1>(sums, a.part, &a.ctl->ticket, red) || threadIdx.x != 0) return;
-  if (!none && a.loss) *a.loss = (float)(sums[0].value() * a.ctl->factor);
+  end<1>(a.ends, sums, sh);
 }
 
 bool on16(const void* p, long long ld) { return ((uintptr_t)p & 15u) == 0 && ld % 4 == 0; }
 
-int check_loss_ws(const void* ws, size_t ws_bytes) {
-  if (!ws) return CTCPB_ENULL;
+// Small calls are one cluster: so few tokens that its blocks are not much longer at
+// them than a second launch is.
+bool one_cluster(long long counted, long long tokens) { return counted <= kCountHere && tokens <= 65536; }
+
+// The launches of a call around its main one, `run(blocks, cluster)`.
+template <int N, class F>
+int loss_call(Ends& e, bool one, int blocks, void* ws, cudaStream_t s, F run) {
+  const LossLayout l = loss_layout();
+  e.here = e.counted.n <= kCountHere;
+  e.one = one;
+  e.ctl = (Ctl*)((char*)ws + l.o_ctl);
+  e.part = (float2*)((char*)ws + l.o_part);
+  e.status = ws ? &((Header*)ws)->status : nullptr;
+  if (one) {
+    if (blocks > kOneBlocks) blocks = kOneBlocks;
+    while (blocks & (blocks - 1)) ++blocks;  // clusters of a power of two
+    return run(blocks, blocks) == cudaSuccess ? CTCPB_OK : CTCPB_ECUDA;
+  }
+  if (!e.here && launch(k_count, 1, 1024, 0, s, 1, e.counted, e.ctl) != cudaSuccess) return CTCPB_ECUDA;
+  if (run(blocks, 1) != cudaSuccess) return CTCPB_ECUDA;
+  if ((e.loss || e.stats) && launch(k_loss_end<N>, 1, 256, 0, s, 1, e, blocks) != cudaSuccess) return CTCPB_ECUDA;
+  return CTCPB_OK;
+}
+
+int check_loss_ws(const void* ws, size_t ws_bytes, bool one) {
+  if (!ws) return one ? CTCPB_OK : CTCPB_ENULL;
   if (((uintptr_t)ws & 255u) != 0) return CTCPB_EALIGN;
-  return ws_bytes < loss_layout().total ? CTCPB_ESIZE : CTCPB_OK;
+  return ws_bytes < (one ? sizeof(Header) : loss_layout().total) ? CTCPB_ESIZE : CTCPB_OK;
+}
+int check_policy(long long S, long long L) {
+  return S < 0 || S > kMaxSeqs || L < 0 || L > kMaxTokens || (L > 0 && S > kMaxCall / L) ? CTCPB_EINVAL : CTCPB_OK;
+}
+int check_lists(long long B, int N, long long L) {
+  return B < 0 || N < 1 || N > kMaxSeqs || B > kMaxSeqs / N || L < 0 || L > kMaxTokens ? CTCPB_EINVAL : CTCPB_OK;
 }
 
 }  // namespace
@@ -497,9 +633,9 @@ using namespace ctcpb;
 extern "C" {
 
 int ctcpb_policy_loss_workspace_size(int64_t S, int64_t L, size_t* bytes) {
-  if (S < 0 || S > kMaxSeqs || L < 0 || L > kMaxTokens) return CTCPB_EINVAL;
+  if (int rc = check_policy(S, L)) return rc;
   if (!bytes) return CTCPB_ENULL;
-  *bytes = loss_layout().total;
+  *bytes = one_cluster(S, S * L) ? sizeof(Header) : loss_layout().total;
   return CTCPB_OK;
 }
 
@@ -508,17 +644,16 @@ int ctcpb_policy_loss(const float* nll, int64_t ld_nll, const float* old_nll, in
                       int64_t S, int64_t L, double clip_low, double clip_high, float kl_weight, int reduction,
                       const float* grad, float* loss, float* stats, float* dnll, void* ws, size_t ws_bytes,
                       ctcpb_stream_t stream) {
-  if (S < 0 || S > kMaxSeqs || L < 0 || L > kMaxTokens) return CTCPB_EINVAL;
+  if (int rc = check_policy(S, L)) return rc;
   if (reduction < CTCPB_REDUCE_NONE || reduction > CTCPB_REDUCE_SEQUENCE_MEAN) return CTCPB_EINVAL;
   if (!(clip_low >= 0.) || std::isinf(clip_low) || !(clip_high >= 0.) || !std::isfinite(kl_weight)) return CTCPB_EINVAL;
-  const bool any = S > 0 && L > 0;
+  const bool any = S > 0 && L > 0, one = one_cluster(S, S * L);
   if (any && (ld_nll < L || ld_old < L || (ref_nll && ld_ref < L) || (ld_advantages != 0 && ld_advantages < L)))
     return CTCPB_EINVAL;
   if (any && (!nll || !old_nll || !advantages)) return CTCPB_ENULL;
   if (any && dnll && !grad) return CTCPB_ENULL;
-  if (int rc = check_loss_ws(ws, ws_bytes)) return rc;
+  if (int rc = check_loss_ws(ws, ws_bytes, one)) return rc;
   cudaStream_t s = (cudaStream_t)stream;
-  const LossLayout l = loss_layout();
   PolicyArgs a{};
   a.nll = nll;
   a.old = old_nll;
@@ -540,34 +675,30 @@ int ctcpb_policy_loss(const float* nll, int64_t ld_nll, const float* old_nll, in
   a.kl = kl_weight;
   a.reduction = reduction;
   a.grad = grad;
-  a.loss = loss;
-  a.stats = stats;
-  a.dnll = dnll;
-  a.ctl = (Ctl*)((char*)ws + l.o_ctl);
-  a.part = (float2*)((char*)ws + l.o_part);
   const bool none = reduction == CTCPB_REDUCE_NONE;
+  a.loss = none ? loss : nullptr;
+  a.dnll = dnll;
   const bool vec = L % 4 == 0 && on16(nll, ld_nll) && on16(old_nll, ld_old) && on16(ref_nll, ref_nll ? ld_ref : 0) &&
                    (ld_advantages == 0 || on16(advantages, ld_advantages)) && on16(dnll, 0) &&
                    (!none || (on16(loss, 0) && on16(grad, 0)));
   const long long pieces = vec ? L / 4 : L;
-  a.tx = 1;
-  while (a.tx < kLossThreads && a.tx < pieces) a.tx *= 2;
-  a.chunks = pieces > 0 ? (pieces + a.tx - 1) / a.tx : 1;
-  const long long rows = kLossThreads / a.tx, work = any ? (S + rows - 1) / rows * a.chunks : 0;
-  const int grid = work < 1 ? 1 : work < kLossBlocks ? (int)work : kLossBlocks;
-  if (launch(k_count_tokens, 1, 1024, 0, s, 1, lengths, a.S, a.L, reduction, grad, a.ctl, &((Header*)ws)->status) !=
-      cudaSuccess)
-    return CTCPB_ECUDA;
-  if ((vec ? launch(k_policy<true>, grid, kLossThreads, 0, s, 1, a) : launch(k_policy<false>, grid, kLossThreads, 0, s, 1, a)) !=
-      cudaSuccess)
-    return CTCPB_ECUDA;
-  return CTCPB_OK;
+  a.pieces = Divisor(any ? (u32)pieces : 1u);
+  a.work = any ? (u32)(S * pieces) : 0u;
+  a.ends.counted = Counted{lengths, nullptr, nullptr, a.S, L, 0, reduction, grad};
+  a.ends.loss = none ? nullptr : loss;
+  a.ends.stats = stats;
+  const long long blocks = ((long long)a.work + kLossThreads - 1) / kLossThreads;
+  const int most = 152 * (vec ? 3 : 4);
+  return loss_call<3>(a.ends, one, blocks < 1 ? 1 : blocks < most ? (int)blocks : most, ws, s, [&](int n, int cluster) {
+    return vec ? launch(k_policy<true>, n, kLossThreads, 0, s, cluster, a)
+               : launch(k_policy<false>, n, kLossThreads, 0, s, cluster, a);
+  });
 }
 
 int ctcpb_preference_loss_workspace_size(int64_t B, int N, int64_t L, size_t* bytes) {
-  if (B < 0 || N < 1 || N > kMaxSeqs || B > kMaxSeqs / N || L < 0 || L > kMaxTokens) return CTCPB_EINVAL;
+  if (int rc = check_lists(B, N, L)) return rc;
   if (!bytes) return CTCPB_ENULL;
-  *bytes = loss_layout().total;
+  *bytes = one_cluster(B, B * N * L) ? sizeof(Header) : loss_layout().total;
   return CTCPB_OK;
 }
 
@@ -576,16 +707,16 @@ int ctcpb_preference_loss(const float* nll, int64_t ld_nll, const float* ref_nll
                           int64_t L, float beta, float margin, float label_smoothing, int average, int reduction,
                           const float* grad, float* loss, float* margins, float* dnll, void* ws, size_t ws_bytes,
                           ctcpb_stream_t stream) {
-  if (B < 0 || N < 1 || N > kMaxSeqs || B > kMaxSeqs / N || L < 0 || L > kMaxTokens) return CTCPB_EINVAL;
+  if (int rc = check_lists(B, N, L)) return rc;
   if (reduction < CTCPB_REDUCE_NONE || reduction > CTCPB_REDUCE_SUM || (average != 0 && average != 1)) return CTCPB_EINVAL;
   if (!std::isfinite(beta) || !std::isfinite(margin) || !(label_smoothing >= 0.f && label_smoothing <= 1.f))
     return CTCPB_EINVAL;
+  const bool one = one_cluster(B, B * N * L);
   if (B > 0 && L > 0 && (ld_nll < L || (ref_nll && ld_ref < L))) return CTCPB_EINVAL;
   if (B > 0 && (!chosen || !rejected || (L > 0 && !nll))) return CTCPB_ENULL;
   if (B > 0 && L > 0 && dnll && !grad) return CTCPB_ENULL;
-  if (int rc = check_loss_ws(ws, ws_bytes)) return rc;
+  if (int rc = check_loss_ws(ws, ws_bytes, one)) return rc;
   cudaStream_t s = (cudaStream_t)stream;
-  const LossLayout l = loss_layout();
   PairArgs a{};
   a.nll = nll;
   a.ref = ref_nll;
@@ -603,23 +734,23 @@ int ctcpb_preference_loss(const float* nll, int64_t ld_nll, const float* ref_nll
   a.average = average;
   a.reduction = reduction;
   a.grad = grad;
-  a.loss = loss;
+  const bool none = reduction == CTCPB_REDUCE_NONE;
+  a.loss = none ? loss : nullptr;
   a.margins = margins;
   a.dnll = L > 0 ? dnll : nullptr;
-  a.ctl = (Ctl*)((char*)ws + l.o_ctl);
-  a.part = (float2*)((char*)ws + l.o_part);
+  a.ends.counted = Counted{nullptr, chosen, rejected, B, 0, N, reduction, grad};
+  a.ends.loss = none ? nullptr : loss;
   const bool vec = L % 4 == 0 && on16(nll, ld_nll) && on16(ref_nll, ref_nll ? ld_ref : 0) && on16(dnll, 0);
   const bool wide = L > 256;
-  const long long per = wide ? 1 : kLossThreads / 32, work = (B + per - 1) / per;
-  const int grid = work < 1 ? 1 : work < kLossBlocks ? (int)work : kLossBlocks;
-  if (launch(k_count_pairs, 1, 1024, 0, s, 1, chosen, rejected, a.B, N, reduction, grad, a.ctl, &((Header*)ws)->status) !=
-      cudaSuccess)
-    return CTCPB_ECUDA;
-  const cudaError_t e = vec ? (wide ? launch(k_preference<true, kLossThreads>, grid, kLossThreads, 0, s, 1, a)
-                                    : launch(k_preference<true, 32>, grid, kLossThreads, 0, s, 1, a))
-                            : (wide ? launch(k_preference<false, kLossThreads>, grid, kLossThreads, 0, s, 1, a)
-                                    : launch(k_preference<false, 32>, grid, kLossThreads, 0, s, 1, a));
-  return e == cudaSuccess ? CTCPB_OK : CTCPB_ECUDA;
+  const long long per = wide ? 1 : kPairThreads / 32, blocks = (B + per - 1) / per;
+  return loss_call<1>(a.ends, one, blocks < 1 ? 1 : blocks < kLossBlocks ? (int)blocks : kLossBlocks, ws, s,
+                      [&](int n, int cluster) {
+                        if (vec)
+                          return wide ? launch(k_preference<true, kPairThreads>, n, kPairThreads, 0, s, cluster, a)
+                                      : launch(k_preference<true, 32>, n, kPairThreads, 0, s, cluster, a);
+                        return wide ? launch(k_preference<false, kPairThreads>, n, kPairThreads, 0, s, cluster, a)
+                                    : launch(k_preference<false, 32>, n, kPairThreads, 0, s, cluster, a);
+                      });
 }
 
 }  // extern "C"

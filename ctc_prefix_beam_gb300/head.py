@@ -460,7 +460,7 @@ def dropout_backward(dy: torch.Tensor, p: float, rng: torch.Tensor, *, out: Opti
 
 def _scores(t, shape, device, what: str):
     """float32 rows [..., L] at one stride: (tensor, stride)."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device or t.shape != shape:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != shape or t.device != device:
         raise ValueError(f"{what} must be a float32 tensor {list(shape)} on {device}")
     if t.is_contiguous():
         return t, shape[-1]
@@ -472,6 +472,11 @@ def _loss_grad(grad, reduction: int, shape, device):
     if grad is not None:
         _given(grad, shape if reduction == NONE else (), torch.float32, device, "grad")
     return grad
+
+
+def _status_or(workspace, need: int, device):
+    """A loss's workspace: small calls have only the status in it, and do without."""
+    return (None, 0) if workspace is None and need <= 256 else _workspace(workspace, need, device)
 
 
 def policy_loss_workspace_size(S: int, L: int) -> int:
@@ -514,7 +519,7 @@ def policy_loss(nll: torch.Tensor, old_nll: torch.Tensor, advantages: torch.Tens
     loss = torch.empty(shape if red == NONE else (), dtype=torch.float32, device=dev)
     stats = torch.empty(2, dtype=torch.float32, device=dev)
     dnll = None if g is None else torch.empty(shape, dtype=torch.float32, device=dev)
-    ws, nbytes = _workspace(workspace, policy_loss_workspace_size(S, L), dev)
+    ws, nbytes = _status_or(workspace, policy_loss_workspace_size(S, L), dev)
     _run(dev, "ctcpb_policy_loss", _p(a), lda, _p(o), ldo, _p(r), ldr, _p(v), ldv, _p(n), S, L, clip_low, clip_high,
          kl_weight, red, _p(g), _p(loss), _p(stats), _p(dnll), _p(ws), nbytes)
     return (loss, stats) if g is None else (loss, stats, dnll)
@@ -551,7 +556,7 @@ def preference_loss(nll: torch.Tensor, chosen: torch.Tensor, rejected: torch.Ten
     loss = torch.empty((B,) if red == NONE else (), dtype=torch.float32, device=dev)
     margins = torch.empty((B,), dtype=torch.float32, device=dev)
     dnll = None if g is None else torch.empty(shape, dtype=torch.float32, device=dev)
-    ws, nbytes = _workspace(workspace, preference_loss_workspace_size(B, N, L), dev)
+    ws, nbytes = _status_or(workspace, preference_loss_workspace_size(B, N, L), dev)
     _run(dev, "ctcpb_preference_loss", _p(a), lda, _p(r), ldr, _p(c), _p(j), _p(n), B, N, L, beta, margin, label_smoothing,
          int(bool(average)), red, _p(g), _p(loss), _p(margins), _p(dnll), _p(ws), nbytes)
     return (loss, margins) if g is None else (loss, margins, dnll)

@@ -645,8 +645,10 @@ int ctcpb_dropout(int type, const void* x, int64_t ldx, const void* residual, in
  *   dnll          [S, L] float32, dense, or NULL: the gradient with respect to nll,
  *                 0 behind the lengths; in the same pass, as ctcpb_cross_entropy_backward
  *                 takes it.
+ *   ws            ctcpb_policy_loss_workspace_size() bytes; may be NULL where that is
+ *                 256 (small calls, which have only the status in it).
  * Sums over tokens are pairs of float32 (value and error), made in a fixed order.
- * Limits: S, L <= 2^24.
+ * Limits: S, L <= 2^24, S * L <= 2^32.
  */
 #define CTCPB_REDUCE_SEQUENCE_MEAN 3
 int ctcpb_policy_loss_workspace_size(int64_t S, int64_t L, size_t* bytes);
@@ -675,6 +677,7 @@ int ctcpb_policy_loss(const float* nll, int64_t ld_nll, const float* old_nll, in
  *   loss, margins      margins [B]: z.  Each may be NULL.
  *   dnll               [B, N, L] float32, dense, or NULL: the gradient with respect to
  *                      nll, 0 for the other hypotheses and behind the lengths.
+ *   ws                 as in ctcpb_policy_loss; without one there is no status.
  * R is summed in pairs of float32 (value and error), in a fixed order.
  * Limits: B * N, L <= 2^24; 0 <= s <= 1; beta and margin finite.
  */

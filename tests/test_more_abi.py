@@ -44,7 +44,11 @@ def test_size_queries(lib):
     for shape in ((1 << 20, 16, 8192, 1), (1 << 24, 1, 64, 1), (1, 1 << 24, 8, 8), (1 << 12, 1 << 12, 513, 27)):
         for dtype, e in ((BF, 2), (torch.float32, 4)):
             assert head.group_norm_workspace_size(dtype, *shape, True) <= (64 << 20) + shape[0] * shape[1] * shape[2] * e // 50
-    assert head.policy_loss_workspace_size(320, 40) % 256 == 0 and head.preference_loss_workspace_size(32, 10, 40) > 0
+    # small calls have only the status in it, and may go without
+    assert head.policy_loss_workspace_size(320, 40) == head.preference_loss_workspace_size(32, 10, 40) == 256
+    for n in (head.policy_loss_workspace_size(4096, 1024), head.preference_loss_workspace_size(1024, 4, 1000),
+              head.policy_loss_workspace_size(1 << 24, 256), head.policy_loss_workspace_size(10000, 1)):
+        assert n % 256 == 0 and 256 < n < 1 << 20
     n = ctypes.c_size_t()
     g, p, q = (lib["ctcpb_%s_workspace_size" % x] for x in ("group_norm", "policy_loss", "preference_loss"))
     for bad in ((-1, 4, 64, 4), (4, -1, 64, 4), (4, 4, 0, 1), (4, 4, 64, 0), (4, 4, 64, 5), (4, 4, 8193, 1),
@@ -52,7 +56,7 @@ def test_size_queries(lib):
         assert g(BF16, *bad, 1, ctypes.byref(n)) == D.EINVAL, bad
     assert g(7, 4, 4, 64, 4, 1, ctypes.byref(n)) == D.EINVAL and g(BF16, 4, 4, 64, 4, 2, ctypes.byref(n)) == D.EINVAL
     assert g(BF16, 4, 4, 64, 4, 1, None) == D.ENULL
-    for bad in ((-1, 4), (4, -1), ((1 << 24) + 1, 4), (4, (1 << 24) + 1)):
+    for bad in ((-1, 4), (4, -1), ((1 << 24) + 1, 4), (4, (1 << 24) + 1), (1 << 16, (1 << 16) + 1)):
         assert p(*bad, ctypes.byref(n)) == D.EINVAL, bad
     for bad in ((-1, 4, 4), (4, 0, 4), (4, 4, -1), (1 << 22, 8, 4), (1, 4, (1 << 24) + 1)):
         assert q(*bad, ctypes.byref(n)) == D.EINVAL, bad
@@ -115,9 +119,9 @@ def test_policy_refusals(lib):
     for kw in (dict(ld=39), dict(ldo=39), dict(ldr=39), dict(lda=39), dict(lda=-1), dict(S=-1), dict(L=-1), dict(lo=-0.1),
                dict(lo=NAN), dict(lo=INF), dict(hi=-0.1), dict(hi=NAN), dict(kl=NAN), dict(kl=INF), dict(red=4), dict(red=-1)):
         assert call(**kw) == D.EINVAL, kw
-    for kw in (dict(nll=None), dict(old=None), dict(adv=None), dict(grad=None), dict(ws=None)):
+    for kw in (dict(nll=None), dict(old=None), dict(adv=None), dict(grad=None), dict(ws=None, S=10000)):
         assert call(**kw) == D.ENULL, kw
-    assert call(ws=P + 16) == D.EALIGN and call(nb=300) == D.ESIZE
+    assert call(ws=P + 16) == D.EALIGN and call(nb=200) == D.ESIZE and call(nb=300, S=10000) == D.ESIZE
 
 
 def test_preference_refusals(lib):
@@ -130,9 +134,9 @@ def test_preference_refusals(lib):
     for kw in (dict(ld=39), dict(ldr=39), dict(B=-1), dict(N=0), dict(L=-1), dict(beta=NAN), dict(beta=INF), dict(margin=INF),
                dict(s=-0.1), dict(s=1.1), dict(s=NAN), dict(avg=2), dict(red=3), dict(red=-1)):
         assert call(**kw) == D.EINVAL, kw
-    for kw in (dict(nll=None), dict(c=None), dict(r=None), dict(grad=None), dict(ws=None)):
+    for kw in (dict(nll=None), dict(c=None), dict(r=None), dict(grad=None), dict(ws=None, B=10000)):
         assert call(**kw) == D.ENULL, kw
-    assert call(ws=P + 16) == D.EALIGN and call(nb=300) == D.ESIZE
+    assert call(ws=P + 16) == D.EALIGN and call(nb=200) == D.ESIZE and call(nb=300, B=10000) == D.ESIZE
 
 
 def test_tensors_must_be_on_a_gpu():
