@@ -98,6 +98,22 @@ struct Sum2 {
     for (int s = 16; s > 0; s >>= 1) add(other(s));
   }
 };
+// Two such sums side by side.
+struct Sum2x2 {
+  u64 hi = 0, lo = 0;
+  __device__ __forceinline__ void add(u64 v) {
+    const u64 minus = pair(-1.f, -1.f), s = add2(hi, v), t = fma2(hi, minus, s);  // (products by -1 are exact)
+    lo = add2(lo, add2(fma2(fma2(t, minus, s), minus, hi), fma2(t, minus, v)));
+    hi = s;
+  }
+  __device__ __forceinline__ void into(Sum2& s) const {
+    Sum2 a, b;
+    unpair(a.hi, b.hi, hi);
+    unpair(a.lo, b.lo, lo);
+    s.add(a);
+    s.add(b);
+  }
+};
 // a - b as value and error
 __device__ __forceinline__ void add_difference(Sum2& s, float a, float b) {
   const float d = a - b, t = d - a;
@@ -105,25 +121,32 @@ __device__ __forceinline__ void add_difference(Sum2& s, float a, float b) {
   s.lo += (a - (d - t)) - (b + t);
 }
 
-// e^x - 1 and e^x - 1 - x.  Near 0 the second is x^2 (1/2! + x/3! + ...), the first
-// that and x: neither loses digits.  Elsewhere the exponential, less 1.
-__device__ __forceinline__ void exp_less(float x, float& e1, float& e2) {
-  if (fabsf(x) < 0.5f) {  // the next term is 2e-9 of the sum
-    float p = 1.f / 362880.f;
-    p = fmaf(p, x, 1.f / 40320.f);
-    p = fmaf(p, x, 1.f / 5040.f);
-    p = fmaf(p, x, 1.f / 720.f);
-    p = fmaf(p, x, 1.f / 120.f);
-    p = fmaf(p, x, 1.f / 24.f);
-    p = fmaf(p, x, 1.f / 6.f);
-    p = fmaf(p, x, 0.5f);
-    e2 = p * x * x;
-    e1 = e2 + x;
-  } else {
-    e1 = expf(x) - 1.f;
-    e2 = isinf(e1) ? e1 : e1 - x;
+// e^x - 1 and e^x - 1 - x.  With n the integer next to x / ln 2 and r = x - n ln 2 (in
+// two steps, Cody and Waite), e^x = 2^n (1 + r + c), c = r^2 (1/2! + r/3! + ...) by its
+// Taylor series (the first term left out is 9e-8 of c at most, at |r| = ln 2 / 2).  Next
+// to 0, where n = 0, nothing cancels: e^x - 1 - x is c.  Above 88.37 the exponential is
+// infinite.  (One value at a time: the constants are immediates then.  In pairs they
+// would take two registers each, and were loaded again for every token.)
+struct ExpLess {
+  float x, r, c, s, less;
+  __device__ __forceinline__ explicit ExpLess(float v) {
+    x = v > 88.37f ? 89.f : v;
+    float y;  // (NaN stays NaN)
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-87.f));
+    const float t = fmaf(y, 1.4426950408889634f, 12582912.f), n = t - 12582912.f;  // n is in t's lowest bits
+    r = fmaf(n, 2.12194440e-4f, fmaf(n, -0.693359375f, y));
+    c = fmaf(1.f / 5040.f, r, 1.f / 720.f);
+    c = fmaf(c, r, 1.f / 120.f);
+    c = fmaf(c, r, 1.f / 24.f);
+    c = fmaf(c, r, 1.f / 6.f);
+    c = fmaf(c, r, 0.5f);
+    c = c * (r * r);
+    s = __int_as_float((__float_as_int(t) << 23) + 0x3f800000);
+    less = s - 1.f;
   }
-}
+  __device__ __forceinline__ float one() const { return fmaf(s, r + c, less); }
+  __device__ __forceinline__ float two() const { return fmaf(s, c, fmaf(s, r, less) - x); }
+};
 
 __device__ __forceinline__ long long length_of(const int* lengths, long long s, long long L) {
   if (!lengths) return L;
@@ -322,39 +345,39 @@ struct PolicyArgs {
   const float* grad;
   float *loss, *dnll;  // the loss of each token (REDUCE_NONE)
   Divisor pieces;      // vectors of a row
+  int dense;           // the rows of all inputs lie end to end
   u32 work;            // vectors of all rows
   Ends ends;
 };
 
-// One token.  `hold`: the ratio is past the border and counts no more.
-__device__ __forceinline__ void token(const PolicyArgs& a, float nll, float old, float ref, float A, Sum2& loss, float& kl,
-                                      float& held, float& slope, float& each) {
+// One token.  A ratio past the border is held there and counts no more.  Returns the
+// loss but for its -A.
+__device__ __forceinline__ float token(const PolicyArgs& a, float nll, float old, float ref, float A, float& kl, float& held,
+                                       float& slope) {
   const float d = old - nll;
-  float q, k;
-  exp_less(d, q, k);
-  bool hold = false;
+  float q = ExpLess(d).one();
+  const bool up = A > 0.f;
+  const float side = __int_as_float(__float_as_int(d) ^ (__float_as_int(A) & 0x80000000)) - (up ? a.fhigh : -a.flow);
+  bool hold = side > 0.f && A != 0.f;
   // d is rounded, which keeps its order with a rounded border: only where the two
   // are equal does it take the exact difference
-  if (A > 0.f)
-    hold = d > a.fhigh || (d == a.fhigh && (double)old - (double)nll > a.high);
-  else if (A < 0.f)
-    hold = d < a.flow || (d == a.flow && (double)old - (double)nll < a.low);
-  else if (A == 0.f)
-    q = 0.f;  // a token without an advantage adds nothing, whatever its ratio overflows to
-  slope = hold ? 0.f : fmaf(A, q, A);
-  if (hold) q = A > 0.f ? a.qhigh : a.qlow;
-  float more = -A * q;
-  if (a.ref) {
-    float e;
-    exp_less(nll - ref, e, k);
-    kl += k;
-    more = fmaf(a.kl, k, more);
-    slope = fmaf(a.kl, e, slope);
+  if (side == 0.f && A != 0.f) {
+    const double exact = (double)old - (double)nll;
+    hold = up ? exact > a.high : exact < a.low;
   }
-  loss.add(-A);
-  loss.add(more);
+  if (A == 0.f) q = 0.f;  // a token without an advantage adds nothing, whatever its ratio overflows to
+  slope = hold ? 0.f : fmaf(A, q, A);
+  if (hold) q = up ? a.qhigh : a.qlow;
+  float rest = -A * q;
+  if (a.ref) {
+    const ExpLess e(nll - ref);
+    const float k = e.two();
+    kl += k;
+    rest = fmaf(a.kl, k, rest);
+    slope = fmaf(a.kl, e.one(), slope);
+  }
   held += hold ? 1.f : 0.f;
-  each = more - A;
+  return rest;
 }
 
 // A thread's tokens: four of a row, or one.
@@ -370,15 +393,16 @@ struct Tokens {
     }
   }
   // (a vector may reach behind the length, not behind the row)
-  __device__ __forceinline__ void load(const PolicyArgs& a, bool none, u32 s, long long t) {
-    get(nll, a.nll + s * a.ld_nll + t);
-    get(old, a.old + s * a.ld_old + t);
-    if (a.ref) get(ref, a.ref + s * a.ld_ref + t);
+  __device__ __forceinline__ void load(const PolicyArgs& a, bool none, u64 x, u32 s, u32 t) {
+    const u64 flat = x * V;  // rows end to end
+    get(nll, a.nll + (a.dense ? flat : s * a.ld_nll + t));
+    get(old, a.old + (a.dense ? flat : s * a.ld_old + t));
+    if (a.ref) get(ref, a.ref + (a.dense ? flat : s * a.ld_ref + t));
     if (a.ld_adv)
-      get(adv, a.adv + s * a.ld_adv + t);
+      get(adv, a.adv + (a.dense ? flat : s * a.ld_adv + t));
     else
       adv[0] = a.adv[s];
-    if (none && a.grad) get(up, a.grad + s * a.L + t);
+    if (none && a.grad) get(up, a.grad + flat);
   }
 };
 // Where a thread's tokens are: the row, the first, how many of its length.
@@ -389,14 +413,15 @@ struct At {
     if (x < a.work) {
       s = a.pieces((u32)x);
       t = ((u32)x - s * a.pieces.d) * V;
-      len = (u32)length_of(a.lengths, s, a.L);
+      const int n = a.lengths ? a.lengths[s] : (int)a.L;
+      len = n < 0 ? 0 : n < (int)a.L ? n : (u32)a.L;
     }
   }
   __device__ __forceinline__ int live(int V) const { return len <= t ? 0 : len - t >= (u32)V ? V : (int)(len - t); }
 };
 
 template <bool VEC>
-__global__ void __launch_bounds__(kLossThreads) k_policy(const PolicyArgs a) {
+__global__ void __launch_bounds__(kLossThreads, 3) k_policy(const PolicyArgs a) {
   __shared__ Shared sh;
   constexpr int V = VEC ? 4 : 1;
   pdl_wait();
@@ -408,38 +433,62 @@ __global__ void __launch_bounds__(kLossThreads) k_policy(const PolicyArgs a) {
   At at, next;
   Tokens<V> ahead;
   at.set(a, x, V);
-  if (at.live(V)) ahead.load(a, none, at.s, at.t);
+  if (at.live(V)) ahead.load(a, none, x, at.s, at.t);
   next.set(a, x + step, V);
   begin(a.ends, sh);
   const float g = sh.ctl.grad;
   Sum2 sums[3];
+  float kl = 0.f, held = 0.f;  // (terms of one sign, some tens a thread)
   for (; x < a.work; x += step) {
-    const Tokens<V> k = ahead;
+    Tokens<V> k = ahead;
     const At now = at;
     at = next;
-    if (at.live(V)) ahead.load(a, none, at.s, at.t);
+    if (at.live(V)) ahead.load(a, none, x + step, at.s, at.t);
     next.set(a, x + 2 * step, V);
     const int live = now.live(V);
-    // 1 / len, and what its rounding took off (len <= 2^24 is exact)
-    const float len = (float)now.len, wt = by_len && live ? 1.f / len : 1.f;
-    const float gw = g * wt;
     float slope[V], each[V];
-    Sum2 loss;
-    float kl = 0.f, held = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      slope[i] = each[i] = 0.f;
-      if (i < live) {
-        token(a, k.nll[i], k.old[i], a.ref ? k.ref[i] : 0.f, k.adv[a.ld_adv ? i : 0], loss, kl, held, slope[i], each[i]);
-        slope[i] *= none ? (a.grad ? k.up[i] : 1.f) : gw;
-      }
-    }
     if (live) {
+      if (!a.ld_adv) {
+#pragma unroll
+        for (int i = 1; i < V; ++i) k.adv[i] = k.adv[0];
+      }
+      if (V > 1 && live < V) {  // a token that is not there has no advantage, and the same score three times
+#pragma unroll
+        for (int i = 1; i < V; ++i)
+          if (i >= live) k.nll[i] = k.old[i] = k.ref[i] = k.adv[i] = 0.f;
+      }
+      // 1 / len, and what its rounding took off (len <= 2^24 is exact)
+      const float len = (float)now.len, wt = by_len ? 1.f / len : 1.f;
+      const float gw = g * wt;
+      float more = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float rest = token(a, k.nll[i], k.old[i], k.ref[i], k.adv[i], kl, held, slope[i]);
+        more += rest;
+        each[i] = rest - k.adv[i];
+        slope[i] *= none ? (a.grad && i < live ? k.up[i] : 1.f) : gw;
+      }
+      if (V > 1 && live < V) {
+#pragma unroll
+        for (int i = 1; i < V; ++i)
+          if (i >= live) slope[i] = each[i] = 0.f;
+      }
+      Sum2 loss;
+      loss.hi = more;
+      if constexpr (V == 4) {
+        Sum2x2 advs;
+        advs.hi = pair(-k.adv[0], -k.adv[1]);
+        advs.add(pair(-k.adv[2], -k.adv[3]));
+        advs.into(loss);
+      } else {
+        loss.add(-k.adv[0]);
+      }
       sums[0].add(by_len ? loss.times(wt, fmaf(-wt, len, 1.f) * wt) : loss);
-      sums[1].add(kl);
-      sums[2].add(held);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) slope[i] = each[i] = 0.f;
     }
-    const long long o = now.s * a.L + now.t;
+    const u64 o = x * V;
     if constexpr (VEC) {
       if (a.dnll) __stcs(reinterpret_cast<float4*>(a.dnll + o), make_float4(slope[0], slope[1], slope[2], slope[3]));
       if (a.loss) __stcs(reinterpret_cast<float4*>(a.loss + o), make_float4(each[0], each[1], each[2], each[3]));
@@ -448,6 +497,8 @@ __global__ void __launch_bounds__(kLossThreads) k_policy(const PolicyArgs a) {
       if (a.loss) a.loss[o] = each[0];
     }
   }
+  sums[1].add(kl);
+  sums[2].add(held);
   end<3>(a.ends, sums, sh);
 }
 
@@ -684,6 +735,7 @@ int ctcpb_policy_loss(const float* nll, int64_t ld_nll, const float* old_nll, in
   const long long pieces = vec ? L / 4 : L;
   a.pieces = Divisor(any ? (u32)pieces : 1u);
   a.work = any ? (u32)(S * pieces) : 0u;
+  a.dense = ld_nll == L && ld_old == L && (!ref_nll || ld_ref == L) && (ld_advantages == 0 || ld_advantages == L);
   a.ends.counted = Counted{lengths, nullptr, nullptr, a.S, L, 0, reduction, grad};
   a.ends.loss = none ? nullptr : loss;
   a.ends.stats = stats;
