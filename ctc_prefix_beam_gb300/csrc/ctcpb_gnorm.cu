@@ -149,13 +149,15 @@ __global__ void __launch_bounds__(kGnThreads, 2) k_gn_bwd(const GnArgs a) {
   Two* const own = each + blockDim.x;
   Two* const all = own + a.gs;
   float* const red = reinterpret_cast<float*>(all + a.gs);
-  const u32 keep = (saddr(red + (a.cols ? 2 * a.cr * a.tw * V : 0)) + 15u & ~15u) + threadIdx.x * W::bytes;
+  const u32 keep = (saddr(red + 2 * a.cr * a.tw * V) + 15u & ~15u) + threadIdx.x * W::bytes;
   const u32 pitch = blockDim.x * W::bytes, second = a.slots * pitch;  // dy lies behind x
   Place p;
   p.set<V>(a, blockIdx.x / (u32)a.parts, blockIdx.x % (u32)a.parts);
   pdl_wait();
   pdl_next();
   u64 w[P], bias[P];
+  params_of<V>(a, p.c0 + p.cv * V, p.on, w, bias);
+  const int group = p.g0 + p.group<V>(a);
   for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
     const int len = frames_of(a, b);
     const Rows rows(a, p, len);
@@ -163,14 +165,16 @@ __global__ void __launch_bounds__(kGnThreads, 2) k_gn_bwd(const GnArgs a) {
     const T* const dy = (const T*)a.dy + (long long)b * a.dy_b + p.c0;
     fetch_rows<T, V>(keep, pitch, x + rows.first * a.x_t + p.cv * V, a.rs * a.x_t, rows.n);
     fetch_rows<T, V>(keep + second, pitch, dy + rows.first * a.dy_t + p.cv * V, a.rs * a.dy_t, rows.n);
-    params_of<V>(a, p.c0 + p.cv * V, p.on, w, bias);
-    const long long o = (long long)b * a.G + p.g0 + p.group<V>(a);
+    const long long o = (long long)b * a.G + group;
     const float mean = a.mean[o], rstd = a.rstd[o];
-    const u64 nm = pair(-mean, -mean), rr = pair(rstd, rstd);
-    cp_wait_all();
-    u64 sw[P], sb[P];
+    const u64 nm = pair(-mean, -mean);
+    u64 wr[P], sw[P], sb[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) sw[i] = sb[i] = 0;
+    for (int i = 0; i < P; ++i) {
+      wr[i] = mul2(w[i], pair(rstd, rstd));
+      sw[i] = sb[i] = 0;
+    }
+    cp_wait_all();
 #pragma unroll 2
     for (int k = 0; k < rows.n; ++k) {
       W raw;
@@ -179,31 +183,21 @@ __global__ void __launch_bounds__(kGnThreads, 2) k_gn_bwd(const GnArgs a) {
       raw.get(v);
       raw.load_shared(keep + second + k * pitch);
       raw.get(d);
-      before(v, d, nm, rr, w, bias, a.act);
+      before(v, d, nm, wr, bias, a.act);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         sw[i] = fma2(d[i], v[i], sw[i]);
         sb[i] = add2(sb[i], d[i]);
       }
     }
-    Two m;
-    {
-      u64 t[P];
-#pragma unroll
-      for (int i = 0; i < P; ++i) t[i] = mul2(sb[i], w[i]);
-      m.a = lanes<V>(t);
-#pragma unroll
-      for (int i = 0; i < P; ++i) t[i] = mul2(sw[i], w[i]);
-      m.b = lanes<V>(t);
-    }
-    if (a.cols) column_sums<V>(a, p, sw, sb, red, (long long)blockIdx.y * a.parts + p.part, b != (int)blockIdx.y);
+    const Two m = thread_sums<V>(sw, sb, wr);
+    if (a.cols) add_columns<V>(a, p, sw, sb, rstd, red, b != (int)blockIdx.y);
     if (a.y) {
       T* const y = (T*)a.y + (long long)b * a.y_b + p.c0;
       by_group<Two, V>(a, p, m, each, [&](int g, const Two& t) { (a.parts > 1 ? own : all)[g] = t; });
       over_cluster(a, p, own, all);
-      const Two t = all[p.group<V>(a)];
-      const float inv = len > 0 ? 1.f / ((float)len * (float)a.D) : 0.f, c0 = -rstd * t.a * inv, c1 = -rstd * t.b * inv;
-      const u64 m0 = pair(c0, c0), m1 = pair(c1, c1);
+      u64 m0, m1;
+      factors(a, all[p.group<V>(a)], len, rstd, m0, m1);
       const long long step = a.rs * a.y_t;
       T* to = y + rows.first * a.y_t + p.cv * V;
 #pragma unroll 2
@@ -214,9 +208,9 @@ __global__ void __launch_bounds__(kGnThreads, 2) k_gn_bwd(const GnArgs a) {
         raw.get(v);
         raw.load_shared(keep + second + k * pitch);
         raw.get(d);
-        before(v, d, nm, rr, w, bias, a.act);
+        before(v, d, nm, wr, bias, a.act);
 #pragma unroll
-        for (int i = 0; i < P; ++i) d[i] = fma2(mul2(d[i], w[i]), rr, fma2(v[i], m1, m0));
+        for (int i = 0; i < P; ++i) d[i] = fma2(d[i], wr[i], fma2(v[i], m1, m0));
         raw.put(d);
         raw.store(to);
       }
@@ -225,6 +219,7 @@ __global__ void __launch_bounds__(kGnThreads, 2) k_gn_bwd(const GnArgs a) {
     }
     __syncthreads();
   }
+  if (a.cols) column_sums<V>(a, p, red, (long long)blockIdx.y * a.parts + p.part);
 }
 
 // dw and db: the blocks' sums, in order (32 slices of them, then the slices).

@@ -335,13 +335,12 @@ __device__ __forceinline__ u64 silu2(u64 h) {
 __device__ __forceinline__ u64 silu_slope2(u64 h) {
   float x, y;
   unpair(x, y, mul2(h, pair(-kLog2e, -kLog2e)));
-  // (NaN stays NaN)
-  x = x > 63.f ? 63.f : x;
-  y = y > 63.f ? 63.f : y;
-  unpair(x, y, add2(pair(ex2(x), ex2(y)), pair(1.f, 1.f)));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(63.f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(63.f));
+  const u64 one = pair(1.f, 1.f), other = add2(pair(ex2(y), ex2(x)), one);  // each lane the other's
+  unpair(y, x, other);
   const float r = rcp(x * y);
-  const u64 s = mul2(pair(r, r), pair(y, x));
-  const u64 one = pair(1.f, 1.f), rest = fma2(s, pair(-1.f, -1.f), one);
+  const u64 s = mul2(pair(r, r), other), rest = fma2(s, pair(-1.f, -1.f), one);
   return mul2(s, fma2(h, rest, one));
 }
 __device__ __forceinline__ float relu(float x) { return x > 0.f ? x : x != x ? x : 0.f; }
@@ -363,23 +362,45 @@ __device__ __forceinline__ void activate(u64 (&v)[P], u64 nm, const u64 (&w)[P],
     }
   }
 }
-// x -> xh, dy -> dh
+// x -> x - mean, dy -> dh (wr: the weight times rstd)
 template <int P>
-__device__ __forceinline__ void before(u64 (&x)[P], u64 (&d)[P], u64 nm, u64 rr, const u64 (&w)[P], const u64 (&b)[P], int act) {
+__device__ __forceinline__ void before(u64 (&x)[P], u64 (&d)[P], u64 nm, const u64 (&wr)[P], const u64 (&b)[P], int act) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) x[i] = mul2(add2(x[i], nm), rr);
+  for (int i = 0; i < P; ++i) x[i] = add2(x[i], nm);
   if (act == CTCPB_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) d[i] = mul2(d[i], silu_slope2(fma2(x[i], w[i], b[i])));
+    for (int i = 0; i < P; ++i) d[i] = mul2(d[i], silu_slope2(fma2(x[i], wr[i], b[i])));
   } else if (act == CTCPB_ACT_RELU) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       float h, k, p, q;
-      unpair(h, k, fma2(x[i], w[i], b[i]));
+      unpair(h, k, fma2(x[i], wr[i], b[i]));
       unpair(p, q, d[i]);
       d[i] = pair(h > 0.f ? p : 0.f, k > 0.f ? q : 0.f);
     }
   }
+}
+// A thread's sums of an utterance, of dh (x - mean) and dh, as the group's of dh w and
+// dh w xh (the first times rstd, which dx has as a factor).
+template <int V>
+__device__ __forceinline__ Two thread_sums(const u64 (&sw)[(V + 1) / 2], const u64 (&sb)[(V + 1) / 2],
+                                           const u64 (&wr)[(V + 1) / 2]) {
+  constexpr int P = (V + 1) / 2;
+  u64 a[P], b[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    a[i] = mul2(sb[i], wr[i]);
+    b[i] = mul2(sw[i], wr[i]);
+  }
+  return Two{lanes<V>(a), lanes<V>(b)};
+}
+// dx = dh wr + (x - mean) m1 + m0, from the group's sums above: m0 = -rstd mean(dh w),
+// m1 = -rstd^2 mean(dh w xh)
+__device__ __forceinline__ void factors(const GnArgs& a, const Two& t, int len, float rstd, u64& m0, u64& m1) {
+  const float inv = len > 0 ? __fdividef(1.f, (float)len * (float)a.D) : 0.f;
+  const float c0 = -t.a * inv, c1 = -t.b * inv * rstd * rstd;
+  m0 = pair(c0, c0);
+  m1 = pair(c1, c1);
 }
 
 // ---------------------------------------------------------------- sums over a block
@@ -402,15 +423,17 @@ __device__ __forceinline__ void by_group(const GnArgs& a, const Place& p, const 
   }
 }
 
-// Column sums of the threads' sw, sb into `red` [cr][2][tw * V] (a warp's threads
-// of one column first, where its columns repeat), then a.cols, in order: set on a
-// block's first utterance, else added.  A barrier is between writing and reading.
+// The threads' column sums of an utterance (of dh (x - mean), times rstd, and dh) into
+// `red` [cr][2][tw * V]: a warp's threads of one column first, where its columns repeat.
+// A thread's place there is its own.
 template <int V>
-__device__ __forceinline__ void column_sums(const GnArgs& a, const Place& p, u64 (&sw)[(V + 1) / 2], u64 (&sb)[(V + 1) / 2],
-                                            float* red, long long row, bool more) {
+__device__ __forceinline__ void add_columns(const GnArgs& a, const Place& p, u64 (&sw)[(V + 1) / 2], u64 (&sb)[(V + 1) / 2],
+                                            float rstd, float* red, bool more) {
   constexpr int P = (V + 1) / 2;
   const int width = a.tw * V;
   const bool by_warp = a.cr < a.rs;
+#pragma unroll
+  for (int i = 0; i < P; ++i) sw[i] = mul2(sw[i], pair(rstd, rstd));
   if (by_warp)
     for (int m = a.tw; m < 32; m <<= 1) {
 #pragma unroll
@@ -421,28 +444,36 @@ __device__ __forceinline__ void column_sums(const GnArgs& a, const Place& p, u64
     }
   const int at = by_warp ? threadIdx.x >> 5 : p.ty;
   if (by_warp ? (int)(threadIdx.x & 31) < a.tw : p.ty < a.rs) {
+    float* const o = red + 2 * at * width + p.cv * V;
+    if constexpr (V == 1) {
+      float x, y, none;
+      unpair(x, none, sw[0]);
+      unpair(y, none, sb[0]);
+      o[0] = more ? o[0] + x : x;
+      o[width] = more ? o[width] + y : y;
+    } else {
+      u64* const ow = reinterpret_cast<u64*>(o);
+      u64* const ob = reinterpret_cast<u64*>(o + width);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      float x[2], y[2];
-      unpair(x[0], x[1], sw[i]);
-      unpair(y[0], y[1], sb[i]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (2 * i + k < V) {
-          red[(2 * at) * width + p.cv * V + 2 * i + k] = x[k];
-          red[(2 * at + 1) * width + p.cv * V + 2 * i + k] = y[k];
-        }
+      for (int i = 0; i < P; ++i) {
+        ow[i] = more ? add2(ow[i], sw[i]) : sw[i];
+        ob[i] = more ? add2(ob[i], sb[i]) : sb[i];
+      }
     }
   }
-  __syncthreads();
+}
+// ... and from there, after a barrier, into a.cols, in order.
+template <int V>
+__device__ __forceinline__ void column_sums(const GnArgs& a, const Place& p, const float* red, long long row) {
+  const int width = a.tw * V;
   float* const to = a.cols + row * 2 * a.C + p.c0;
   for (int e = threadIdx.x; e < 2 * width; e += blockDim.x) {
     const int second = e >= width, c = e - second * width;
     if (c >= p.wv * V) continue;
     float s = 0.f;
+#pragma unroll 4
     for (int k = 0; k < a.cr; ++k) s += red[2 * k * width + e];
-    float* const o = to + second * (long long)a.C + c;
-    *o = more ? *o + s : s;
+    to[second * (long long)a.C + c] = s;
   }
 }
 

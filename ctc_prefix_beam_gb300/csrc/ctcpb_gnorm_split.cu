@@ -155,10 +155,13 @@ __global__ void __launch_bounds__(kGnThreads, 1) k_gn_bwd_sums(const GnArgs a) {
     const T* dy = (const T*)a.dy + (long long)b * a.dy_b + p.c0 + rows.first * a.dy_t + p.cv * V;
     const long long step = a.rs * a.x_t, d_step = a.rs * a.dy_t, o = (long long)b * a.G + p.g0 + p.group<V>(a);
     const float mean = a.mean[o], rstd = a.rstd[o];
-    const u64 nm = pair(-mean, -mean), rr = pair(rstd, rstd);
-    u64 sw[P], sb[P];
+    const u64 nm = pair(-mean, -mean);
+    u64 wr[P], sw[P], sb[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) sw[i] = sb[i] = 0;
+    for (int i = 0; i < P; ++i) {
+      wr[i] = mul2(w[i], pair(rstd, rstd));
+      sw[i] = sb[i] = 0;
+    }
     for (int k = 0; k < rows.n; k += U, x += U * step, dy += U * d_step) {
       W raw[U], raw_d[U];
 #pragma unroll
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(kGnThreads, 1) k_gn_bwd_sums(const GnArgs a) {
           u64 v[P], d[P];
           raw[i].get(v);
           raw_d[i].get(d);
-          before(v, d, nm, rr, w, bias, a.act);
+          before(v, d, nm, wr, bias, a.act);
 #pragma unroll
           for (int j = 0; j < P; ++j) {
             sw[j] = fma2(d[j], v[j], sw[j]);
@@ -181,20 +184,12 @@ __global__ void __launch_bounds__(kGnThreads, 1) k_gn_bwd_sums(const GnArgs a) {
           }
         }
     }
-    Two m;
-    {
-      u64 t[P];
-#pragma unroll
-      for (int i = 0; i < P; ++i) t[i] = mul2(sb[i], w[i]);
-      m.a = lanes<V>(t);
-#pragma unroll
-      for (int i = 0; i < P; ++i) t[i] = mul2(sw[i], w[i]);
-      m.b = lanes<V>(t);
-    }
-    if (a.cols) column_sums<V>(a, p, sw, sb, red, (long long)blockIdx.z * a.parts + p.part, b != (int)blockIdx.z);
+    const Two m = thread_sums<V>(sw, sb, wr);
+    if (a.cols) add_columns<V>(a, p, sw, sb, rstd, red, b != (int)blockIdx.z);
     if (a.y) by_group<Two, V>(a, p, m, each, [&](int g, const Two& t) { group_slot<Two>(a, p, b)[g * a.pieces] = t; });
     __syncthreads();
   }
+  if (a.cols) column_sums<V>(a, p, red, (long long)blockIdx.z * a.parts + p.part);
 }
 
 template <class T, int V>
@@ -217,11 +212,12 @@ __global__ void __launch_bounds__(kGnThreads, 1) k_gn_bwd_apply(const GnArgs a) 
     T* const y = (T*)a.y + (long long)b * a.y_b + p.c0;
     const long long o = (long long)b * a.G + p.g0 + p.group<V>(a);
     const float mean = a.mean[o], rstd = a.rstd[o];
-    const u64 nm = pair(-mean, -mean), rr = pair(rstd, rstd);
+    const u64 nm = pair(-mean, -mean);
+    u64 wr[P], m0, m1;
+#pragma unroll
+    for (int i = 0; i < P; ++i) wr[i] = mul2(w[i], pair(rstd, rstd));
     over_parts<Two>(a, p, b, all);
-    const Two t = all[p.group<V>(a)];
-    const float inv = len > 0 ? 1.f / ((float)len * (float)a.D) : 0.f, c0 = -rstd * t.a * inv, c1 = -rstd * t.b * inv;
-    const u64 m0 = pair(c0, c0), m1 = pair(c1, c1);
+    factors(a, all[p.group<V>(a)], len, rstd, m0, m1);
     const long long step = a.rs * a.x_t, d_step = a.rs * a.dy_t, y_step = a.rs * a.y_t;
     T* to = y + rows.first * a.y_t + p.cv * V;
     for (int k = 0; k < rows.n; k += U, x += U * step, dy += U * d_step, to += U * y_step) {
@@ -238,9 +234,9 @@ __global__ void __launch_bounds__(kGnThreads, 1) k_gn_bwd_apply(const GnArgs a) 
           u64 v[P], d[P];
           raw[i].get(v);
           raw_d[i].get(d);
-          before(v, d, nm, rr, w, bias, a.act);
+          before(v, d, nm, wr, bias, a.act);
 #pragma unroll
-          for (int j = 0; j < P; ++j) d[j] = fma2(mul2(d[j], w[j]), rr, fma2(v[j], m1, m0));
+          for (int j = 0; j < P; ++j) d[j] = fma2(d[j], wr[j], fma2(v[j], m1, m0));
           raw[i].put(d);
           raw[i].store(to + i * y_step);
         }

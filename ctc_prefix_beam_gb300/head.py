@@ -172,10 +172,13 @@ if _raw is not None:
         return _raw(dev.index)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # without its lazy initialisation
+
+
 def _run(dev: torch.device, what: str, *args):
     """Call a library entry point on ``dev``'s current stream, ``dev`` current."""
-    fn = _lib()[what]
-    if dev.index == torch.cuda.current_device():
+    fn = (_fns or _lib())[what]
+    if dev.index == _current_device():
         rc = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -332,6 +335,11 @@ def cross_entropy_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Te
     return dx, dw, db
 
 
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _frames(t: torch.Tensor, what: str, dtype=None):
     """``t`` [B, T, C], channels contiguous and the rows of an utterance at one
     stride of at least C (else it is copied): (tensor, its strides)."""
@@ -340,7 +348,9 @@ def _frames(t: torch.Tensor, what: str, dtype=None):
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}")
     B, T, C = t.shape
-    if not t.is_contiguous() and (C > 1 and t.stride(2) != 1 or T > 1 and t.stride(1) < C):
+    if t.is_contiguous():
+        return t, T * C, C
+    if C > 1 and t.stride(2) != 1 or T > 1 and t.stride(1) < C:
         t = t.contiguous()
     return t, t.stride(0) if B > 1 else T * C, t.stride(1) if T > 1 else C
 
@@ -381,9 +391,9 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
     w, b, pt = _params(dt, C, dev, "weight", weight, "bias", bias)
     n = _ints(lengths, (B,), dev, "lengths")
     if outputs is None:
-        y = torch.empty((B, T, C), dtype=dt, device=dev)
+        y = _like(xr)
         mean = torch.empty((B, G), dtype=torch.float32, device=dev)
-        rstd = torch.empty((B, G), dtype=torch.float32, device=dev)
+        rstd = torch.empty_like(mean)
     else:
         y, mean, rstd = outputs
         _given(y, x.shape, dt, dev, "y")
@@ -421,13 +431,16 @@ def group_norm_backward(dy: torch.Tensor, x: torch.Tensor, groups: int, weight: 
             raise ValueError(f"param_dtype must be {dt} or float32")
         pt = param_dtype
     n = _ints(lengths, (B,), dev, "lengths")
-    dx = torch.empty((B, T, C), dtype=dt, device=dev)
+    dx = _like(xr)
     dw = torch.empty((C,), dtype=pt, device=dev)
-    db = torch.empty((C,), dtype=pt, device=dev)
+    db = torch.empty_like(dw)
     ws, nbytes = _workspace(workspace, group_norm_workspace_size(dt, B, T, C, G, True), dev)
     _run(dev, "ctcpb_group_norm_backward", _TYPES[dt], _TYPES[pt], _p(dyr), db_, dt_, _p(xr), sb, st, _p(w), _p(b), _p(n),
          _p(mean), _p(rstd), act, B, T, C, G, _p(dx), T * C, C, _p(dw), _p(db), _p(ws), nbytes)
     return dx, dw, db
+
+
+_TWO = torch.Size((2,))
 
 
 def dropout(x: torch.Tensor, p: float, rng: torch.Tensor, *, residual: Optional[torch.Tensor] = None,
@@ -439,7 +452,7 @@ def dropout(x: torch.Tensor, p: float, rng: torch.Tensor, *, residual: Optional[
     ``out``: the tensor to write, which may be x or residual."""
     xr, N, H, ldx = _rows(x, "x")
     dev, dt = xr.device, xr.dtype
-    if not isinstance(rng, torch.Tensor) or rng.dtype != torch.int64 or rng.shape != (2,) or rng.device != dev or \
+    if not isinstance(rng, torch.Tensor) or rng.dtype is not torch.int64 or rng.shape != _TWO or rng.device != dev or \
             not rng.is_contiguous():
         raise ValueError(f"rng must be a contiguous int64 tensor [2] on {dev}")
     r, ldr = None, 0
@@ -447,7 +460,7 @@ def dropout(x: torch.Tensor, p: float, rng: torch.Tensor, *, residual: Optional[
         r, _, _, ldr = _rows(residual, "residual", dt)
         if residual.shape != x.shape or r.device != dev:
             raise ValueError("residual must have x's shape and device")
-    y = torch.empty(x.shape, dtype=dt, device=dev) if out is None else _given(out, x.shape, dt, dev, "out")
+    y = _like(x) if out is None else _given(out, x.shape, dt, dev, "out")
     _run(dev, "ctcpb_dropout", _TYPES[dt], _p(xr), ldx, _p(r), ldr, p, _p(rng), N, H, _p(y), H)
     return y
 
@@ -516,9 +529,9 @@ def policy_loss(nll: torch.Tensor, old_nll: torch.Tensor, advantages: torch.Tens
     n = _ints(lengths, lead, dev, "lengths")
     S = lead.numel()
     g = _loss_grad(grad, red, shape, dev)
-    loss = torch.empty(shape if red == NONE else (), dtype=torch.float32, device=dev)
+    loss = _like(nll) if red == NONE else torch.empty((), dtype=torch.float32, device=dev)
     stats = torch.empty(2, dtype=torch.float32, device=dev)
-    dnll = None if g is None else torch.empty(shape, dtype=torch.float32, device=dev)
+    dnll = None if g is None else _like(nll)
     ws, nbytes = _status_or(workspace, policy_loss_workspace_size(S, L), dev)
     _run(dev, "ctcpb_policy_loss", _p(a), lda, _p(o), ldo, _p(r), ldr, _p(v), ldv, _p(n), S, L, clip_low, clip_high,
          kl_weight, red, _p(g), _p(loss), _p(stats), _p(dnll), _p(ws), nbytes)
@@ -555,7 +568,7 @@ def preference_loss(nll: torch.Tensor, chosen: torch.Tensor, rejected: torch.Ten
     g = _loss_grad(grad, red, (B,), dev)
     loss = torch.empty((B,) if red == NONE else (), dtype=torch.float32, device=dev)
     margins = torch.empty((B,), dtype=torch.float32, device=dev)
-    dnll = None if g is None else torch.empty(shape, dtype=torch.float32, device=dev)
+    dnll = None if g is None else _like(nll)
     ws, nbytes = _status_or(workspace, preference_loss_workspace_size(B, N, L), dev)
     _run(dev, "ctcpb_preference_loss", _p(a), lda, _p(r), ldr, _p(c), _p(j), _p(n), B, N, L, beta, margin, label_smoothing,
          int(bool(average)), red, _p(g), _p(loss), _p(margins), _p(dnll), _p(ws), nbytes)
