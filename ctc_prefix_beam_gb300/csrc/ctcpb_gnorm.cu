@@ -20,9 +20,9 @@
 namespace ctcpb {
 namespace {
 
-constexpr int kGnRanks = 8;              // blocks that share a slab at most
-constexpr int kGnSmem = 200 * 1024;      // what a block keeps of a slab at most
-constexpr int kGnSmemShare = 72 * 1024;  // ... and where more blocks can share it: three on an SM
+constexpr int kGnRanks = 16;             // blocks that share a slab at most
+constexpr int kGnSmem = 80 * 1024;       // what a block has of shared memory at most
+constexpr int kGnSmemShare = 72 * 1024;  // ... and keeps of a slab, where more can share it: three on an SM
 constexpr int kGnPart = 4096;            // blocks of a backward launch that hold column sums
 constexpr long long kGnPartSize = 1 << 22;  // ... and their columns
 
@@ -259,39 +259,56 @@ int gn_vec(int type, int D, uintptr_t at, long long strides) {
 }
 int up32(long long n) { return (int)((n + 31) / 32 * 32); }
 
-GnShape gn_shape(int type, int v, int B, int T, int C, int G, bool bwd) {
-  GnShape s{};
-  const int e = type == CTCPB_F32 ? 4 : 2, D = C / G, dv = D / v;
-  s.v = v;
-  // 128 bytes of a row, more where there are too few rows to fill a warp
-  s.gs = 128 / (D * e) > 1 ? 128 / (D * e) : 1;
-  while (s.gs < G && (long long)s.gs * dv * T < 32) s.gs *= 2;
+// Slabs of `bytes` of a row, at least a group, and as many of their rows at a time as
+// `threads` take.
+void gn_slabs(GnShape& s, int e, int T, int C, int G, int bytes, int threads) {
+  const int D = C / G, dv = D / s.v;
+  s.gs = bytes / (D * e) > 1 ? bytes / (D * e) : 1;
+  while (s.gs < G && (long long)s.gs * dv * T < 32) s.gs *= 2;  // more where there are too few rows to fill a warp
   if (s.gs > G) s.gs = G;
   s.pieces = s.gs * dv > kGnThreads ? (dv + kGnThreads - 1) / kGnThreads : 1;
   s.tw = s.pieces > 1 ? (dv + s.pieces - 1) / s.pieces : s.gs * dv;
   s.slabs = s.pieces > 1 ? G * s.pieces : (G + s.gs - 1) / s.gs;
-  s.threads = s.tw > 256 ? up32(s.tw) : up32((long long)s.tw * T < 256 ? (long long)s.tw * T : 256);
+  s.threads = s.tw > threads ? up32(s.tw) : up32((long long)s.tw * T < threads ? (long long)s.tw * T : threads);
   if (s.threads < 32) s.threads = 32;
   s.rs = s.threads / s.tw;
   s.cr = 32 % s.tw == 0 && s.rs * s.tw == s.threads ? s.threads / 32 : s.rs;
-  const size_t stat = align_up((size_t)(s.threads + 2 * s.gs) * (bwd ? sizeof(Two) : sizeof(Moments)) +
-                                   (bwd ? (size_t)s.cr * 2 * s.tw * v * 4 : 0), 16);
+}
+size_t gn_sums(const GnShape& s, bool bwd) {  // shared memory but for the slab
+  return align_up((size_t)(s.threads + 2 * s.gs) * (bwd ? sizeof(Two) : sizeof(Moments)) +
+                      (bwd ? (size_t)s.cr * 2 * s.tw * s.v * 4 : 0), 16);
+}
+
+GnShape gn_shape(int type, int v, int B, int T, int C, int G, bool bwd) {
+  GnShape s{};
+  const int e = type == CTCPB_F32 ? 4 : 2;
+  s.v = v;
+  // slabs of 64 bytes of a row, so that a block keeps more frames of one (32 x 500 x 512: 11.6 us with 128
+  // bytes, 10.8 with 64; forward and backward of 128 x 500 x 1024: 157 and 150); the forward pass has
+  // blocks of 128 threads where there are many, whose start is then divided by twice the rows (50 us, 63
+  // with 256; where there are few, 12.4 us instead of 10.8)
+  gn_slabs(s, e, T, C, G, 64, 256);
+  if (!bwd && (long long)B * s.slabs >= 152 * 8) gn_slabs(s, e, T, C, G, 64, 128);
   auto slab = [&](int ranks) {
     s.slots = ((T + ranks - 1) / ranks + s.rs - 1) / s.rs;
     return (size_t)s.slots * s.threads * v * e * (bwd ? 2 : 1);
   };
   s.parts = 1;
   while (s.parts < kGnRanks && T > 2 * s.parts * s.rs &&
-         (slab(s.parts) > (size_t)kGnSmemShare || (long long)B * s.slabs * s.parts < 304))
+         (slab(s.parts) > (size_t)kGnSmemShare || (long long)B * s.slabs * s.parts < 152))
     s.parts *= 2;
-  s.smem = stat + slab(s.parts);
+  s.smem = gn_sums(s, bwd) + slab(s.parts);
   s.split = s.pieces > 1 || s.smem > (size_t)kGnSmem;
-  if (s.split) {  // so many chunks of frames that the blocks fill the SMs, eight of a thread's rows in each at least
+  if (s.split) {
+    // rows of 256 bytes (2 x 20000 x 512 float16: 27 us with 128, 23 with 256, 24 with 512, whose groups'
+    // sums are of more parts), so many chunks of frames that the blocks just fill the SMs (29 us with
+    // two thirds of it), eight of a thread's rows in each at least
+    gn_slabs(s, e, T, C, G, 256, 256);
     const long long most = ((long long)T + 8 * s.rs - 1) / (8 * s.rs);
-    long long parts = (152 * 6 + (long long)B * s.slabs - 1) / ((long long)B * s.slabs);
+    long long parts = (152 * 3 + (long long)B * s.slabs - 1) / ((long long)B * s.slabs);
     if (parts > most) parts = most;
     s.parts = (int)(parts > 1 ? parts : 1);
-    s.smem = stat;
+    s.smem = gn_sums(s, bwd);
   }
   long long by = B;
   if (bwd) {  // column sums of so many blocks at most
@@ -318,7 +335,9 @@ cudaError_t gn_whole(bool bwd, const GnArgs& a, const GnShape& s, cudaStream_t s
   return gn_each_vec<T>(s.v, [&](auto, auto vc) {
     constexpr int V = decltype(vc)::value;
     constexpr auto f = k_gn<T, V>, g = k_gn_bwd<T, V>;
-    const cudaError_t e = bwd ? smem_optin<g>(s.smem) : smem_optin<f>(s.smem);
+    cudaError_t e = bwd ? smem_optin<g>(s.smem) : smem_optin<f>(s.smem);
+    if (e == cudaSuccess && s.parts > 8)
+      e = cudaFuncSetAttribute(bwd ? (const void*)g : (const void*)f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     return e != cudaSuccess ? e : launch(bwd ? g : f, dim3(s.slabs * s.parts, s.by), s.threads, s.smem, st, s.parts, a);
   });
 }

@@ -12,6 +12,10 @@ namespace {
 
 constexpr int kAhead = 8;  // rows that a thread has on their way
 
+// The second launches begin before the first is done: what they read besides its sums
+// was there before the first began, since that had waited for it when it let them begin
+// (pdl_wait, then pdl_next).
+
 // The group's sums over the parts of the frames, in order (a warp for each group).
 template <class S>
 __device__ __forceinline__ void over_parts(const GnArgs& a, const Place& p, int b, S* all) {
@@ -93,15 +97,22 @@ __global__ void __launch_bounds__(kGnThreads, 2) k_gn_apply(const GnArgs a) {
   Moments* const all = reinterpret_cast<Moments*>(smem);
   Place p;
   p.set<V>(a, blockIdx.x, blockIdx.y);
-  pdl_wait();
-  pdl_next();
+  u64 w[P], bias[P];
+  params_of<V>(a, p.c0 + p.cv * V, p.on, w, bias);
+  const long long step = a.rs * a.x_t, y_step = a.rs * a.y_t;
   for (int b = blockIdx.z; b < a.B; b += gridDim.z) {
     const int len = frames_of(a, b);
     const Rows rows(a, p, len);
     const T* x = (const T*)a.x + (long long)b * a.x_b + p.c0 + rows.first * a.x_t + p.cv * V;
     T* const y = (T*)a.y + (long long)b * a.y_b + p.c0;
-    u64 w[P], bias[P];
-    params_of<V>(a, p.c0 + p.cv * V, p.on, w, bias);
+    W raw[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (i < rows.n) raw[i].load(x + i * step);
+    if (b == (int)blockIdx.z) {
+      pdl_wait();
+      pdl_next();
+    }
     over_parts<Moments>(a, p, b, all);
     if (a.mean && p.part == 0 && p.piece == 0)
       for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
@@ -112,23 +123,26 @@ __global__ void __launch_bounds__(kGnThreads, 2) k_gn_apply(const GnArgs a) {
     const Moments t = all[p.group<V>(a)];
     const float rstd = t.rstd(a.eps);
     const u64 nm = pair(-t.mean, -t.mean);
+    u64 wr[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) w[i] = mul2(w[i], pair(rstd, rstd));
-    const long long step = a.rs * a.x_t, y_step = a.rs * a.y_t;
+    for (int i = 0; i < P; ++i) wr[i] = mul2(w[i], pair(rstd, rstd));
     T* to = y + rows.first * a.y_t + p.cv * V;
-    for (int k = 0; k < rows.n; k += U, x += U * step, to += U * y_step) {
-      W raw[U];
+    for (int k = 0; k < rows.n; k += U, to += U * y_step) {
+      W now[U];
+      x += U * step;
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (k + i < rows.n) raw[i].load(x + i * step);
+      for (int i = 0; i < U; ++i) {
+        now[i] = raw[i];
+        if (k + U + i < rows.n) raw[i].load(x + i * step);
+      }
 #pragma unroll
       for (int i = 0; i < U; ++i)
         if (k + i < rows.n) {
           u64 v[P];
-          raw[i].get(v);
-          activate(v, nm, w, bias, a.act);
-          raw[i].put(v);
-          raw[i].store(to + i * y_step);
+          now[i].get(v);
+          activate(v, nm, wr, bias, a.act);
+          now[i].put(v);
+          now[i].store(to + i * y_step);
         }
     }
     zero_rows<T, V>(a, p, y, len);
@@ -200,10 +214,9 @@ __global__ void __launch_bounds__(kGnThreads, 1) k_gn_bwd_apply(const GnArgs a) 
   Two* const all = reinterpret_cast<Two*>(smem);
   Place p;
   p.set<V>(a, blockIdx.x, blockIdx.y);
-  pdl_wait();
-  pdl_next();
   u64 w[P], bias[P];
   params_of<V>(a, p.c0 + p.cv * V, p.on, w, bias);
+  const long long step = a.rs * a.x_t, d_step = a.rs * a.dy_t, y_step = a.rs * a.y_t;
   for (int b = blockIdx.z; b < a.B; b += gridDim.z) {
     const int len = frames_of(a, b);
     const Rows rows(a, p, len);
@@ -211,34 +224,49 @@ __global__ void __launch_bounds__(kGnThreads, 1) k_gn_bwd_apply(const GnArgs a) 
     const T* dy = (const T*)a.dy + (long long)b * a.dy_b + p.c0 + rows.first * a.dy_t + p.cv * V;
     T* const y = (T*)a.y + (long long)b * a.y_b + p.c0;
     const long long o = (long long)b * a.G + p.g0 + p.group<V>(a);
+    W raw[U], raw_d[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (i < rows.n) {
+        raw[i].load(x + i * step);
+        raw_d[i].load(dy + i * d_step);
+      }
     const float mean = a.mean[o], rstd = a.rstd[o];
     const u64 nm = pair(-mean, -mean);
     u64 wr[P], m0, m1;
 #pragma unroll
     for (int i = 0; i < P; ++i) wr[i] = mul2(w[i], pair(rstd, rstd));
+    if (b == (int)blockIdx.z) {
+      pdl_wait();
+      pdl_next();
+    }
     over_parts<Two>(a, p, b, all);
     factors(a, all[p.group<V>(a)], len, rstd, m0, m1);
-    const long long step = a.rs * a.x_t, d_step = a.rs * a.dy_t, y_step = a.rs * a.y_t;
     T* to = y + rows.first * a.y_t + p.cv * V;
-    for (int k = 0; k < rows.n; k += U, x += U * step, dy += U * d_step, to += U * y_step) {
-      W raw[U], raw_d[U];
+    for (int k = 0; k < rows.n; k += U, to += U * y_step) {
+      W now[U], now_d[U];
+      x += U * step;
+      dy += U * d_step;
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        if (k + i < rows.n) {
+      for (int i = 0; i < U; ++i) {
+        now[i] = raw[i];
+        now_d[i] = raw_d[i];
+        if (k + U + i < rows.n) {
           raw[i].load(x + i * step);
           raw_d[i].load(dy + i * d_step);
         }
+      }
 #pragma unroll
       for (int i = 0; i < U; ++i)
         if (k + i < rows.n) {
           u64 v[P], d[P];
-          raw[i].get(v);
-          raw_d[i].get(d);
+          now[i].get(v);
+          now_d[i].get(d);
           before(v, d, nm, wr, bias, a.act);
 #pragma unroll
           for (int j = 0; j < P; ++j) d[j] = fma2(d[j], wr[j], fma2(v[j], m1, m0));
-          raw[i].put(d);
-          raw[i].store(to + i * y_step);
+          now[i].put(d);
+          now[i].store(to + i * y_step);
         }
     }
     zero_rows<T, V>(a, p, y, len);
