@@ -27,9 +27,10 @@ namespace {
 constexpr int kLossThreads = 256;  // of a block of the policy loss
 constexpr int kPairThreads = 128;  // ... of the preference loss
 constexpr int kLossBlocks = 152 * 8;
+constexpr int kWarpList = 256;     // tokens up to which a list is a warp's, not a block's
 constexpr int kOneBlocks = 8;      // of a call that is one cluster
 constexpr int kCountHere = 8192;   // lengths or pairs that every block counts itself
-constexpr long long kMaxSeqs = 1 << 24, kMaxTokens = 1 << 24, kMaxCall = 1ll << 32;
+constexpr long long kMaxSeqs = 1 << 24, kMaxTokens = 1 << 24, kMaxCall = (1ll << 32) - 1;
 
 // What a call's lengths or pairs come to.
 struct Ctl {
@@ -640,9 +641,12 @@ __global__ void __launch_bounds__(kPairThreads) k_preference(const PairArgs a) {
 
 bool on16(const void* p, long long ld) { return ((uintptr_t)p & 15u) == 0 && ld % 4 == 0; }
 
-// Small calls are one cluster: so few tokens that its blocks are not much longer at
-// them than a second launch is.
-bool one_cluster(long long counted, long long tokens) { return counted <= kCountHere && tokens <= 65536; }
+// Small calls are one cluster, where its blocks are not much longer at them than a
+// second launch is (3 us of the host's): 320 x 40 tokens 8.4 us on the GPU, in two
+// launches 7.6; 320 x 200 are 13.9 and 8.1.  Lists: 32 x 10 x 40 7.5 and 8.2, 64 x 10 x
+// 40 11.2 and 7.8; of more tokens, a block each: 8 x 4 x 1000 6.9 and 7.5, 16: 9.9 and 7.2.
+bool one_policy(long long S, long long L) { return S <= kCountHere && S * L <= 16384; }
+bool one_preference(long long B, int N, long long L) { return B <= (L > kWarpList ? 8 : 32) && B * N * L <= 65536; }
 
 // The launches of a call around its main one, `run(blocks, cluster)`.
 template <int N, class F>
@@ -686,7 +690,7 @@ extern "C" {
 int ctcpb_policy_loss_workspace_size(int64_t S, int64_t L, size_t* bytes) {
   if (int rc = check_policy(S, L)) return rc;
   if (!bytes) return CTCPB_ENULL;
-  *bytes = one_cluster(S, S * L) ? sizeof(Header) : loss_layout().total;
+  *bytes = one_policy(S, L) ? sizeof(Header) : loss_layout().total;
   return CTCPB_OK;
 }
 
@@ -698,7 +702,7 @@ int ctcpb_policy_loss(const float* nll, int64_t ld_nll, const float* old_nll, in
   if (int rc = check_policy(S, L)) return rc;
   if (reduction < CTCPB_REDUCE_NONE || reduction > CTCPB_REDUCE_SEQUENCE_MEAN) return CTCPB_EINVAL;
   if (!(clip_low >= 0.) || std::isinf(clip_low) || !(clip_high >= 0.) || !std::isfinite(kl_weight)) return CTCPB_EINVAL;
-  const bool any = S > 0 && L > 0, one = one_cluster(S, S * L);
+  const bool any = S > 0 && L > 0, one = one_policy(S, L);
   if (any && (ld_nll < L || ld_old < L || (ref_nll && ld_ref < L) || (ld_advantages != 0 && ld_advantages < L)))
     return CTCPB_EINVAL;
   if (any && (!nll || !old_nll || !advantages)) return CTCPB_ENULL;
@@ -750,7 +754,7 @@ int ctcpb_policy_loss(const float* nll, int64_t ld_nll, const float* old_nll, in
 int ctcpb_preference_loss_workspace_size(int64_t B, int N, int64_t L, size_t* bytes) {
   if (int rc = check_lists(B, N, L)) return rc;
   if (!bytes) return CTCPB_ENULL;
-  *bytes = one_cluster(B, B * N * L) ? sizeof(Header) : loss_layout().total;
+  *bytes = one_preference(B, N, L) ? sizeof(Header) : loss_layout().total;
   return CTCPB_OK;
 }
 
@@ -763,7 +767,7 @@ int ctcpb_preference_loss(const float* nll, int64_t ld_nll, const float* ref_nll
   if (reduction < CTCPB_REDUCE_NONE || reduction > CTCPB_REDUCE_SUM || (average != 0 && average != 1)) return CTCPB_EINVAL;
   if (!std::isfinite(beta) || !std::isfinite(margin) || !(label_smoothing >= 0.f && label_smoothing <= 1.f))
     return CTCPB_EINVAL;
-  const bool one = one_cluster(B, B * N * L);
+  const bool one = one_preference(B, N, L);
   if (B > 0 && L > 0 && (ld_nll < L || (ref_nll && ld_ref < L))) return CTCPB_EINVAL;
   if (B > 0 && (!chosen || !rejected || (L > 0 && !nll))) return CTCPB_ENULL;
   if (B > 0 && L > 0 && dnll && !grad) return CTCPB_ENULL;
@@ -793,7 +797,7 @@ int ctcpb_preference_loss(const float* nll, int64_t ld_nll, const float* ref_nll
   a.ends.counted = Counted{nullptr, chosen, rejected, B, 0, N, reduction, grad};
   a.ends.loss = none ? nullptr : loss;
   const bool vec = L % 4 == 0 && on16(nll, ld_nll) && on16(ref_nll, ref_nll ? ld_ref : 0) && on16(dnll, 0);
-  const bool wide = L > 256;
+  const bool wide = L > kWarpList;
   const long long per = wide ? 1 : kPairThreads / 32, blocks = (B + per - 1) / per;
   return loss_call<1>(a.ends, one, blocks < 1 ? 1 : blocks < kLossBlocks ? (int)blocks : kLossBlocks, ws, s,
                       [&](int n, int cluster) {

@@ -648,7 +648,7 @@ int ctcpb_dropout(int type, const void* x, int64_t ldx, const void* residual, in
  *   ws            ctcpb_policy_loss_workspace_size() bytes; may be NULL where that is
  *                 256 (small calls, which have only the status in it).
  * Sums over tokens are pairs of float32 (value and error), made in a fixed order.
- * Limits: S, L <= 2^24, S * L <= 2^32.
+ * Limits: S, L <= 2^24, S * L < 2^32.
  */
 #define CTCPB_REDUCE_SEQUENCE_MEAN 3
 int ctcpb_policy_loss_workspace_size(int64_t S, int64_t L, size_t* bytes);

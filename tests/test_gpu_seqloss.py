@@ -228,6 +228,25 @@ def test_preference_pairs_and_status():
     assert abs(loss.item() - 0.6931472) < 1e-6 and (margins == 0).all()
 
 
+def test_without_a_workspace():
+    """Small calls may go without one, by the C call too; with one they leave their status in it."""
+    nll, old, ref, adv, n, _ = lists((5, 4), 30)
+    c, r = torch.tensor([0, 1, 9, 2, 3], dtype=torch.int32, device="cuda"), torch.zeros(5, dtype=torch.int32, device="cuda")
+    one, s = torch.ones((), device="cuda"), torch.cuda.current_stream().cuda_stream
+    want = head.preference_loss(nll, c, r, lengths=n, ref_nll=ref)
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    for w in (None, ws):
+        loss, margins = torch.empty((), device="cuda"), torch.empty(5, device="cuda")
+        assert head._lib()["ctcpb_preference_loss"](
+            nll.data_ptr(), 30, ref.data_ptr(), 30, c.data_ptr(), r.data_ptr(), n.data_ptr(), 5, 4, 30, 0.1, 0.0, 0.0, 0, 1,
+            one.data_ptr(), loss.data_ptr(), margins.data_ptr(), None, None if w is None else w.data_ptr(),
+            0 if w is None else 256, s) == D.OK
+        assert torch.equal(loss, want[0]) and torch.equal(margins, want[1])
+    assert D.read_status(ws) == head.DEV_TARGET
+    head.policy_loss(nll, old, adv, lengths=n, workspace=ws)
+    assert D.read_status(ws) == 0
+
+
 def test_preference_lengths():
     nll, _, ref, _, _, _ = lists((5, 3), 40)
     n = torch.tensor([[0, 1, 40], [40, 0, 0], [0, 0, 5], [-3, 99, 7], [20, 20, 20]], dtype=torch.int32, device="cuda")

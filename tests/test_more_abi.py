@@ -47,7 +47,8 @@ def test_size_queries(lib):
     # small calls have only the status in it, and may go without
     assert head.policy_loss_workspace_size(320, 40) == head.preference_loss_workspace_size(32, 10, 40) == 256
     for n in (head.policy_loss_workspace_size(4096, 1024), head.preference_loss_workspace_size(1024, 4, 1000),
-              head.policy_loss_workspace_size(1 << 24, 256), head.policy_loss_workspace_size(10000, 1)):
+              head.policy_loss_workspace_size(1 << 24, 255), head.policy_loss_workspace_size(10000, 1),
+              head.preference_loss_workspace_size(100, 2, 4)):
         assert n % 256 == 0 and 256 < n < 1 << 20
     n = ctypes.c_size_t()
     g, p, q = (lib["ctcpb_%s_workspace_size" % x] for x in ("group_norm", "policy_loss", "preference_loss"))
@@ -56,7 +57,7 @@ def test_size_queries(lib):
         assert g(BF16, *bad, 1, ctypes.byref(n)) == D.EINVAL, bad
     assert g(7, 4, 4, 64, 4, 1, ctypes.byref(n)) == D.EINVAL and g(BF16, 4, 4, 64, 4, 2, ctypes.byref(n)) == D.EINVAL
     assert g(BF16, 4, 4, 64, 4, 1, None) == D.ENULL
-    for bad in ((-1, 4), (4, -1), ((1 << 24) + 1, 4), (4, (1 << 24) + 1), (1 << 16, (1 << 16) + 1)):
+    for bad in ((-1, 4), (4, -1), ((1 << 24) + 1, 4), (4, (1 << 24) + 1), (1 << 16, 1 << 16)):
         assert p(*bad, ctypes.byref(n)) == D.EINVAL, bad
     for bad in ((-1, 4, 4), (4, 0, 4), (4, 4, -1), (1 << 22, 8, 4), (1, 4, (1 << 24) + 1)):
         assert q(*bad, ctypes.byref(n)) == D.EINVAL, bad
