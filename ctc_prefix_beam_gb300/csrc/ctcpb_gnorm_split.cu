@@ -2,7 +2,8 @@
 // frames of some whole groups, or too few blocks would work: the utterances' frames
 // are dealt to as many blocks as fill the GPU, first for the groups' sums of each
 // block's frames, then, every block adding up its groups' over all of them, for the
-// outputs.  x (and dy) are read twice, the second time from L2 where they fit.
+// outputs.  x (and dy) are read twice, the second time from L2 where they fit: 2 x 20000
+// x 512 float16 23 us (3.6 TB/s of x read and y written once; 12 us would be HBM's).
 #include <type_traits>
 
 #include "ctcpb_gnorm.cuh"

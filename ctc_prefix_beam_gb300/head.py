@@ -400,8 +400,8 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
         _given(mean, (B, G), torch.float32, dev, "mean")
         _given(rstd, (B, G), torch.float32, dev, "rstd")
     ws, nbytes = _workspace(workspace, group_norm_workspace_size(dt, B, T, C, G, False), dev)
-    _run(dev, "ctcpb_group_norm", _TYPES[dt], _TYPES[pt], _p(xr), sb, st, _p(w), _p(b), _p(n), eps, act, B, T, C, G, _p(y),
-         T * C, C, _p(mean), _p(rstd), _p(ws), nbytes)
+    _run(dev, "ctcpb_group_norm", _TYPES[dt], _TYPES[pt], xr.data_ptr(), sb, st, _p(w), _p(b), _p(n), eps, act, B, T, C, G,
+         y.data_ptr(), T * C, C, mean.data_ptr(), rstd.data_ptr(), _p(ws), nbytes)
     return y, mean, rstd
 
 
@@ -435,8 +435,9 @@ def group_norm_backward(dy: torch.Tensor, x: torch.Tensor, groups: int, weight: 
     dw = torch.empty((C,), dtype=pt, device=dev)
     db = torch.empty_like(dw)
     ws, nbytes = _workspace(workspace, group_norm_workspace_size(dt, B, T, C, G, True), dev)
-    _run(dev, "ctcpb_group_norm_backward", _TYPES[dt], _TYPES[pt], _p(dyr), db_, dt_, _p(xr), sb, st, _p(w), _p(b), _p(n),
-         _p(mean), _p(rstd), act, B, T, C, G, _p(dx), T * C, C, _p(dw), _p(db), _p(ws), nbytes)
+    _run(dev, "ctcpb_group_norm_backward", _TYPES[dt], _TYPES[pt], dyr.data_ptr(), db_, dt_, xr.data_ptr(), sb, st, _p(w), _p(b),
+         _p(n), mean.data_ptr(), rstd.data_ptr(), act, B, T, C, G, dx.data_ptr(), T * C, C, dw.data_ptr(), db.data_ptr(), _p(ws),
+         nbytes)
     return dx, dw, db
 
 
@@ -461,7 +462,7 @@ def dropout(x: torch.Tensor, p: float, rng: torch.Tensor, *, residual: Optional[
         if residual.shape != x.shape or r.device != dev:
             raise ValueError("residual must have x's shape and device")
     y = _like(x) if out is None else _given(out, x.shape, dt, dev, "out")
-    _run(dev, "ctcpb_dropout", _TYPES[dt], _p(xr), ldx, _p(r), ldr, p, _p(rng), N, H, _p(y), H)
+    _run(dev, "ctcpb_dropout", _TYPES[dt], xr.data_ptr(), ldx, _p(r), ldr, p, rng.data_ptr(), N, H, y.data_ptr(), H)
     return y
 
 
@@ -533,8 +534,8 @@ def policy_loss(nll: torch.Tensor, old_nll: torch.Tensor, advantages: torch.Tens
     stats = torch.empty(2, dtype=torch.float32, device=dev)
     dnll = None if g is None else _like(nll)
     ws, nbytes = _status_or(workspace, policy_loss_workspace_size(S, L), dev)
-    _run(dev, "ctcpb_policy_loss", _p(a), lda, _p(o), ldo, _p(r), ldr, _p(v), ldv, _p(n), S, L, clip_low, clip_high,
-         kl_weight, red, _p(g), _p(loss), _p(stats), _p(dnll), _p(ws), nbytes)
+    _run(dev, "ctcpb_policy_loss", a.data_ptr(), lda, o.data_ptr(), ldo, _p(r), ldr, v.data_ptr(), ldv, _p(n), S, L, clip_low,
+         clip_high, kl_weight, red, _p(g), loss.data_ptr(), stats.data_ptr(), _p(dnll), _p(ws), nbytes)
     return (loss, stats) if g is None else (loss, stats, dnll)
 
 
@@ -570,6 +571,6 @@ def preference_loss(nll: torch.Tensor, chosen: torch.Tensor, rejected: torch.Ten
     margins = torch.empty((B,), dtype=torch.float32, device=dev)
     dnll = None if g is None else _like(nll)
     ws, nbytes = _status_or(workspace, preference_loss_workspace_size(B, N, L), dev)
-    _run(dev, "ctcpb_preference_loss", _p(a), lda, _p(r), ldr, _p(c), _p(j), _p(n), B, N, L, beta, margin, label_smoothing,
-         int(bool(average)), red, _p(g), _p(loss), _p(margins), _p(dnll), _p(ws), nbytes)
+    _run(dev, "ctcpb_preference_loss", a.data_ptr(), lda, _p(r), ldr, c.data_ptr(), j.data_ptr(), _p(n), B, N, L, beta, margin,
+         label_smoothing, int(bool(average)), red, _p(g), loss.data_ptr(), margins.data_ptr(), _p(dnll), _p(ws), nbytes)
     return (loss, margins) if g is None else (loss, margins, dnll)
