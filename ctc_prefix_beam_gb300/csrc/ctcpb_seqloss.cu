@@ -13,7 +13,7 @@
 // shared memory; larger ones leave them to a launch after, which starts meanwhile.
 //
 // 4096 sequences of up to 1024 tokens (3.1 M), with a reference and an advantage each:
-// 23 us, bound by instructions (130 a token, two exponentials and the sums' errors; HBM
+// 23 us, bound by instructions (170 a token, two exponentials and the sums' errors; HBM
 // would take 10); 1024 lists of 4 x 1000 tokens 10 us (HBM 4.4; a block's chain: the
 // pair, its lengths, its rows, the gradient).
 //
