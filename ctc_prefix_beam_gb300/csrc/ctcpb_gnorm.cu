@@ -386,14 +386,15 @@ size_t gn_need(int type, int B, int T, int C, int G, bool bwd) {
     }
   return most;
 }
-int gn_workspace(GnArgs& a, int type, const GnShape& s, int B, int T, int C, int G, bool bwd, void* ws, size_t ws_bytes) {
-  const size_t need = gn_need(type, B, T, C, G, bwd);
-  if (need == 0) return CTCPB_OK;
+// What this call needs, at most gn_need.
+int gn_workspace(GnArgs& a, const GnShape& s, bool bwd, void* ws, size_t ws_bytes) {
+  const GnLayout l = gn_layout(s, a.B, a.C, a.G, bwd);
+  if (l.total == 0) return CTCPB_OK;
   if (!ws) return CTCPB_ENULL;
   if (((uintptr_t)ws & 255u) != 0) return CTCPB_EALIGN;
-  if (ws_bytes < need) return CTCPB_ESIZE;
+  if (ws_bytes < l.total) return CTCPB_ESIZE;
   a.cols = bwd ? (float*)ws : nullptr;
-  a.group = (float*)((char*)ws + gn_layout(s, B, C, G, bwd).o_group);
+  a.group = (float*)((char*)ws + l.o_group);
   return CTCPB_OK;
 }
 
@@ -437,7 +438,7 @@ int ctcpb_group_norm(int type, int param_type, const void* x, int64_t x_stride_b
   a.rstd = rstd;
   const int v = gn_vec(type, a.D, (uintptr_t)x | (uintptr_t)y, x_stride_b | x_stride_t | y_stride_b | y_stride_t);
   const GnShape s = gn_shape(type, v, B, T, C, G, false);
-  if ((rc = gn_workspace(a, type, s, B, T, C, G, false, ws, ws_bytes))) return rc;
+  if ((rc = gn_workspace(a, s, false, ws, ws_bytes))) return rc;
   return gn_run(type, false, a, s, (cudaStream_t)stream) == cudaSuccess ? CTCPB_OK : CTCPB_ECUDA;
 }
 
@@ -493,7 +494,7 @@ int ctcpb_group_norm_backward(int type, int param_type, const void* dy, int64_t 
     const int v = gn_vec(type, a.D, (uintptr_t)x | (uintptr_t)dy | (uintptr_t)dx,
                          x_stride_b | x_stride_t | dy_stride_b | dy_stride_t | a.y_b | a.y_t);
     const GnShape s = gn_shape(type, v, B, T, C, G, true);
-    if ((rc = gn_workspace(a, type, s, B, T, C, G, true, ws, ws_bytes))) return rc;
+    if ((rc = gn_workspace(a, s, true, ws, ws_bytes))) return rc;
     if (!cols) a.cols = nullptr;
     rows = s.by * s.parts;
     if (gn_run(type, true, a, s, st) != cudaSuccess) return CTCPB_ECUDA;
