@@ -328,20 +328,14 @@ __device__ __forceinline__ u64 silu2(u64 h) {
   unpair(x, y, add2(pair(ex2(x), ex2(y)), pair(1.f, 1.f)));
   return mul2(h, pair(rcp(x), rcp(y)));
 }
-// Its slope s (1 + h (1 - s)), s = 1 / (1 + e^-h).  The two of a pair share one
-// reciprocal, that of their product: the exponentials and reciprocals of both
-// passes would take as long as the memory.  e^-h is held to 2^63, so that the
-// product is finite: where h < -43.6 the slope is off by less than 1e-17.
+// Its slope s (1 + h (1 - s)), s = 1 / (1 + e^-h)
 __device__ __forceinline__ u64 silu_slope2(u64 h) {
   float x, y;
   unpair(x, y, mul2(h, pair(-kLog2e, -kLog2e)));
-  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(63.f));
-  asm("min.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(63.f));
-  const u64 one = pair(1.f, 1.f), other = add2(pair(ex2(y), ex2(x)), one);  // each lane the other's
-  unpair(y, x, other);
-  const float r = rcp(x * y);
-  const u64 s = mul2(pair(r, r), other), rest = fma2(s, pair(-1.f, -1.f), one);
-  return mul2(s, fma2(h, rest, one));
+  const u64 one = pair(1.f, 1.f);
+  unpair(x, y, add2(pair(ex2(x), ex2(y)), one));
+  const u64 s = pair(rcp(x), rcp(y));
+  return mul2(s, fma2(h, fma2(s, pair(-1.f, -1.f), one), one));
 }
 __device__ __forceinline__ float relu(float x) { return x > 0.f ? x : x != x ? x : 0.f; }
 
