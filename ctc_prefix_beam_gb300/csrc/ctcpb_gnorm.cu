@@ -354,7 +354,6 @@ cudaError_t gn_run(int type, bool bwd, GnArgs& a, const GnShape& s, cudaStream_t
   a.slots = s.slots;
   a.parts = s.parts;
   a.cr = s.cr;
-  a.by = s.by;
   a.by_tw = reciprocal(s.tw);
   a.by_rs = reciprocal(s.rs);
   a.by_dv = reciprocal(a.D / s.v);

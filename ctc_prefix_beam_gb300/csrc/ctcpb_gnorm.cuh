@@ -30,7 +30,6 @@ struct GnArgs {
   int slots;   // rows of a thread that shared memory holds
   int parts;   // blocks that share an utterance's frames (ranks of a cluster, or chunks)
   int cr;      // partial column sums of a block
-  int by;
   int pvec;    // the parameters' vectors of V start at multiples of their size
   u32 by_tw, by_rs, by_dv;  // divisors' reciprocals (quot)
 };

@@ -35,6 +35,7 @@ constexpr int kLossBlocks = 152 * 8;
 constexpr int kWarpList = 256;     // tokens up to which a list is a warp's, not a block's
 constexpr int kOneBlocks = 8;      // of a call that is one cluster
 constexpr int kCountHere = 8192;   // lengths or pairs that every block counts itself
+constexpr int kCountBlocks = 128;  // blocks of the launch that counts more
 constexpr long long kMaxSeqs = 1 << 24, kMaxTokens = 1 << 24, kMaxCall = (1ll << 32) - 1;
 
 // What a call's lengths or pairs come to.
@@ -45,12 +46,13 @@ struct Ctl {
   u32 bad;          // an index past the end
 };
 struct LossLayout {
-  size_t o_ctl, o_part, total;
+  size_t o_ctl, o_counts, o_part, total;
 };
 LossLayout loss_layout() {
   LossLayout l{};
   l.o_ctl = sizeof(Header);
-  l.o_part = l.o_ctl + 256;
+  l.o_counts = l.o_ctl + 256;
+  l.o_part = l.o_counts + kCountBlocks * sizeof(longlong2);
   l.total = align_up(l.o_part + (size_t)kLossBlocks * 3 * sizeof(float2), 256);
   return l;
 }
@@ -175,13 +177,17 @@ struct Counted {
   long long n, L;  // lengths, or lists
   int N, reduction;
   const float* grad;
+  const longlong2* counts;  // ... or what the blocks of a launch before counted of them
 };
-// A block's count of all of them; thread 0 has it.
-__device__ __forceinline__ Ctl count(const Counted& a, long long (*red)[2]) {
+// A block's count, of every `step`-th from `first` on for its first thread; thread 0 has it.
+__device__ __forceinline__ longlong2 count(const Counted& a, long long first, long long step, long long (*red)[2]) {
   long long v[2] = {0, 0};
 #pragma unroll 8
-  for (long long i = threadIdx.x; i < a.n; i += blockDim.x) {
-    if (a.chosen) {
+  for (long long i = first + threadIdx.x; i < (a.counts ? kCountBlocks : a.n); i += step) {
+    if (a.counts) {
+      v[0] += a.counts[i].x;
+      v[1] += a.counts[i].y;
+    } else if (a.chosen) {
       int c, r;
       v[0] += pair_of(a.chosen, a.rejected, i, a.N, c, r);
       v[1] += c >= a.N || r >= a.N;
@@ -200,28 +206,30 @@ __device__ __forceinline__ Ctl count(const Counted& a, long long (*red)[2]) {
     red[threadIdx.x >> 5][1] = v[1];
   }
   __syncthreads();
-  Ctl c{};
-  if (threadIdx.x == 0) {
-    v[0] = v[1] = 0;
+  v[0] = v[1] = 0;
+  if (threadIdx.x == 0)
     for (u32 w = 0; w < blockDim.x >> 5; ++w) {
       v[0] += red[w][0];
       v[1] += red[w][1];
     }
-    const bool mean = a.reduction == CTCPB_REDUCE_MEAN || a.reduction == CTCPB_REDUCE_SEQUENCE_MEAN;
-    const double of = (double)(a.reduction == CTCPB_REDUCE_SEQUENCE_MEAN ? v[1] : v[0]);
-    c.items = v[0];
-    c.factor = mean ? 1. / of : 1.;
-    c.grad = a.reduction == CTCPB_REDUCE_NONE || !a.grad ? 1.f : mean ? (float)((double)*a.grad / of) : *a.grad;
-    c.bad = a.chosen && v[1] ? 1u : 0u;
-  }
+  return make_longlong2(v[0], v[1]);
+}
+__device__ __forceinline__ Ctl ctl_of(const Counted& a, const longlong2& v) {
+  const bool mean = a.reduction == CTCPB_REDUCE_MEAN || a.reduction == CTCPB_REDUCE_SEQUENCE_MEAN;
+  const double of = (double)(a.reduction == CTCPB_REDUCE_SEQUENCE_MEAN ? v.y : v.x);
+  Ctl c;
+  c.items = v.x;
+  c.factor = mean ? 1. / of : 1.;
+  c.grad = a.reduction == CTCPB_REDUCE_NONE || !a.grad ? 1.f : mean ? (float)((double)*a.grad / of) : *a.grad;
+  c.bad = a.chosen && v.y ? 1u : 0u;
   return c;
 }
-__global__ void __launch_bounds__(1024) k_count(const Counted a, Ctl* ctl) {
+__global__ void __launch_bounds__(1024) k_count(const Counted a, longlong2* counts) {
   __shared__ long long red[32][2];
   pdl_wait();
   pdl_next();
-  const Ctl c = count(a, red);
-  if (threadIdx.x == 0) *ctl = c;
+  const longlong2 v = count(a, (long long)blockIdx.x * blockDim.x, (long long)gridDim.x * blockDim.x, red);
+  if (threadIdx.x == 0) counts[blockIdx.x] = v;
 }
 
 // ---------------------------------------------------------------- the end of a call
@@ -229,7 +237,6 @@ __global__ void __launch_bounds__(1024) k_count(const Counted a, Ctl* ctl) {
 // How a launch's blocks come by the counts and leave their sums.
 struct Ends {
   Counted counted;
-  int here;       // every block counts (else ctl was written by a launch before)
   int one;        // the launch is one cluster (else sums go to part, for k_loss_end)
   Ctl* ctl;
   float2* part;   // [blocks][3]
@@ -243,14 +250,10 @@ struct Shared {
   Ctl ctl;
 };
 __device__ __forceinline__ void begin(const Ends& a, Shared& sh) {
-  if (a.here) {
-    const Ctl c = count(a.counted, sh.count);
-    if (threadIdx.x == 0) {
-      sh.ctl = c;
-      if (blockIdx.x == 0 && !a.one) *a.ctl = c;  // for the launch after
-    }
-  } else if (threadIdx.x == 0) {
-    sh.ctl = *a.ctl;
+  const longlong2 v = count(a.counted, 0, blockDim.x, sh.count);
+  if (threadIdx.x == 0) {
+    sh.ctl = ctl_of(a.counted, v);
+    if (blockIdx.x == 0 && !a.one) *a.ctl = sh.ctl;  // for the launch after
   }
   if (threadIdx.x == 0 && blockIdx.x == 0 && a.status) *a.status = sh.ctl.bad ? CTCPB_DEV_TARGET : 0u;
   __syncthreads();
@@ -539,8 +542,9 @@ __device__ __forceinline__ void write_row(float* row, long long L, long long len
 // A list is worked on by GT threads (a warp, or the block): both rows' sums, the
 // pair's loss, then the two rows' gradients; the other rows' zeros while the sums'
 // values are on their way.
+// (Eight blocks an SM: 1024 lists are one wave, 12.7 us; with 80 registers a thread 16.6.)
 template <bool VEC, int GT>
-__global__ void __launch_bounds__(kPairThreads) k_preference(const PairArgs a) {
+__global__ void __launch_bounds__(kPairThreads, 8) k_preference(const PairArgs a) {
   __shared__ Shared sh;
   __shared__ float2 rowsum[2][GT / 32];
   __shared__ float slopes[kPairThreads / GT];
@@ -657,7 +661,6 @@ bool one_preference(long long B, int N, long long L) { return B <= (L > kWarpLis
 template <int N, class F>
 int loss_call(Ends& e, bool one, int blocks, void* ws, cudaStream_t s, F run) {
   const LossLayout l = loss_layout();
-  e.here = e.counted.n <= kCountHere;
   e.one = one;
   e.ctl = (Ctl*)((char*)ws + l.o_ctl);
   e.part = (float2*)((char*)ws + l.o_part);
@@ -667,7 +670,11 @@ int loss_call(Ends& e, bool one, int blocks, void* ws, cudaStream_t s, F run) {
     while (blocks & (blocks - 1)) ++blocks;  // clusters of a power of two
     return run(blocks, blocks) == cudaSuccess ? CTCPB_OK : CTCPB_ECUDA;
   }
-  if (!e.here && launch(k_count, 1, 1024, 0, s, 1, e.counted, e.ctl) != cudaSuccess) return CTCPB_ECUDA;
+  if (e.counted.n > kCountHere) {
+    longlong2* const counts = (longlong2*)((char*)ws + l.o_counts);
+    if (launch(k_count, kCountBlocks, 1024, 0, s, 1, e.counted, counts) != cudaSuccess) return CTCPB_ECUDA;
+    e.counted.counts = counts;
+  }
   if (run(blocks, 1) != cudaSuccess) return CTCPB_ECUDA;
   if ((e.loss || e.stats) && launch(k_loss_end<N>, 1, 256, 0, s, 1, e, blocks) != cudaSuccess) return CTCPB_ECUDA;
   return CTCPB_OK;
@@ -745,7 +752,7 @@ int ctcpb_policy_loss(const float* nll, int64_t ld_nll, const float* old_nll, in
   a.pieces = Divisor(any ? (u32)pieces : 1u);
   a.work = any ? (u32)(S * pieces) : 0u;
   a.dense = ld_nll == L && ld_old == L && (!ref_nll || ld_ref == L) && (ld_advantages == 0 || ld_advantages == L);
-  a.ends.counted = Counted{lengths, nullptr, nullptr, a.S, L, 0, reduction, grad};
+  a.ends.counted = Counted{lengths, nullptr, nullptr, a.S, L, 0, reduction, grad, nullptr};
   a.ends.loss = none ? nullptr : loss;
   a.ends.stats = stats;
   const long long blocks = ((long long)a.work + kLossThreads - 1) / kLossThreads;
@@ -799,7 +806,7 @@ int ctcpb_preference_loss(const float* nll, int64_t ld_nll, const float* ref_nll
   a.loss = none ? loss : nullptr;
   a.margins = margins;
   a.dnll = L > 0 ? dnll : nullptr;
-  a.ends.counted = Counted{nullptr, chosen, rejected, B, 0, N, reduction, grad};
+  a.ends.counted = Counted{nullptr, chosen, rejected, B, 0, N, reduction, grad, nullptr};
   a.ends.loss = none ? nullptr : loss;
   const bool vec = L % 4 == 0 && on16(nll, ld_nll) && on16(ref_nll, ref_nll ? ld_ref : 0) && on16(dnll, 0);
   const bool wide = L > kWarpList;
