@@ -35,6 +35,7 @@ constexpr long long kGnPartSize = 1 << 22;  // ... and their columns
 template <class S>
 __device__ __forceinline__ void over_cluster(const GnArgs& a, const Place& p, S* own, S* all) {
   if (a.parts > 1) {
+    __syncwarp();  // the barrier takes whole warps
     cluster_sync();
     constexpr int n = sizeof(S) / 4;
     for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {

@@ -298,6 +298,7 @@ __device__ __forceinline__ void end(const Ends& a, Sum2 (&v)[N], Shared& sh) {
       for (int i = 0; i < N; ++i) a.part[(size_t)blockIdx.x * 3 + i] = sh.block[i];
     return;
   }
+  __syncwarp();  // the barrier takes whole warps
   cluster_sync();
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     Sum2 s[3];
@@ -311,6 +312,7 @@ __device__ __forceinline__ void end(const Ends& a, Sum2 (&v)[N], Shared& sh) {
       }
     results(a, sh.ctl, s);
   }
+  __syncwarp();
   cluster_sync();  // no block leaves before its sums are read
 }
 // The blocks' sums, in order.
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(kLossThreads, 3) k_policy(const PolicyArgs a) 
   begin(a.ends, sh);
   const float g = sh.ctl.grad;
   Sum2 sums[3];
-  float kl = 0.f, held = 0.f;  // (terms of one sign, some tens a thread)
+  float held = 0.f;  // (whole numbers below 2^24)
   for (; x < a.work; x += step) {
     Tokens<V> k = ahead;
     const At now = at;
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(kLossThreads, 3) k_policy(const PolicyArgs a) 
       // 1 / len, and what its rounding took off (len <= 2^24 is exact)
       const float len = (float)now.len, wt = by_len ? 1.f / len : 1.f;
       const float gw = g * wt;
-      float more = 0.f;
+      float more = 0.f, kl = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float rest = token(a, k.nll[i], k.old[i], k.ref[i], k.adv[i], kl, held, slope[i]);
@@ -484,6 +486,7 @@ __global__ void __launch_bounds__(kLossThreads, 3) k_policy(const PolicyArgs a) 
       }
       Sum2 loss;
       loss.hi = more;
+      sums[1].add(kl);
       if constexpr (V == 4) {
         Sum2x2 advs;
         advs.hi = pair(-k.adv[0], -k.adv[1]);
@@ -506,7 +509,6 @@ __global__ void __launch_bounds__(kLossThreads, 3) k_policy(const PolicyArgs a) 
       if (a.loss) a.loss[o] = each[0];
     }
   }
-  sums[1].add(kl);
   sums[2].add(held);
   end<3>(a.ends, sums, sh);
 }

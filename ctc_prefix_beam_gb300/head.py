@@ -399,6 +399,8 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
         _given(y, x.shape, dt, dev, "y")
         _given(mean, (B, G), torch.float32, dev, "mean")
         _given(rstd, (B, G), torch.float32, dev, "rstd")
+        if y.data_ptr() == xr.data_ptr() and y.numel():
+            raise ValueError("y must not be x")
     ws, nbytes = _workspace(workspace, group_norm_workspace_size(dt, B, T, C, G, False), dev)
     _run(dev, "ctcpb_group_norm", _TYPES[dt], _TYPES[pt], xr.data_ptr(), sb, st, _p(w), _p(b), _p(n), eps, act, B, T, C, G,
          y.data_ptr(), T * C, C, mean.data_ptr(), rstd.data_ptr(), _p(ws), nbytes)

@@ -217,7 +217,7 @@ def test_refusals():
                 lambda: head.group_norm(x, 8, w, b.float()), lambda: head.group_norm(x, 8, w[:3]),
                 lambda: head.group_norm(x, 8, activation="gelu"), lambda: head.group_norm(x, 8, lengths=n.long()),
                 lambda: head.group_norm(x, 8, lengths=n[:1]), lambda: head.group_norm(x, 8, lengths=n.cpu()),
-                lambda: head.group_norm(x, 8, outputs=(y[:1], mean, rstd)),
+                lambda: head.group_norm(x, 8, outputs=(y[:1], mean, rstd)), lambda: head.group_norm(x, 8, outputs=(x, mean, rstd)),
                 lambda: head.group_norm_backward(dy.float(), x, 8, w, b, mean, rstd),
                 lambda: head.group_norm_backward(dy[:1], x, 8, w, b, mean, rstd),
                 lambda: head.group_norm_backward(dy, x, 8, w, b, mean[:1], rstd),
