@@ -17,7 +17,7 @@
 // 128 utterances of up to 500 frames (375 on average) of 1024 channels, bfloat16, SiLU:
 // forward 49 us (4.7 TB/s of x read and y written, padding and all), backward 96 (3.4),
 // its column sums 5.  What bounds it is the work between a block's loads and its stores:
-// with three to six blocks an SM the issue slots are 55 to 62% busy, HBM some 45%.
+// with three to six blocks an SM the issue slots are 52 to 62% busy, HBM some 45%.
 #include <type_traits>
 
 #include "ctcpb_gnorm.cuh"
